@@ -267,6 +267,76 @@ int sl_linear_fwd_nvfp4w(void* stream, const void* X, const void* Wm, float w_sc
 int sl_linear_dgrad_nvfp4w(void* stream, const void* dY, const void* Wm, float w_scale, void* dX,
                            int64_t T, int64_t in, int64_t out);
 
+/* ---- MXFP4 -----------------------------------------------------------------------------------
+ * Microscaled 4-bit floats (OCP MX v1.0): E2M1 elements (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
+ * negatives) with one E8M0 scale per 32 elements along the axis that the product contracts.  A
+ * quantised matrix M[r, k] (k a multiple of 32) is passed as packed codes Mq[r, k/2] (uint8, element
+ * 2j of a row in the low nibble of byte j) and scales Ms[r, k/32] (uint8), and stands for
+ *   deq(q, s) = E2M1(q) * 2^(s - 127),  NaN where s = 255.
+ * All code pointers must be 16-byte aligned; scale pointers have no alignment requirement (rows of
+ * scales are read in whole aligned 4-byte words, so up to 3 bytes beside the array, in the same
+ * word as one of its bytes, are read and not used).
+ *
+ * sl_mxfp4_quantize: x[rows, cols] bf16 (cols % 8 == 0, 16-byte aligned) into rowwise codes
+ * q_rows[rows, Cp/2] + scales s_rows[rows, Cp/32] and/or columnwise ones, stored transposed,
+ * q_cols[cols, Rp/2] + s_cols[cols, Rp/32], where Cp and Rp are cols and rows rounded up to 32: the
+ * last block of a row or column is padded with zeros.  A NULL pair is skipped (a code pointer
+ * without its scale pointer, or the reverse, is SL_EINVAL).  With v = x / 2^X for the block's
+ * shared exponent X (scale byte X + 127):
+ *   SL_ROUND_NEAREST     X = clamp(floor(log2 amax) - 2, -127, 127); code = E2M1 of v, round half to
+ *                        even, saturating at 6 (the OCP MX conversion)
+ *   SL_ROUND_STOCHASTIC  X = the least exponent >= -127 with amax <= 6 * 2^X, so that nothing
+ *                        saturates; with s the step of E2M1 at |v| (0.5 below 2, 1 below 4, else 2),
+ *                        |code| = s * floor((floor(|v| / s * 2^16) + r) / 2^16).  r is the element's
+ *                        16-bit draw: element i of x (row-major) takes half word i % 8 (low halves
+ *                        first) of Philox4x32-7 at counter i / 8 with the 64-bit key
+ *                        seed + (seed_offset ? *seed_offset : 0) (mod 2^64).  Both copies use the same
+ *                        draws; the same key gives the same codes.
+ * seed_offset is a device pointer (8-byte aligned) or NULL, read when the kernel runs, so that a
+ * captured graph can be replayed with other draws; both are ignored by SL_ROUND_NEAREST.  A block of
+ * zeros has scale 0 and codes 0; a block with an infinity or a NaN has scale 255 and codes 0.
+ *
+ * sl_mxfp4_dequantize: out[rows, cols] (bf16) = deq(q, s); cols % 32 == 0.  Exact; 4 and 6 at scale
+ * 253 and every nonzero element from 2 up at scale 254 pass bf16's range and become infinite.
+ *
+ * Products (fp32 accumulation; bf16 results are rounded once):
+ *   fwd:   Y[T,out]           = deq(Xq)[T,in] . deq(Wq)[out,in]^T      in % 32 == 0
+ *   dgrad: dX[T,in]           = deq(dYq)[T,out] . deq(WqT)[in,out]^T   out % 32 == 0
+ *   wgrad: main_grad[out,in] += deq(dYqT)[out,T] . deq(XqT)[in,T]^T    T % 32 == 0, fp32, in place
+ * (the contracted extent is the padded one that sl_mxfp4_quantize writes; the others follow the
+ * conventions above; a contracted extent above 2^23 is SL_ESHAPE).  The weight gradient takes a device workspace of at least
+ * sl_mxfp4_wgrad_workspace_bytes(T, in, out) bytes (fp32 split-K planes; 0 when the shape needs no
+ * split, workspace may then be NULL): its initial contents do not matter, and calls that may run
+ * concurrently need distinct workspaces.  main_grad is read and written only inside [out, in].
+ *
+ * bf16 activations with MXFP4 weights blocked along in (in % 32 == 0), for serving and for frozen
+ * weights; every dequantised weight must be a finite bf16 value or a NaN:
+ *   fwd:   Y[T,out] = X[T,in] . deq(Wq)[out,in]^T        dgrad: dX[T,in] = dY[T,out] . deq(Wq)
+ * Each takes a device workspace of at least its query's bytes (0 for the forms that read the codes
+ * directly, few tokens among them; workspace may then be NULL), with the rules above.
+ * --------------------------------------------------------------------------------------------- */
+enum { SL_ROUND_NEAREST = 0, SL_ROUND_STOCHASTIC = 1 };
+int sl_mxfp4_quantize(void* stream, const void* x, int64_t rows, int64_t cols, uint8_t* q_rows,
+                      uint8_t* s_rows, uint8_t* q_cols, uint8_t* s_cols, int32_t rounding,
+                      uint64_t seed, const uint64_t* seed_offset);
+int sl_mxfp4_dequantize(void* stream, const uint8_t* q, const uint8_t* s, void* out, int64_t rows,
+                        int64_t cols);
+int sl_linear_fwd_mxfp4(void* stream, const uint8_t* Xq, const uint8_t* Xs, const uint8_t* Wq,
+                        const uint8_t* Ws, void* Y, int64_t T, int64_t in, int64_t out);
+int sl_linear_dgrad_mxfp4(void* stream, const uint8_t* dYq, const uint8_t* dYs, const uint8_t* WqT,
+                          const uint8_t* WsT, void* dX, int64_t T, int64_t in, int64_t out);
+size_t sl_mxfp4_wgrad_workspace_bytes(int64_t T, int64_t in, int64_t out);
+int sl_linear_wgrad_accum_mxfp4(void* stream, const uint8_t* dYqT, const uint8_t* dYsT,
+                                const uint8_t* XqT, const uint8_t* XsT, float* main_grad, int64_t T,
+                                int64_t in, int64_t out, void* workspace, size_t workspace_bytes);
+size_t sl_mxfp4w_fwd_workspace_bytes(int64_t T, int64_t in, int64_t out);
+int sl_linear_fwd_mxfp4w(void* stream, const void* X, const uint8_t* Wq, const uint8_t* Ws, void* Y,
+                         int64_t T, int64_t in, int64_t out, void* workspace, size_t workspace_bytes);
+size_t sl_mxfp4w_dgrad_workspace_bytes(int64_t T, int64_t in, int64_t out);
+int sl_linear_dgrad_mxfp4w(void* stream, const void* dY, const uint8_t* Wq, const uint8_t* Ws,
+                           void* dX, int64_t T, int64_t in, int64_t out, void* workspace,
+                           size_t workspace_bytes);
+
 #ifdef __cplusplus
 }
 #endif

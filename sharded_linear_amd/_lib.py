@@ -15,6 +15,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libsharded_linear.so")
 
 c_i32, c_i64, c_vp, c_sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t
+c_u64 = ctypes.c_uint64
 P_I64 = ctypes.POINTER(ctypes.c_int64)
 P_I32 = ctypes.POINTER(ctypes.c_int32)
 
@@ -46,6 +47,17 @@ PROTOTYPES = {
     "sl_nvfp4_materialize": (ctypes.c_int, [c_vp, c_vp, c_vp, c_vp, c_i64, c_i64]),
     "sl_linear_fwd_nvfp4w": (ctypes.c_int, [c_vp, c_vp, c_vp, ctypes.c_float, c_vp, c_i64, c_i64, c_i64]),
     "sl_linear_dgrad_nvfp4w": (ctypes.c_int, [c_vp, c_vp, c_vp, ctypes.c_float, c_vp, c_i64, c_i64, c_i64]),
+    "sl_mxfp4_quantize": (ctypes.c_int, [c_vp, c_vp, c_i64, c_i64, c_vp, c_vp, c_vp, c_vp, c_i32, c_u64, c_vp]),
+    "sl_mxfp4_dequantize": (ctypes.c_int, [c_vp, c_vp, c_vp, c_vp, c_i64, c_i64]),
+    "sl_linear_fwd_mxfp4": (ctypes.c_int, [c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64]),
+    "sl_linear_dgrad_mxfp4": (ctypes.c_int, [c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64]),
+    "sl_mxfp4_wgrad_workspace_bytes": (c_sz, [c_i64, c_i64, c_i64]),
+    "sl_linear_wgrad_accum_mxfp4": (ctypes.c_int, [c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64,
+                                                   c_vp, c_sz]),
+    "sl_mxfp4w_fwd_workspace_bytes": (c_sz, [c_i64, c_i64, c_i64]),
+    "sl_linear_fwd_mxfp4w": (ctypes.c_int, [c_vp, c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_vp, c_sz]),
+    "sl_mxfp4w_dgrad_workspace_bytes": (c_sz, [c_i64, c_i64, c_i64]),
+    "sl_linear_dgrad_mxfp4w": (ctypes.c_int, [c_vp, c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_vp, c_sz]),
 }
 
 _lib = None

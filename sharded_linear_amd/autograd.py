@@ -10,7 +10,8 @@ from __future__ import annotations
 
 import torch
 
-from .ops import sl_linear_dgrad, sl_linear_fwd, sl_linear_wgrad_accum
+from .ops import (sl_linear_dgrad, sl_linear_dgrad_mxfp4, sl_linear_fwd, sl_linear_fwd_mxfp4, sl_linear_wgrad_accum,
+                  sl_linear_wgrad_accum_mxfp4, sl_mxfp4_quantize)
 
 
 class LinearWithGradAccumulation(torch.autograd.Function):
@@ -36,3 +37,46 @@ class LinearWithGradAccumulation(torch.autograd.Function):
 
 def linear_with_grad_accumulation(input: torch.Tensor, weight: torch.Tensor) -> torch.Tensor:
     return LinearWithGradAccumulation.apply(input, weight)
+
+
+class LinearMXFP4WithGradAccumulation(torch.autograd.Function):
+    """The linear step with every product on MXFP4 operands: X, W and dY are cast inside the step, each
+    along the axis its product contracts.  What is kept for backward is X's columnwise copy (0.53 bytes an
+    element) and W's."""
+
+    @staticmethod
+    def forward(ctx, input, weight, seed, weight_mxfp4):
+        if ctx.needs_input_grad[1] and not hasattr(weight, "main_grad"):
+            raise ValueError("gradient accumulation fusion needs weight.main_grad (a grad_data view)")
+        x2 = input.reshape(-1, input.shape[-1]).contiguous()
+        xr, xrs, xc, xcs = sl_mxfp4_quantize(x2, cols=ctx.needs_input_grad[1])
+        if weight_mxfp4 is None:
+            weight_mxfp4 = sl_mxfp4_quantize(weight.detach(), cols=ctx.needs_input_grad[0])
+        wr, wrs, wc, wcs = weight_mxfp4
+        if ctx.needs_input_grad[0] and wc is None:
+            raise ValueError("the input gradient needs the weight's columnwise MXFP4 copy")
+        y = sl_linear_fwd_mxfp4(xr, xrs, wr, wrs)
+        ctx.save_for_backward(weight, xc, xcs, wc, wcs)
+        ctx.seed, ctx.shape = seed, input.shape
+        return y.view(*input.shape[:-1], weight.shape[0])
+
+    @staticmethod
+    def backward(ctx, grad_output):
+        weight, xc, xcs, wc, wcs = ctx.saved_tensors
+        dy = grad_output.reshape(-1, grad_output.shape[-1]).contiguous()
+        need_x, need_w = ctx.needs_input_grad[:2]
+        dr, drs, dc, dcs = sl_mxfp4_quantize(dy, rows=need_x, cols=need_w, seed=ctx.seed)
+        dx = sl_linear_dgrad_mxfp4(dr, drs, wc, wcs).view(ctx.shape) if need_x else None
+        if need_w:
+            sl_linear_wgrad_accum_mxfp4(dc, dcs, xc, xcs, weight.main_grad)
+            weight.grad_added_to_main_grad = True
+        return dx, None, None, None
+
+
+def linear_mxfp4_with_grad_accumulation(input: torch.Tensor, weight: torch.Tensor, seed=None,
+                                        weight_mxfp4=None) -> torch.Tensor:
+    """linear_with_grad_accumulation with all three products in MXFP4.  ``seed`` (see sl_mxfp4_quantize)
+    rounds dY stochastically, which keeps the gradients unbiased; a training loop gives every call its
+    own.  ``weight_mxfp4`` is sl_mxfp4_quantize(weight), made once and passed to every micro-batch that
+    uses the same weight; without it the weight is cast in each call."""
+    return LinearMXFP4WithGradAccumulation.apply(input, weight, seed, weight_mxfp4)

@@ -1,0 +1,47 @@
+// Internal interface of the MXFP4 kernels (not part of the C ABI).
+//
+// An MXFP4 matrix [R][K] (K a multiple of 32) is packed E2M1 codes [R][K/2], element 2j of a row in
+// the low nibble of byte j, and E8M0 scales [R][K/32]: element (r, k) stands for
+// E2M1(code) * 2^(scale[r][k/32] - 127).  E2M1 = sign, 2 exponent bits (bias 1), 1 mantissa bit
+// (0, 0.5, 1, 1.5, 2, 3, 4, 6).
+#pragma once
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+// Status of the launchers below: 0, or -5 where the HIP runtime reported an error at launch.
+
+// Quantises x[R][C] (bf16, row-major, 16-byte aligned, C % 8 == 0): rowwise codes qr[R][Cp/2] and
+// scales sr[R][Cp/32], and columnwise ones, stored transposed, qc[C][Rp/2] and sc[C][Rp/32], Cp and
+// Rp the extents rounded up to 32 (the last block padded with zeros).  A null pair is skipped.
+// Rounds to nearest, or stochastically with the key seed + (seed_offset ? *seed_offset : 0).
+struct F4QuantArgs {
+  const void* x;
+  int64_t R, C;
+  uint8_t *qr, *sr, *qc, *sc;
+  bool stochastic;
+  uint64_t seed;
+  const uint64_t* seed_offset;
+};
+int f4_quantize(hipStream_t st, const F4QuantArgs& a);
+
+// bf16 out[rows][cols] of codes q and scales s; cols % 32 == 0.
+int f4_dequantize(hipStream_t st, const uint8_t* q, const uint8_t* s, void* out, int64_t rows, int64_t cols);
+
+// C[M][N] = A . B^T of two MXFP4 operands A[M][K], B[N][K]: bf16 C, or fp32 C += (accum), unsplit or
+// with the partial sums of each split of K in its plane of ws[splits][M][N].  N % 8 == 0.
+struct F4Args {
+  const void *a, *b;    // codes
+  const void *sa, *sb;  // scales
+  void* c;
+  int64_t M, N, K;
+  float* ws;
+  int splits;           // splits of K, of kt_per_split stages each (accumulating product only)
+  int kt_per_split;
+  int cfg;
+};
+int f4_gemm(hipStream_t st, const F4Args& g);
+int f4_accum(hipStream_t st, const F4Args& g);
+
+// main_grad[M][N] += the planes of ws in split order (sl_gemm.hip).
+int f4_reduce(hipStream_t st, float* c, const float* ws, int64_t M, int64_t N, int splits);

@@ -27,6 +27,7 @@
 #include "sl_device.h"
 #include "sl_epi.h"
 #include "sl_gemm_f8.h"
+#include "sl_mx.h"
 
 namespace sl2 {
 
@@ -310,11 +311,6 @@ __global__ void __launch_bounds__(WGM * WGN * 64) gemm_f8fwd(F8Args g) {
 // flight (the kernel is bound by HBM bytes, 3 per element).  The product is formed by
 // v_cvt_scalef32_pk_bf16_fp8 with the scale as an fp32 power of two; it is exact whenever the
 // result is a normal bf16, which the entry points require.
-__device__ __forceinline__ float e8m0_to_f32(uint32_t s) {
-  if (s == 0xFFu) return __builtin_bit_cast(float, 0x7FC00000u);             // NaN scale
-  return s ? __builtin_bit_cast(float, s << 23) : __builtin_bit_cast(float, 0x00400000u);  // 2^-127
-}
-
 __global__ void __launch_bounds__(256) mx_dequant_bf16(const uint2* codes, const uint8_t* scales, uint4* out,
                                                        int64_t n8) {
   constexpr int U = 4;

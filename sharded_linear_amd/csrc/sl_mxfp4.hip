@@ -1,0 +1,140 @@
+// C-ABI entry points of the MXFP4 operators: argument checks and launches.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "sharded_linear.h"
+#include "sl_f4.h"
+
+namespace {
+
+constexpr int64_t kMaxExtent = int64_t(1) << 31;
+constexpr int64_t kMaxTiles = int64_t(1) << 31;        // workgroups of one launch
+constexpr int64_t kMaxK = int64_t(1) << 23;            // contraction extent: a tile's rows stay within 32-bit offsets
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Extents of a product [T, out] x [out, in]: k is the contracted one, held in blocks of 32.
+int check_product(int64_t T, int64_t in, int64_t out, int64_t k) {
+  if (T < 0 || in < 0 || out < 0) return SL_EINVAL;
+  if (T >= kMaxExtent || in >= kMaxExtent || out >= kMaxExtent) return SL_ESHAPE;
+  if (in % 8 || out % 8 || k % 32 || k > kMaxK) return SL_ESHAPE;
+  return SL_OK;
+}
+
+int check_grid(int64_t M, int64_t N) { return (M + 63) / 64 * ((N + 63) / 64) < kMaxTiles ? SL_OK : SL_ESHAPE; }
+
+// C[M][N] = A . B^T (bf16) over K
+int product(void* stream, const uint8_t* a, const uint8_t* sa, const uint8_t* b, const uint8_t* sb, void* c, int64_t M,
+            int64_t N, int64_t K) {
+  if (M == 0 || N == 0) return SL_OK;
+  if (!c || (K > 0 && (!a || !sa || !b || !sb))) return SL_EINVAL;
+  if (!aligned16(c) || !aligned16(a) || !aligned16(b)) return SL_EALIGN;
+  const int st = check_grid(M, N);
+  if (st) return st;
+  F4Args g{};
+  g.a = a; g.b = b; g.sa = sa; g.sb = sb; g.c = c;
+  g.M = M; g.N = N; g.K = K;
+  g.splits = 1;
+  return f4_gemm(static_cast<hipStream_t>(stream), g) == 0 ? SL_OK : SL_EHIP;
+}
+
+}  // namespace
+
+extern "C" int sl_mxfp4_quantize(void* stream, const void* x, int64_t rows, int64_t cols, uint8_t* q_rows,
+                                 uint8_t* s_rows, uint8_t* q_cols, uint8_t* s_cols, int32_t rounding, uint64_t seed,
+                                 const uint64_t* seed_offset) {
+  if (rows < 0 || cols < 0 || (rounding != SL_ROUND_NEAREST && rounding != SL_ROUND_STOCHASTIC)) return SL_EINVAL;
+  if (rows >= kMaxExtent || cols >= kMaxExtent || cols % 8) return SL_ESHAPE;
+  if (!q_rows != !s_rows || !q_cols != !s_cols) return SL_EINVAL;
+  if (rows == 0 || cols == 0 || (!q_rows && !q_cols)) return SL_OK;
+  if (!x) return SL_EINVAL;
+  if (!aligned16(x) || (q_rows && !aligned16(q_rows)) || (q_cols && !aligned16(q_cols))) return SL_EALIGN;
+  if (reinterpret_cast<uintptr_t>(seed_offset) & 7u) return SL_EALIGN;
+  const F4QuantArgs a{x, rows, cols, q_rows, s_rows, q_cols, s_cols, rounding == SL_ROUND_STOCHASTIC, seed, seed_offset};
+  return f4_quantize(static_cast<hipStream_t>(stream), a) == 0 ? SL_OK : SL_EHIP;
+}
+
+extern "C" int sl_mxfp4_dequantize(void* stream, const uint8_t* q, const uint8_t* s, void* out, int64_t rows,
+                                   int64_t cols) {
+  if (rows < 0 || cols < 0) return SL_EINVAL;
+  if (rows >= kMaxExtent || cols >= kMaxExtent || cols % 32) return SL_ESHAPE;
+  if (rows == 0 || cols == 0) return SL_OK;
+  if (!q || !s || !out) return SL_EINVAL;
+  if (!aligned16(q) || !aligned16(out)) return SL_EALIGN;
+  return f4_dequantize(static_cast<hipStream_t>(stream), q, s, out, rows, cols) == 0 ? SL_OK : SL_EHIP;
+}
+
+extern "C" int sl_linear_fwd_mxfp4(void* stream, const uint8_t* Xq, const uint8_t* Xs, const uint8_t* Wq,
+                                   const uint8_t* Ws, void* Y, int64_t T, int64_t in, int64_t out) {
+  const int st = check_product(T, in, out, in);
+  return st ? st : product(stream, Xq, Xs, Wq, Ws, Y, T, out, in);
+}
+
+extern "C" int sl_linear_dgrad_mxfp4(void* stream, const uint8_t* dYq, const uint8_t* dYs, const uint8_t* WqT,
+                                     const uint8_t* WsT, void* dX, int64_t T, int64_t in, int64_t out) {
+  const int st = check_product(T, in, out, out);
+  return st ? st : product(stream, dYq, dYs, WqT, WsT, dX, T, in, out);
+}
+
+extern "C" size_t sl_mxfp4_wgrad_workspace_bytes(int64_t T, int64_t in, int64_t out) {
+  if (check_product(T, in, out, T) || T == 0 || in == 0 || out == 0) return 0;
+  return 0;
+}
+
+extern "C" int sl_linear_wgrad_accum_mxfp4(void* stream, const uint8_t* dYqT, const uint8_t* dYsT, const uint8_t* XqT,
+                                           const uint8_t* XsT, float* main_grad, int64_t T, int64_t in, int64_t out,
+                                           void* workspace, size_t workspace_bytes) {
+  int st = check_product(T, in, out, T);
+  if (st) return st;
+  if (T == 0 || in == 0 || out == 0) return SL_OK;
+  if (!dYqT || !dYsT || !XqT || !XsT || !main_grad) return SL_EINVAL;
+  if (!aligned16(dYqT) || !aligned16(XqT) || !aligned16(main_grad)) return SL_EALIGN;
+  st = check_grid(out, in);
+  if (st) return st;
+  (void)workspace;
+  (void)workspace_bytes;
+  F4Args g{};
+  g.a = dYqT; g.b = XqT; g.sa = dYsT; g.sb = XsT; g.c = main_grad;
+  g.M = out; g.N = in; g.K = T;
+  g.splits = 1;
+  return f4_accum(static_cast<hipStream_t>(stream), g) == 0 ? SL_OK : SL_EHIP;
+}
+
+// ---- bf16 activations with MXFP4 weights ------------------------------------------------------
+
+extern "C" size_t sl_mxfp4w_fwd_workspace_bytes(int64_t T, int64_t in, int64_t out) {
+  if (check_product(T, in, out, in) || T == 0 || in == 0 || out == 0) return 0;
+  return size_t(out) * size_t(in) * 2;
+}
+
+extern "C" size_t sl_mxfp4w_dgrad_workspace_bytes(int64_t T, int64_t in, int64_t out) {
+  if (check_product(T, in, out, in) || T == 0 || in == 0 || out == 0) return 0;
+  return size_t(out) * size_t(in) * 2;
+}
+
+extern "C" int sl_linear_fwd_mxfp4w(void* stream, const void* X, const uint8_t* Wq, const uint8_t* Ws, void* Y,
+                                    int64_t T, int64_t in, int64_t out, void* workspace, size_t workspace_bytes) {
+  const int st = check_product(T, in, out, in);
+  if (st) return st;
+  if (T == 0 || out == 0) return SL_OK;
+  if (!Y || (in > 0 && (!X || !Wq || !Ws))) return SL_EINVAL;
+  if (!aligned16(X) || !aligned16(Wq) || !aligned16(Y)) return SL_EALIGN;
+  const size_t need = sl_mxfp4w_fwd_workspace_bytes(T, in, out);
+  if (need && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return SL_EWORKSPACE;
+  if (in > 0 && f4_dequantize(static_cast<hipStream_t>(stream), Wq, Ws, workspace, out, in)) return SL_EHIP;
+  return sl_linear_fwd(stream, X, workspace, Y, T, in, out);
+}
+
+extern "C" int sl_linear_dgrad_mxfp4w(void* stream, const void* dY, const uint8_t* Wq, const uint8_t* Ws, void* dX,
+                                      int64_t T, int64_t in, int64_t out, void* workspace, size_t workspace_bytes) {
+  const int st = check_product(T, in, out, in);
+  if (st) return st;
+  if (T == 0 || in == 0) return SL_OK;
+  if (!dX || (out > 0 && (!dY || !Wq || !Ws))) return SL_EINVAL;
+  if (!aligned16(dY) || !aligned16(Wq) || !aligned16(dX)) return SL_EALIGN;
+  const size_t need = sl_mxfp4w_dgrad_workspace_bytes(T, in, out);
+  if (need && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return SL_EWORKSPACE;
+  if (out > 0 && f4_dequantize(static_cast<hipStream_t>(stream), Wq, Ws, workspace, out, in)) return SL_EHIP;
+  return sl_linear_dgrad(stream, dY, workspace, dX, T, in, out);
+}

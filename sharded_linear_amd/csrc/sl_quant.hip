@@ -32,6 +32,7 @@
 
 #include "sl_device.h"
 #include "sl_gemm_f8.h"
+#include "sl_mx.h"
 
 namespace sl2 {
 
@@ -49,21 +50,6 @@ __device__ __forceinline__ uint32_t e4m3_code(float v) {
     code = uint32_t(__builtin_rintf(__uint_as_float(ab) * 512.0f));
   }
   return code | ((b >> 24) & 0x80u);
-}
-
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef short s16x2 __attribute__((ext_vector_type(2)));
-typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
-typedef short i16x4q __attribute__((ext_vector_type(4)));
-
-// Largest magnitude field of N words of two bf16 elements: |bf16| orders like its 15-bit magnitude.
-// Both halves are compared at once (packed 16-bit max).
-template <int N>
-__device__ __forceinline__ uint32_t mag_max(const uint32_t (&w)[N]) {
-  u16x2 m = {0, 0};
-#pragma unroll
-  for (int i = 0; i < N; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, w[i] & 0x7FFF7FFFu));
-  return m[0] > m[1] ? m[0] : m[1];
 }
 
 // Encodes N words of two bf16 elements (element 2i in the low half of word i) of a block whose
@@ -109,14 +95,6 @@ __device__ __forceinline__ uint32_t mx_encode(const uint32_t (&w)[N], uint32_t a
 // One block of 32 elements held by one thread.
 __device__ __forceinline__ uint32_t mx_block(const uint32_t (&w)[16], uint32_t (&q)[8]) {
   return mx_encode(w, mag_max(w), q);
-}
-
-// Largest value of m over the four lanes of a quad (DPP quad permutes [1,0,3,2] and [2,3,0,1]).
-__device__ __forceinline__ uint32_t quad_max(uint32_t m) {
-  uint32_t o = uint32_t(__builtin_amdgcn_update_dpp(0, int(m), 0xB1, 0xF, 0xF, false));
-  m = o > m ? o : m;
-  o = uint32_t(__builtin_amdgcn_update_dpp(0, int(m), 0x4E, 0xF, 0xF, false));
-  return o > m ? o : m;
 }
 
 constexpr int kQT = 128;                 // tile edge

@@ -344,3 +344,177 @@ def sl_linear_dgrad_nvfp4w(dY, Wm, w_scale: float, dX=None):
     check("sl_linear_dgrad_nvfp4w", lib().sl_linear_dgrad_nvfp4w(
         _stream(dev), _ptr(dY), _ptr(Wm), float(w_scale), _ptr(dX), T, n_in, n_out))
     return dX
+
+
+# ---- MXFP4 --------------------------------------------------------------------------------------
+# Matrices [r, k] as packed codes [r, k/2] and scales [r, k/32] (uint8), k a multiple of 32.
+
+def _launch(name, dev, *args):
+    """Calls the entry point on the current stream of ``dev``, with ``dev`` current."""
+    fn = getattr(lib(), name)
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        st = fn(_stream(dev), *args)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(_stream(dev), *args)
+    if st:
+        check(name, st)
+
+
+def _scratch(dev, need, workspace):
+    """(tensor, bytes) of the caller's workspace, or of one of this library's: the stream's shared one, or
+    under graph capture a new one, which belongs to the graph alone."""
+    if workspace is None and need:
+        with torch.cuda.device(dev):
+            workspace = (torch.empty(need, dtype=U8, device=dev) if torch.cuda.is_current_stream_capturing()
+                         else wgrad_workspace(dev, need))
+    return workspace, workspace.numel() * workspace.element_size() if workspace is not None else 0
+
+
+def _want_mxfp4(q, s, names, dev):
+    """Checks codes and scales against each other; returns (rows, k)."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 2:
+        raise ValueError(f"{names[0]} must be a matrix of packed codes [rows, k / 2]")
+    rows, half = q.shape
+    if half % 16:
+        raise ValueError(f"{names[0]} has {2 * half} elements to a row, which is no multiple of 32")
+    _want(q, names[0], U8, (rows, half), dev)
+    _want(s, names[1], U8, (rows, half // 16), dev)
+    return rows, 2 * half
+
+
+def _same(a, b, what):
+    if a != b:
+        raise ValueError(f"{what} differ: {a} and {b}")
+
+
+def sl_mxfp4_quantize(x, rows=True, cols=True, seed=None, out=None):
+    """MXFP4 copies of bf16 x[R, C] (C % 8 == 0): returns (q_rows, s_rows, q_cols, s_cols); a copy not
+    asked for is None.  Rowwise blocks of 32 run along C, columnwise ones down the columns, stored
+    transposed; the last block of a row or column is padded with zeros, so the copies are
+    [R, Cp/2] + [R, Cp/32] and [C, Rp/2] + [C, Rp/32] with the extents rounded up to 32.
+
+    ``seed`` None rounds to nearest (OCP MX).  An int, or a one-element int64 tensor on x's device
+    (read when the kernel runs, so a replayed graph can take another), rounds stochastically: the
+    same seed gives the same codes.  ``out`` may supply the four tensors."""
+    dev = _device(x)
+    if x.dim() != 2:
+        raise ValueError(f"x has shape {tuple(x.shape)}, expected a matrix")
+    R, C = x.shape
+    _want(x, "x", BF16, (R, C), dev)
+    if C % 8:
+        raise ValueError(f"x has {C} columns, which is no multiple of 8")
+    Rp, Cp = (R + 31) // 32 * 32, (C + 31) // 32 * 32
+    if out is None:
+        new = lambda *shape: torch.empty(shape, dtype=U8, device=dev)  # noqa: E731
+        out = ((new(R, Cp // 2), new(R, Cp // 32)) if rows else (None, None)) + \
+              ((new(C, Rp // 2), new(C, Rp // 32)) if cols else (None, None))
+    qr, sr, qc, sc = out
+    if qr is not None:
+        _want(qr, "q_rows", U8, (R, Cp // 2), dev)
+        _want(sr, "s_rows", U8, (R, Cp // 32), dev)
+    if qc is not None:
+        _want(qc, "q_cols", U8, (C, Rp // 2), dev)
+        _want(sc, "s_cols", U8, (C, Rp // 32), dev)
+    offset, key = None, 0
+    if isinstance(seed, torch.Tensor):
+        offset = seed
+        if offset.numel() != 1:
+            raise ValueError("a seed tensor has one element")
+        _want(offset, "seed", torch.int64, offset.shape, dev)
+    elif seed is not None:
+        key = int(seed) & 0xFFFFFFFFFFFFFFFF
+    _launch("sl_mxfp4_quantize", dev, _ptr(x), R, C, _ptr(qr), _ptr(sr), _ptr(qc), _ptr(sc),
+            int(seed is not None), key, _ptr(offset))
+    return qr, sr, qc, sc
+
+
+def sl_mxfp4_dequantize(q, s, out=None):
+    """bf16 out[r, k] = E2M1(code) * 2^(s[r, k/32] - 127) of packed codes q[R, K/2] and scales s[R, K/32]."""
+    dev = _device(q)
+    R, K = _want_mxfp4(q, s, ("q", "s"), dev)
+    if out is None:
+        out = torch.empty((R, K), dtype=BF16, device=dev)
+    _want(out, "out", BF16, (R, K), dev)
+    _launch("sl_mxfp4_dequantize", dev, _ptr(q), _ptr(s), _ptr(out), R, K)
+    return out
+
+
+def sl_linear_fwd_mxfp4(Xq, Xs, Wq, Ws, Y=None):
+    """Y[T,out] = deq(Xq, Xs)[T,in] . deq(Wq, Ws)[out,in]^T (bf16 out)."""
+    dev = _device(Xq)
+    T, n_in = _want_mxfp4(Xq, Xs, ("Xq", "Xs"), dev)
+    n_out, k = _want_mxfp4(Wq, Ws, ("Wq", "Ws"), dev)
+    _same(n_in, k, "the contracted extents of Xq and Wq")
+    if Y is None:
+        Y = torch.empty((T, n_out), dtype=BF16, device=dev)
+    _want(Y, "Y", BF16, (T, n_out), dev)
+    _launch("sl_linear_fwd_mxfp4", dev, _ptr(Xq), _ptr(Xs), _ptr(Wq), _ptr(Ws), _ptr(Y), T, n_in, n_out)
+    return Y
+
+
+def sl_linear_dgrad_mxfp4(dYq, dYs, WqT, WsT, dX=None):
+    """dX[T,in] = deq(dYq, dYs)[T,out] . deq(WqT, WsT)[in,out]^T (bf16 out)."""
+    dev = _device(dYq)
+    T, n_out = _want_mxfp4(dYq, dYs, ("dYq", "dYs"), dev)
+    n_in, k = _want_mxfp4(WqT, WsT, ("WqT", "WsT"), dev)
+    _same(n_out, k, "the contracted extents of dYq and WqT")
+    if dX is None:
+        dX = torch.empty((T, n_in), dtype=BF16, device=dev)
+    _want(dX, "dX", BF16, (T, n_in), dev)
+    _launch("sl_linear_dgrad_mxfp4", dev, _ptr(dYq), _ptr(dYs), _ptr(WqT), _ptr(WsT), _ptr(dX), T, n_in, n_out)
+    return dX
+
+
+def sl_mxfp4_wgrad_workspace_bytes(T: int, n_in: int, n_out: int) -> int:
+    return int(lib().sl_mxfp4_wgrad_workspace_bytes(T, n_in, n_out))
+
+
+def sl_linear_wgrad_accum_mxfp4(dYqT, dYsT, XqT, XsT, main_grad, workspace=None):
+    """main_grad[out,in] += deq(dYqT, dYsT)[out,T] . deq(XqT, XsT)[in,T]^T in fp32, in place."""
+    dev = _device(dYqT)
+    n_out, T = _want_mxfp4(dYqT, dYsT, ("dYqT", "dYsT"), dev)
+    n_in, k = _want_mxfp4(XqT, XsT, ("XqT", "XsT"), dev)
+    _same(T, k, "the contracted extents of dYqT and XqT")
+    _want(main_grad, "main_grad", F32, (n_out, n_in), dev)
+    workspace, nbytes = _scratch(dev, sl_mxfp4_wgrad_workspace_bytes(T, n_in, n_out), workspace)
+    _launch("sl_linear_wgrad_accum_mxfp4", dev, _ptr(dYqT), _ptr(dYsT), _ptr(XqT), _ptr(XsT), _ptr(main_grad), T, n_in,
+            n_out, _ptr(workspace), nbytes)
+    return main_grad
+
+
+def sl_mxfp4w_fwd_workspace_bytes(T: int, n_in: int, n_out: int) -> int:
+    return int(lib().sl_mxfp4w_fwd_workspace_bytes(T, n_in, n_out))
+
+
+def sl_linear_fwd_mxfp4w(X, Wq, Ws, Y=None, workspace=None):
+    """Y[T,out] = X[T,in] . deq(Wq, Ws)[out,in]^T with bf16 X and Y, from one token on."""
+    dev = _device(X)
+    n_out, n_in = _want_mxfp4(Wq, Ws, ("Wq", "Ws"), dev)
+    T = X.shape[0]
+    _want(X, "X", BF16, (T, n_in), dev)
+    if Y is None:
+        Y = torch.empty((T, n_out), dtype=BF16, device=dev)
+    _want(Y, "Y", BF16, (T, n_out), dev)
+    workspace, nbytes = _scratch(dev, sl_mxfp4w_fwd_workspace_bytes(T, n_in, n_out), workspace)
+    _launch("sl_linear_fwd_mxfp4w", dev, _ptr(X), _ptr(Wq), _ptr(Ws), _ptr(Y), T, n_in, n_out, _ptr(workspace), nbytes)
+    return Y
+
+
+def sl_mxfp4w_dgrad_workspace_bytes(T: int, n_in: int, n_out: int) -> int:
+    return int(lib().sl_mxfp4w_dgrad_workspace_bytes(T, n_in, n_out))
+
+
+def sl_linear_dgrad_mxfp4w(dY, Wq, Ws, dX=None, workspace=None):
+    """dX[T,in] = dY[T,out] . deq(Wq, Ws)[out,in] with bf16 dY and dX (a frozen MXFP4 weight's input gradient)."""
+    dev = _device(dY)
+    n_out, n_in = _want_mxfp4(Wq, Ws, ("Wq", "Ws"), dev)
+    T = dY.shape[0]
+    _want(dY, "dY", BF16, (T, n_out), dev)
+    if dX is None:
+        dX = torch.empty((T, n_in), dtype=BF16, device=dev)
+    _want(dX, "dX", BF16, (T, n_in), dev)
+    workspace, nbytes = _scratch(dev, sl_mxfp4w_dgrad_workspace_bytes(T, n_in, n_out), workspace)
+    _launch("sl_linear_dgrad_mxfp4w", dev, _ptr(dY), _ptr(Wq), _ptr(Ws), _ptr(dX), T, n_in, n_out, _ptr(workspace),
+            nbytes)
+    return dX
