@@ -35,13 +35,18 @@ struct F4Args {
   const void *sa, *sb;  // scales
   void* c;
   int64_t M, N, K;
+  int64_t ldc;          // N
   float* ws;
   int splits;           // splits of K, of kt_per_split stages each (accumulating product only)
   int kt_per_split;
-  int cfg;
+  int cfg;              // tile configuration: 0 256x256, 1 128x128, 2 256x128
+  float alpha;          // bf16 results are alpha * (A . B^T)
 };
+constexpr int kF4StageK = 256;                  // k elements of one stage
 int f4_gemm(hipStream_t st, const F4Args& g);
 int f4_accum(hipStream_t st, const F4Args& g);
 
+// The SL_TUNE_F8_CONFIG knob: a forced tile configuration of the block-scaled products, or -1 (sl_gemm.hip).
+int block_scaled_config();
 // main_grad[M][N] += the planes of ws in split order (sl_gemm.hip).
 int f4_reduce(hipStream_t st, float* c, const float* ws, int64_t M, int64_t N, int splits);

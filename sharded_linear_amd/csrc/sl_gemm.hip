@@ -36,6 +36,7 @@
 #include "sharded_linear.h"
 #include "sl_device.h"
 #include "sl_gemm2.h"
+#include "sl_f4.h"
 #include "sl_gemm_f8.h"
 
 namespace {
@@ -832,6 +833,16 @@ extern "C" int sl_linear_wgrad_accum_noalloc(void* stream, const void* X, const 
     if (st) return st;
   }
   return sl_linear_wgrad_accum(stream, X, dY, main_grad, T, in, out, ws, need ? kNoAllocScratchBytes : 0);
+}
+
+// ---- shared with the MXFP4 entry points (sl_f4.h) ----------------------------------------------
+
+int block_scaled_config() { return g_tune[SL_TUNE_F8_CONFIG].load(std::memory_order_relaxed); }
+
+int f4_reduce(hipStream_t st, float* c, const float* ws, int64_t M, int64_t N, int splits) {
+  Args a{};
+  a.M = int(M); a.N = int(N); a.c = c; a.ldc = N; a.splits = splits; a.ws = const_cast<float*>(ws);
+  return reduce_splits(st, a) == SL_OK ? 0 : -5;
 }
 
 // ---- MXFP8 operand entry points -----------------------------------------------------------

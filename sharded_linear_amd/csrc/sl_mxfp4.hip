@@ -24,6 +24,15 @@ int check_product(int64_t T, int64_t in, int64_t out, int64_t k) {
 
 int check_grid(int64_t M, int64_t N) { return (M + 63) / 64 * ((N + 63) / 64) < kMaxTiles ? SL_OK : SL_ESHAPE; }
 
+int64_t ntiles(int64_t M, int64_t N, int bm, int bn) { return (M + bm - 1) / bm * ((N + bn - 1) / bn); }
+
+// Tiles of a bf16 result: 256x256 where they fill most of the 256 CUs, else 128x128.
+int pick_config(int64_t M, int64_t N) {
+  const int forced = block_scaled_config();
+  if (forced >= 0) return forced;
+  return ntiles(M, N, 256, 256) >= 200 ? 0 : 1;
+}
+
 // C[M][N] = A . B^T (bf16) over K
 int product(void* stream, const uint8_t* a, const uint8_t* sa, const uint8_t* b, const uint8_t* sb, void* c, int64_t M,
             int64_t N, int64_t K) {
@@ -34,9 +43,33 @@ int product(void* stream, const uint8_t* a, const uint8_t* sa, const uint8_t* b,
   if (st) return st;
   F4Args g{};
   g.a = a; g.b = b; g.sa = sa; g.sb = sb; g.c = c;
-  g.M = M; g.N = N; g.K = K;
+  g.M = M; g.N = N; g.K = K; g.ldc = N;
   g.splits = 1;
+  g.alpha = 1.0f;
+  g.cfg = pick_config(M, N);
   return f4_gemm(static_cast<hipStream_t>(stream), g) == 0 ? SL_OK : SL_EHIP;
+}
+
+// Tiles and split of K of the weight gradient: 256x256 tiles; where those fill about half the chip and
+// 256x128 tiles fill it once, those, unsplit; otherwise K split to fill the 256 CUs, with at least 4
+// stages (an even number) to a split and at most 16 splits.
+F4Args wgrad_plan(int64_t T, int64_t in, int64_t out) {
+  F4Args g{};
+  g.M = out; g.N = in; g.K = T; g.ldc = in;
+  const int64_t t256 = ntiles(out, in, 256, 256), t128 = ntiles(out, in, 256, 128), nkt = (T + kF4StageK - 1) / kF4StageK;
+  const int forced = block_scaled_config();
+  g.cfg = forced >= 0 ? forced : (t256 <= 144 && t128 >= 240 && t128 <= 288) ? 2 : 0;
+  const int64_t tiles = g.cfg == 0 ? t256 : g.cfg == 2 ? t128 : ntiles(out, in, 128, 128);
+  int64_t s = tiles < 200 ? (256 + tiles / 2) / tiles : 1;
+  if (s > nkt / 4) s = nkt / 4;
+  if (s > 16) s = 16;
+  if (s < 1) s = 1;
+  int64_t per = (nkt + s - 1) / s;
+  per += per & 1;                        // the kernel starts at an even stage
+  g.kt_per_split = int(per);
+  g.splits = int((nkt + per - 1) / per);
+  g.alpha = 1.0f;
+  return g;
 }
 
 }  // namespace
@@ -79,7 +112,8 @@ extern "C" int sl_linear_dgrad_mxfp4(void* stream, const uint8_t* dYq, const uin
 
 extern "C" size_t sl_mxfp4_wgrad_workspace_bytes(int64_t T, int64_t in, int64_t out) {
   if (check_product(T, in, out, T) || T == 0 || in == 0 || out == 0) return 0;
-  return 0;
+  const F4Args g = wgrad_plan(T, in, out);
+  return g.splits > 1 ? size_t(g.splits) * size_t(out) * size_t(in) * 4 : 0;
 }
 
 extern "C" int sl_linear_wgrad_accum_mxfp4(void* stream, const uint8_t* dYqT, const uint8_t* dYsT, const uint8_t* XqT,
@@ -92,13 +126,17 @@ extern "C" int sl_linear_wgrad_accum_mxfp4(void* stream, const uint8_t* dYqT, co
   if (!aligned16(dYqT) || !aligned16(XqT) || !aligned16(main_grad)) return SL_EALIGN;
   st = check_grid(out, in);
   if (st) return st;
-  (void)workspace;
-  (void)workspace_bytes;
-  F4Args g{};
+  F4Args g = wgrad_plan(T, in, out);
+  if (g.splits > 1) {
+    if (!workspace || !aligned16(workspace) || workspace_bytes < sl_mxfp4_wgrad_workspace_bytes(T, in, out))
+      return SL_EWORKSPACE;
+    g.ws = static_cast<float*>(workspace);
+  }
   g.a = dYqT; g.b = XqT; g.sa = dYsT; g.sb = XsT; g.c = main_grad;
-  g.M = out; g.N = in; g.K = T;
-  g.splits = 1;
-  return f4_accum(static_cast<hipStream_t>(stream), g) == 0 ? SL_OK : SL_EHIP;
+  const hipStream_t hs = static_cast<hipStream_t>(stream);
+  if (f4_accum(hs, g)) return SL_EHIP;
+  if (g.splits > 1 && f4_reduce(hs, main_grad, g.ws, out, in, g.splits)) return SL_EHIP;
+  return SL_OK;
 }
 
 // ---- bf16 activations with MXFP4 weights ------------------------------------------------------
