@@ -50,33 +50,39 @@ __device__ __forceinline__ i32x8 f4_operand(i32x4 v) {           // the 4-bit fo
   return __builtin_shufflevector(v, v, 0, 1, 2, 3, -1, -1, -1, -1);
 }
 
-// Block scales, two ways.  SC: where every row of scales starts 16-byte aligned (K % 512 == 0), the
-// scales of two stages come at once, 16 bytes a row, into a double-buffered cache behind the
-// operand slots.  Otherwise each stage brings, into its slot, the three aligned dwords that hold a row's 8 bytes,
-// wherever they start, and the reader shifts them into place.
+// Block scales are 8 bytes a row and stage, far less than the 128-byte lines they lie in: direct loads
+// to LDS of 16 bytes a row and two stages moved a line for every 16 bytes and cost 335 of a stage's 3150
+// cycles, and where rows of scales start at odd addresses (4-byte pieces) 2100 of 5300.  So each thread
+// loads its rows' scales of 8 stages (64 bytes a row) into registers ahead of time, and they go to
+// LDS together when the 8 stages before them are done.  On the way a row's bytes are shifted into place
+// and cut at the row's end, so any K and any address takes the same path.
+template <int BM, int BN, int WGM, int WGN, bool ACC>
+struct F4Layout {
+  static constexpr int WAVES = WGM * WGN;
+  static constexpr int kSlot = (BM + BN) * kF4Row;
+  static constexpr int kRows = (BM + BN + WAVES * 64 - 1) / (WAVES * 64);   // rows of scales of a thread
+  static constexpr int kCache = 2 * kSlot;
+  static constexpr int kRing = kCache + kRows * WAVES * 64 * 8 * kF4Blocks;
+  static constexpr int kEpi = WAVES * EpiOf<BM / WGM, BN / WGN, ACC>::kBytes;
+  static constexpr int kLds = kRing > kEpi ? kRing : kEpi;
+  static_assert(kLds <= 160 * 1024, "LDS");
+};
+
 // One operand of a workgroup's tile: rows row0 .. row0 + R - 1 of a matrix of `rows` rows.
-template <int R, int WAVES, bool SC>
+template <int R, int WAVES>
 struct F4Side {
   static constexpr int kLoads = R * kF4Row / 1024 / WAVES;       // code loads of a wave in a stage
-  // scale loads of a wave, for a group of two stages or for one stage, and their LDS bytes: whole
-  // rounds of the waves' loads, the surplus reading zeros
-  static constexpr int kScaleLoads = (R * (SC ? 1 : 3) / 64 + WAVES - 1) / WAVES;
-  static constexpr int kScaleBytes = kScaleLoads * WAVES * 64 * (SC ? 16 : 4);
   static_assert(R * kF4Row % (1024 * WAVES) == 0 && WAVES % 2 == 0, "loads per wave");
-  i32x4 rc, rs;
-  uint32_t voff, step, nb, rows, sbase;
+  i32x4 rc;
+  uint32_t voff, step, nb;
   int chunk;
 
-  __device__ __forceinline__ void init(const void* codes, const void* scales, int64_t row0, int64_t all, int64_t K,
-                                       int lane, int wave) {
+  __device__ __forceinline__ void init(const void* codes, int64_t row0, int64_t all, int64_t K, int lane, int wave) {
     nb = uint32_t(K / 32);
-    rows = uint32_t(all - row0 < R ? all - row0 : R);
-    // descriptors over this tile's rows: offsets fit 32 bits whatever the matrix's size, and rows
+    // a descriptor over this tile's rows: offsets fit 32 bits whatever the matrix's size, and rows
     // past the end read zeros
+    const uint32_t rows = uint32_t(all - row0 < R ? all - row0 : R);
     rc = rsrc(static_cast<const char*>(codes) + row0 * (K / 2), rows * uint32_t(K / 2));
-    const uintptr_t s = reinterpret_cast<uintptr_t>(scales) + uintptr_t(row0 * nb);
-    sbase = uint32_t(s & 3);
-    rs = rsrc(reinterpret_cast<const void*>(s & ~uintptr_t(3)), (sbase + rows * nb + 3) & ~3u);
     // wave-load wl = it * WAVES + wave covers rows 8 wl .. 8 wl + 7, 8 lanes a row; its swizzle depends
     // on the wave alone, since WAVES is even
     chunk = (lane & 7) ^ f4_swz(8 * wave + (lane >> 3));
@@ -90,34 +96,62 @@ struct F4Side {
   __device__ __forceinline__ void load(uint32_t lds, uint32_t off, int it, int wave) const {
     lds_dma16(rc, lds + uint32_t(it * WAVES + wave) * 1024, off + uint32_t(it) * step);
   }
-  // SC: wave-load q of scale group G: 16 bytes of rows 64 q .. 64 q + 63
-  __device__ __forceinline__ void load_group(uint32_t lds, int q, int G, int lane) const {
-    const uint32_t r = uint32_t(q * 64 + lane);
-    lds_dma16(rs, lds + uint32_t(q) * 1024, r < rows && uint32_t(G) * 16 < nb ? r * nb + uint32_t(G) * 16 : kOOB);
-  }
-  // not SC: wave-load q of the stage's scale dwords [3][R]; dword d of row r holds bytes 4 d .. of the
-  // aligned words that start at or below the row's first byte of this stage
-  __device__ __forceinline__ void load_scales(uint32_t lds, int q, int kt, int lane) const {
-    const uint32_t i = uint32_t(q * 64 + lane), d = i / R, r = i % R;
-    const uint32_t a = ((sbase + r * nb + uint32_t(kt) * kF4Blocks) & ~3u) + d * 4;
-    lds_dma4(rs, lds + uint32_t(q) * 256, d < 3 && r < rows && uint32_t(kt) * kF4Blocks < nb ? a : kOOB);
-  }
 };
 
-template <int BM, int BN, int WGM, int WGN, bool ACC, bool SC>
-struct F4Layout {
-  static constexpr int WAVES = WGM * WGN;
-  static constexpr int kCodes = (BM + BN) * kF4Row;
-  using SA = F4Side<BM, WAVES, SC>;
-  using SB = F4Side<BN, WAVES, SC>;
-  static constexpr int kScaleB = kCodes + SA::kScaleBytes;       // not SC: B's scales in the slot, A's at kCodes
-  static constexpr int kSlot = kCodes + (SC ? 0 : SA::kScaleBytes + SB::kScaleBytes);
-  static constexpr int kCache = 2 * kSlot;
-  static constexpr int kGroup = SA::kScaleBytes + SB::kScaleBytes;
-  static constexpr int kRing = kCache + (SC ? 2 * kGroup : 0);
-  static constexpr int kEpi = WAVES * EpiOf<BM / WGM, BN / WGN, ACC>::kBytes;
-  static constexpr int kLds = kRing > kEpi ? kRing : kEpi;
-  static_assert(kLds <= 160 * 1024, "LDS");
+// LDS place of the 8 scale bytes of stage u (0 .. 7 of its group) of row r: every 32 consecutive rows
+// of a stage lie in distinct banks.
+__device__ __forceinline__ uint32_t f4_scale_at(int r, int u) {
+  return uint32_t(r) * (8 * kF4Blocks) + (uint32_t(u ^ ((r >> 2) & 7)) << 3);
+}
+
+// A row's scales of a group of 8 stages, as the 17 aligned dwords that hold their 64 bytes.
+struct F4Scales {
+  __amdgpu_buffer_rsrc_t rs;
+  uint32_t first, nb;        // byte offset of the row's first scale in rs, and its scales
+  uint32_t w[17];
+
+  // row r of the tile at row0 (r < rows) of a matrix of scales; other rows hold zeros
+  __device__ __forceinline__ void init(const void* scales, int64_t row0, uint32_t rows, uint32_t r, int64_t K) {
+    nb = uint32_t(K / 32);
+    const uintptr_t s = reinterpret_cast<uintptr_t>(scales) + uintptr_t(row0 * nb);
+    const uint32_t low = uint32_t(s & 3);
+    // the first and last word may hold up to 3 bytes beside the tile's scales; of a load that passes the
+    // extent, the words inside arrive
+    rs = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(s & ~uintptr_t(3)), 0, int((low + rows * nb + 3) & ~3u),
+                                           kRsrcWord3);
+    first = low + r * nb;
+    if (r >= rows) nb = 0;
+  }
+  // stages kt .. kt + 7
+  __device__ __forceinline__ void load(int kt) {
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    const uint32_t off = uint32_t(kt) * kF4Blocks < nb ? (first + uint32_t(kt) * kF4Blocks) & ~3u : kOOB;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const u32x4 v = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, off + q * 16, 0, 0));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[4 * q + e] = v[e];
+    }
+    w[16] = __builtin_amdgcn_raw_buffer_load_b32(rs, off + 64, 0, 0);
+  }
+  // to row r of the cache at lds; CUT: the group that starts at stage kt passes the row's end
+  template <bool CUT>
+  __device__ __forceinline__ void store(uint32_t lds, int r, int kt) const {
+    const uint32_t sh = first & 3;
+    // what follows a row's last block is another row's scale, perhaps a NaN: the zero codes there get 2^-127
+    const int left = int(nb) - kt * kF4Blocks;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      i32x2 d;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t v = __builtin_amdgcn_alignbyte(w[2 * u + e + 1], w[2 * u + e], sh);
+        const int n = left - 4 * (2 * u + e);                    // bytes of this dword within the row
+        d[e] = int(!CUT || n >= 4 ? v : n <= 0 ? 0u : v & (0xFFFFFFFFu >> (32 - 8 * n)));
+      }
+      *reinterpret_cast<__attribute__((address_space(3))) i32x2*>(uintptr_t(lds + f4_scale_at(r, u))) = d;
+    }
+  }
 };
 
 // The four scale bytes that lane group h needs of 8 consecutive ones, 2 ks + h in byte ks.
@@ -125,12 +159,12 @@ __device__ __forceinline__ int f4_pick(uint32_t lo, uint32_t hi, uint32_t sel) {
   return int(__builtin_amdgcn_perm(hi, lo, sel));
 }
 
-template <int BM, int BN, int WGM, int WGN, bool ACC, bool SC>
+template <int BM, int BN, int WGM, int WGN, bool ACC>
 __global__ void __launch_bounds__(WGM * WGN * 64) gemm_f4(F4Args g) {
-  using L = F4Layout<BM, BN, WGM, WGN, ACC, SC>;
+  using L = F4Layout<BM, BN, WGM, WGN, ACC>;
   constexpr int WAVES = WGM * WGN, WM = BM / WGM, WN = BN / WGN, TM = WM / 32, TN = WN / 32;
-  using SA = F4Side<BM, WAVES, SC>;
-  using SB = F4Side<BN, WAVES, SC>;
+  using SA = F4Side<BM, WAVES>;
+  using SB = F4Side<BN, WAVES>;
   extern __shared__ __attribute__((aligned(1024))) char smem[];
   const uint32_t lds = lds_addr(smem);
 
@@ -150,8 +184,17 @@ __global__ void __launch_bounds__(WGM * WGN * 64) gemm_f4(F4Args g) {
 
   SA a;
   SB b;
-  a.init(g.a, g.sa, m0, g.M, g.K, lane, wave);
-  b.init(g.b, g.sb, n0, g.N, g.K, lane, wave);
+  a.init(g.a, m0, g.M, g.K, lane, wave);
+  b.init(g.b, n0, g.N, g.K, lane, wave);
+  // row q of A's then B's rows belongs to thread q % threads; every wave's rows are of one operand
+  F4Scales sc[L::kRows];
+  const uint32_t rows_a = uint32_t(min(g.M - m0, int64_t(BM))), rows_b = uint32_t(min(g.N - n0, int64_t(BN)));
+#pragma unroll
+  for (int n = 0; n < L::kRows; ++n) {
+    const int q0 = n * WAVES * 64 + wave * 64;
+    if (q0 < BM) sc[n].init(g.sa, m0, rows_a, q0 + lane, g.K);
+    else sc[n].init(g.sb, n0, rows_b, q0 - BM + lane, g.K);
+  }
 
   // fragment addresses: row r's chunk 2 ks + h sits in slot (2 ks + h) ^ swz(r) of the row's eight
   const int fr = lane & 31, h = lane >> 5;
@@ -159,50 +202,21 @@ __global__ void __launch_bounds__(WGM * WGN * 64) gemm_f4(F4Args g) {
   const uint32_t fb0 = lds + BM * kF4Row + uint32_t(wn * WN + fr) * kF4Row + uint32_t((h ^ f4_swz(fr)) << 4);
   const uint32_t sel = h ? 0x07050301u : 0x06040200u;
 
-  auto load_group = [&](int G) {                                 // SC
-    const uint32_t c = lds + L::kCache + uint32_t(G & 1) * L::kGroup;
+  auto load_scales = [&](int kt) {
 #pragma unroll
-    for (int it = 0; it < SA::kScaleLoads; ++it) a.load_group(c, it * WAVES + wave, G, lane);
-#pragma unroll
-    for (int it = 0; it < SB::kScaleLoads; ++it) b.load_group(c + SA::kScaleBytes, it * WAVES + wave, G, lane);
+    for (int n = 0; n < L::kRows; ++n) sc[n].load(kt);
   };
-  auto load_scales = [&](int kt, uint32_t slot) {                // not SC
+  auto store_scales = [&](int kt) {
 #pragma unroll
-    for (int it = 0; it < SA::kScaleLoads; ++it) a.load_scales(slot + L::kCodes, it * WAVES + wave, kt, lane);
-#pragma unroll
-    for (int it = 0; it < SB::kScaleLoads; ++it) b.load_scales(slot + L::kScaleB, it * WAVES + wave, kt, lane);
-  };
-  // the LDS words with the scales of row r, A's or B's, of a stage in half `par` of its group and in
-  // slot `par`; and the register of scale bytes made of them
-  struct Raw { uint32_t d[SC ? 2 : 3]; };
-  auto read_scales = [&](auto is_a, int r, int kt, auto par) {
-    constexpr bool A = decltype(is_a)::value != 0;
-    Raw w;
-    if constexpr (SC) {
-      const i32x2 v = lds_read<i32x2>(lds + L::kCache + uint32_t((kt >> 1) & 1) * L::kGroup + (A ? 0 : SA::kScaleBytes) +
-                                      uint32_t(r) * 16 + par.value * 8);
-      w.d[0] = v[0];
-      w.d[1] = v[1];
-    } else {
-      const uint32_t at = lds + par.value * L::kSlot + (A ? L::kCodes : L::kScaleB) + uint32_t(r) * 4;
-#pragma unroll
-      for (int d = 0; d < 3; ++d) w.d[d] = lds_read<uint32_t>(at + d * (A ? BM : BN) * 4);
-    }
-    return w;
-  };
-  auto make_scales = [&](auto is_a, const Raw& w, int r, int kt) -> int {
-    if constexpr (SC) {
-      return f4_pick(w.d[0], w.d[1], sel);
-    } else {
-      const uint32_t nb = a.nb, base = decltype(is_a)::value ? a.sbase : b.sbase;
-      const uint32_t sh = (base + uint32_t(r) * nb) & 3;
-      const int v = f4_pick(__builtin_amdgcn_alignbyte(w.d[1], w.d[0], sh), __builtin_amdgcn_alignbyte(w.d[2], w.d[1], sh), sel);
-      // what follows a row's last block is another row's scale, perhaps a NaN: the zero codes there get 2^-127
-      const int left = int(nb) - kt * kF4Blocks - h;
-      return v & (left > 6 ? -1 : left > 4 ? 0xFFFFFF : left > 2 ? 0xFFFF : left > 0 ? 0xFF : 0);
+    for (int n = 0; n < L::kRows; ++n) {
+      const uint32_t c = lds + L::kCache;
+      if (kt * kF4Blocks + 8 * kF4Blocks <= int(g.K / 32)) sc[n].template store<false>(c, n * WAVES * 64 + tid, kt);
+      else sc[n].template store<true>(c, n * WAVES * 64 + tid, kt);
     }
   };
-  const int ar = wm * WM + fr, br = wn * WN + fr;                // this lane's first fragment rows
+  auto read_scales = [&](int r, int kt) { return lds_read<i32x2>(lds + L::kCache + f4_scale_at(r, (kt - kt0) & 7)); };
+  auto make_scales = [&](i32x2 w) -> int { return f4_pick(w[0], w[1], sel); };
+  const int ar = wm * WM + fr, br = BM + wn * WN + fr;          // this lane's first fragment rows, A's and B's
 
   f32x16 acc[TM][TN];
 #pragma unroll
@@ -220,7 +234,7 @@ __global__ void __launch_bounds__(WGM * WGN * 64) gemm_f4(F4Args g) {
   auto stage = [&](int kt, auto par) {
     constexpr int P = decltype(par)::value;
     const uint32_t cur = P * L::kSlot, nxt = L::kSlot - cur;
-    Raw na[TM], nb[TN];
+    i32x2 na[TM], nb[TN];
     static_for<4>([&](auto kc) {
       constexpr int ks = decltype(kc)::value, p = ks & 1;
       uint32_t oa = kOOB, ob = kOOB;
@@ -231,8 +245,6 @@ __global__ void __launch_bounds__(WGM * WGN * 64) gemm_f4(F4Args g) {
         bare_barrier();
         oa = kt + 2 < kt1 ? a.at(kt + 2) : kOOB;
         ob = kt + 2 < kt1 ? b.at(kt + 2) : kOOB;
-        if constexpr (!SC) load_scales(kt + 2, lds + cur);
-        else if constexpr (P == 0) load_group((kt + 2) >> 1);
       }
       const uint32_t ra = (ks == 3 ? fa0 + nxt : (fa0 ^ uint32_t((ks + 1) << 5)) + cur);
       const uint32_t rb = (ks == 3 ? fb0 + nxt : (fb0 ^ uint32_t((ks + 1) << 5)) + cur);
@@ -242,8 +254,8 @@ __global__ void __launch_bounds__(WGM * WGN * 64) gemm_f4(F4Args g) {
         constexpr int n = decltype(nc)::value;
         if constexpr (n < TN) fb[p ^ 1][n] = lds_read<i32x4>(rb + n * 32 * kF4Row);
         else if constexpr (n < kReads) fa[p ^ 1][n - TN] = lds_read<i32x4>(ra + (n - TN) * 32 * kF4Row);
-        else if constexpr (ks == 3 && n < kReads + TN) nb[n - kReads] = read_scales(ic<0>{}, br + (n - kReads) * 32, kt + 1, ic<1 - P>{});
-        else if constexpr (ks == 3 && n < 2 * kReads) na[n - kReads - TN] = read_scales(ic<1>{}, ar + (n - kReads - TN) * 32, kt + 1, ic<1 - P>{});
+        else if constexpr (ks == 3 && n < kReads + TN) nb[n - kReads] = read_scales(br + (n - kReads) * 32, kt + 1);
+        else if constexpr (ks == 3 && n < 2 * kReads) na[n - kReads - TN] = read_scales(ar + (n - kReads - TN) * 32, kt + 1);
       };
       auto load = [&](auto nc) {
         constexpr int n = decltype(nc)::value;
@@ -263,38 +275,47 @@ __global__ void __launch_bounds__(WGM * WGN * 64) gemm_f4(F4Args g) {
       });
     });
 #pragma unroll
-    for (int j = 0; j < TN; ++j) scb[j] = make_scales(ic<0>{}, nb[j], br + j * 32, kt + 1);
+    for (int j = 0; j < TN; ++j) scb[j] = make_scales(nb[j]);
 #pragma unroll
-    for (int i = 0; i < TM; ++i) sca[i] = make_scales(ic<1>{}, na[i], ar + i * 32, kt + 1);
+    for (int i = 0; i < TM; ++i) sca[i] = make_scales(na[i]);
   };
 
   if (kt0 < kt1) {
-    // stages kt0 (even) and kt0 + 1
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const int kt = kt0 + s;
-      const uint32_t slot = lds + s * L::kSlot, oa = kt < kt1 ? a.at(kt) : kOOB, ob = kt < kt1 ? b.at(kt) : kOOB;
-      if constexpr (!SC) load_scales(kt, slot);
-      else if (s == 0) load_group(kt >> 1);
+    auto load_stage = [&](int kt, uint32_t slot) {
+      const uint32_t oa = kt < kt1 ? a.at(kt) : kOOB, ob = kt < kt1 ? b.at(kt) : kOOB;
 #pragma unroll
       for (int it = 0; it < SA::kLoads; ++it) a.load(slot, oa, it, wave);
 #pragma unroll
       for (int it = 0; it < SB::kLoads; ++it) b.load(slot + BM * kF4Row, ob, it, wave);
-    }
-    wait_vmcnt<kLoads>();
+    };
+    load_scales(kt0);
+    load_stage(kt0, lds);
+    wait_vmcnt<0>();
+    load_stage(kt0 + 1, lds + L::kSlot);
+    store_scales(kt0);
+    wait_lgkm0();
     bare_barrier();
 #pragma unroll
     for (int j = 0; j < TN; ++j) fb[0][j] = lds_read<i32x4>(fb0 + j * 32 * kF4Row);
 #pragma unroll
     for (int i = 0; i < TM; ++i) fa[0][i] = lds_read<i32x4>(fa0 + i * 32 * kF4Row);
 #pragma unroll
-    for (int j = 0; j < TN; ++j) scb[j] = make_scales(ic<0>{}, read_scales(ic<0>{}, br + j * 32, kt0, ic<0>{}), br + j * 32, kt0);
+    for (int j = 0; j < TN; ++j) scb[j] = make_scales(read_scales(br + j * 32, kt0));
 #pragma unroll
-    for (int i = 0; i < TM; ++i) sca[i] = make_scales(ic<1>{}, read_scales(ic<1>{}, ar + i * 32, kt0, ic<0>{}), ar + i * 32, kt0);
+    for (int i = 0; i < TM; ++i) sca[i] = make_scales(read_scales(ar + i * 32, kt0));
 
     // an odd last stage is followed by one of zeros: with one exit the accumulators stay in place
     for (int kt = kt0; kt < kt1; kt += 2) {
+      const int u = (kt - kt0) & 7;
+      if (u == 0) load_scales(kt + 8);
       stage(kt, ic<0>{});
+      if (u == 6) {
+        // the group's last scales are in registers once every wave is here; the next group's landed long
+        // ago and is read after the coming stage's barrier
+        wait_lgkm0();
+        bare_barrier();
+        store_scales(kt + 2);
+      }
       stage(kt + 1, ic<1>{});
     }
   }
@@ -303,21 +324,15 @@ __global__ void __launch_bounds__(WGM * WGN * 64) gemm_f4(F4Args g) {
   store_tile<WM, WN, TM, TN, ACC>(g, acc, smem, m0 + wm * WM, n0 + wn * WN, split, lane, wave);
 }
 
-template <int BM, int BN, int WGM, int WGN, bool ACC, bool SC>
-int launch_f4_sc(hipStream_t st, const F4Args& g) {
-  constexpr int lds = F4Layout<BM, BN, WGM, WGN, ACC, SC>::kLds;
-  auto kfn = gemm_f4<BM, BN, WGM, WGN, ACC, SC>;
+template <int BM, int BN, int WGM, int WGN, bool ACC>
+int launch_f4(hipStream_t st, const F4Args& g) {
+  constexpr int lds = F4Layout<BM, BN, WGM, WGN, ACC>::kLds;
+  auto kfn = gemm_f4<BM, BN, WGM, WGN, ACC>;
   static std::atomic<uint64_t> attr{0};
   if (smem_attr_once(reinterpret_cast<const void*>(kfn), lds, attr)) return -5;
   const int64_t tiles = (g.M + BM - 1) / BM * ((g.N + BN - 1) / BN);
   hipLaunchKernelGGL(kfn, dim3(unsigned(tiles), 1, ACC ? g.splits : 1), dim3(WGM * WGN * 64), lds, st, g);
   return hipGetLastError() == hipSuccess ? 0 : -5;
-}
-
-template <int BM, int BN, int WGM, int WGN, bool ACC>
-int launch_f4(hipStream_t st, const F4Args& g) {
-  const bool sc = g.K % 512 == 0 && ((reinterpret_cast<uintptr_t>(g.sa) | reinterpret_cast<uintptr_t>(g.sb)) & 15u) == 0;
-  return sc ? launch_f4_sc<BM, BN, WGM, WGN, ACC, true>(st, g) : launch_f4_sc<BM, BN, WGM, WGN, ACC, false>(st, g);
 }
 
 template <bool ACC>
