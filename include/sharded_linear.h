@@ -304,8 +304,8 @@ int sl_linear_dgrad_nvfp4w(void* stream, const void* dY, const void* Wm, float w
  *   dgrad: dX[T,in]           = deq(dYq)[T,out] . deq(WqT)[in,out]^T   out % 32 == 0
  *   wgrad: main_grad[out,in] += deq(dYqT)[out,T] . deq(XqT)[in,T]^T    T % 32 == 0, fp32, in place
  * (the contracted extent is the padded one that sl_mxfp4_quantize writes; the others follow the
- * conventions above; a contracted extent above 2^23 is SL_ESHAPE).  The weight gradient takes a device workspace of at least
- * sl_mxfp4_wgrad_workspace_bytes(T, in, out) bytes (fp32 split-K planes; 0 when the shape needs no
+ * conventions above; in, out or a contracted extent above 2^23 is SL_ESHAPE).  The weight gradient
+ * takes a device workspace of at least sl_mxfp4_wgrad_workspace_bytes(T, in, out) bytes (fp32 split-K planes; 0 when the shape needs no
  * split, workspace may then be NULL): its initial contents do not matter, and calls that may run
  * concurrently need distinct workspaces.  main_grad is read and written only inside [out, in].
  *

@@ -35,12 +35,10 @@ struct F4Args {
   const void *sa, *sb;  // scales
   void* c;
   int64_t M, N, K;
-  int64_t ldc;          // N
   float* ws;
   int splits;           // splits of K, of kt_per_split stages each (accumulating product only)
   int kt_per_split;
   int cfg;              // tile configuration: 0 256x256, 1 128x128, 2 256x128
-  float alpha;          // bf16 results are alpha * (A . B^T)
 };
 constexpr int kF4StageK = 256;                  // k elements of one stage
 int f4_gemm(hipStream_t st, const F4Args& g);

@@ -21,8 +21,8 @@
 #include <cstdint>
 
 #include "sl_device.h"
-#include "sl_epi.h"
 #include "sl_f4.h"
+#include "sl_mx.h"
 
 namespace sl2 {
 
@@ -33,6 +33,7 @@ constexpr int kF4Blocks = kF4StageK / 32;       // scale blocks (and 16-byte chu
 __device__ __forceinline__ int f4_swz(int r) { return (r & 7) ^ ((r >> 3) & 1); }
 
 typedef int i32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 // LDS reads by byte address
 template <class T>
@@ -56,15 +57,13 @@ __device__ __forceinline__ i32x8 f4_operand(i32x4 v) {           // the 4-bit fo
 // loads its rows' scales of 8 stages (64 bytes a row) into registers ahead of time, and they go to
 // LDS together when the 8 stages before them are done.  On the way a row's bytes are shifted into place
 // and cut at the row's end, so any K and any address takes the same path.
-template <int BM, int BN, int WGM, int WGN, bool ACC>
+template <int BM, int BN, int WGM, int WGN>
 struct F4Layout {
   static constexpr int WAVES = WGM * WGN;
   static constexpr int kSlot = (BM + BN) * kF4Row;
   static constexpr int kRows = (BM + BN + WAVES * 64 - 1) / (WAVES * 64);   // rows of scales of a thread
   static constexpr int kCache = 2 * kSlot;
-  static constexpr int kRing = kCache + kRows * WAVES * 64 * 8 * kF4Blocks;
-  static constexpr int kEpi = WAVES * EpiOf<BM / WGM, BN / WGN, ACC>::kBytes;
-  static constexpr int kLds = kRing > kEpi ? kRing : kEpi;
+  static constexpr int kLds = kCache + kRows * WAVES * 64 * 8 * kF4Blocks;
   static_assert(kLds <= 160 * 1024, "LDS");
 };
 
@@ -77,12 +76,15 @@ struct F4Side {
   uint32_t voff, step, nb;
   int chunk;
 
-  __device__ __forceinline__ void init(const void* codes, int64_t row0, int64_t all, int64_t K, int lane, int wave) {
+  // a descriptor over the tile's rows: offsets fit 32 bits whatever the matrix's size, and rows past the
+  // end read zeros
+  __device__ __forceinline__ void set_rows(const void* codes, int row0, int all, int64_t K) {
+    rc = rsrc(static_cast<const char*>(codes) + int64_t(row0) * (K / 2), uint32_t(min(all - row0, R)) * uint32_t(K / 2));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) rc[e] = __builtin_amdgcn_readfirstlane(rc[e]);
+  }
+  __device__ __forceinline__ void init(int64_t K, int lane, int wave) {
     nb = uint32_t(K / 32);
-    // a descriptor over this tile's rows: offsets fit 32 bits whatever the matrix's size, and rows
-    // past the end read zeros
-    const uint32_t rows = uint32_t(all - row0 < R ? all - row0 : R);
-    rc = rsrc(static_cast<const char*>(codes) + row0 * (K / 2), rows * uint32_t(K / 2));
     // wave-load wl = it * WAVES + wave covers rows 8 wl .. 8 wl + 7, 8 lanes a row; its swizzle depends
     // on the wave alone, since WAVES is even
     chunk = (lane & 7) ^ f4_swz(8 * wave + (lane >> 3));
@@ -106,26 +108,24 @@ __device__ __forceinline__ uint32_t f4_scale_at(int r, int u) {
 
 // A row's scales of a group of 8 stages, as the 17 aligned dwords that hold their 64 bytes.
 struct F4Scales {
-  __amdgpu_buffer_rsrc_t rs;
-  uint32_t first, nb;        // byte offset of the row's first scale in rs, and its scales
   uint32_t w[17];
+  uint32_t sh;               // bytes before the group's first in w[0]
+  int left;                  // the row's bytes from the group's first on, none for rows past the edge
 
-  // row r of the tile at row0 (r < rows) of a matrix of scales; other rows hold zeros
-  __device__ __forceinline__ void init(const void* scales, int64_t row0, uint32_t rows, uint32_t r, int64_t K) {
-    nb = uint32_t(K / 32);
-    const uintptr_t s = reinterpret_cast<uintptr_t>(scales) + uintptr_t(row0 * nb);
+  // stages kt .. kt + 7 of row r of the tile at row0, of a matrix of `all` rows; rows past the end hold zeros
+  template <int R>
+  __device__ __forceinline__ void load(const void* scales, int row0, int all, uint32_t r, int64_t K, int kt) {
+    const uint32_t nb = uint32_t(K / 32), rows = uint32_t(min(all - row0, R));
+    const uintptr_t s = reinterpret_cast<uintptr_t>(scales) + uintptr_t(int64_t(row0) * nb);
     const uint32_t low = uint32_t(s & 3);
     // the first and last word may hold up to 3 bytes beside the tile's scales; of a load that passes the
     // extent, the words inside arrive
-    rs = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(s & ~uintptr_t(3)), 0, int((low + rows * nb + 3) & ~3u),
-                                           kRsrcWord3);
-    first = low + r * nb;
-    if (r >= rows) nb = 0;
-  }
-  // stages kt .. kt + 7
-  __device__ __forceinline__ void load(int kt) {
-    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-    const uint32_t off = uint32_t(kt) * kF4Blocks < nb ? (first + uint32_t(kt) * kF4Blocks) & ~3u : kOOB;
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(s & ~uintptr_t(3)), 0,
+                                                                        int((low + rows * nb + 3) & ~3u), kRsrcWord3);
+    const uint32_t at = low + r * nb + uint32_t(kt) * kF4Blocks;
+    sh = at & 3;
+    left = r < rows ? int(nb) - kt * kF4Blocks : 0;
+    const uint32_t off = left > 0 ? at & ~3u : kOOB;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const u32x4 v = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, off + q * 16, 0, 0));
@@ -134,18 +134,16 @@ struct F4Scales {
     }
     w[16] = __builtin_amdgcn_raw_buffer_load_b32(rs, off + 64, 0, 0);
   }
-  // to row r of the cache at lds; CUT: the group that starts at stage kt passes the row's end
+  // to row r of the cache at lds; CUT: the group passes the row's end
   template <bool CUT>
-  __device__ __forceinline__ void store(uint32_t lds, int r, int kt) const {
-    const uint32_t sh = first & 3;
-    // what follows a row's last block is another row's scale, perhaps a NaN: the zero codes there get 2^-127
-    const int left = int(nb) - kt * kF4Blocks;
+  __device__ __forceinline__ void store(uint32_t lds, int r) const {
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       i32x2 d;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const uint32_t v = __builtin_amdgcn_alignbyte(w[2 * u + e + 1], w[2 * u + e], sh);
+        // what follows a row's last block is another row's scale, perhaps a NaN: the zero codes there get 2^-127
         const int n = left - 4 * (2 * u + e);                    // bytes of this dword within the row
         d[e] = int(!CUT || n >= 4 ? v : n <= 0 ? 0u : v & (0xFFFFFFFFu >> (32 - 8 * n)));
       }
@@ -154,14 +152,114 @@ struct F4Scales {
   }
 };
 
+// v, as a value that the compiler computes with where it stands: what follows from it is not kept in
+// registers through the loops around.
+__device__ __forceinline__ int here(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
 // The four scale bytes that lane group h needs of 8 consecutive ones, 2 ks + h in byte ks.
 __device__ __forceinline__ int f4_pick(uint32_t lo, uint32_t hi, uint32_t sel) {
   return int(__builtin_amdgcn_perm(hi, lo, sel));
 }
 
+// Stores a wave's blocks straight from the accumulators.  The MFMAs take the B fragment first, so lane l
+// of block (i, j) has row 32 i + l % 32 and in registers 4q .. 4q + 3 the columns
+// 32 j + 8 q + 4 (l / 32) + 0..3: 16 bytes of fp32 as they are; for bf16 the halves of the wave trade
+// pieces, so that each lane has 8 columns.  No LDS is used: the next tile's stages land there meanwhile.
+// Rows and columns past the edges go to offsets that the descriptors refuse, so that no branch stands
+// between the blocks and few accumulators are read ahead.
+
+// Keeps a block in its accumulator registers up to here: otherwise all of them are copied out together.
+__device__ __forceinline__ void f4_pin(f32x16& v) { asm volatile("" : "+a"(v)); }
+
+// Rows m .. m + 31 of a matrix of M rows of N elements of E bytes.
+template <int E>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t f4_rows(const void* c, int64_t m, int64_t M, int64_t N) {
+  const int rows = __builtin_amdgcn_readfirstlane(int(M - m < 0 ? 0 : M - m < 32 ? M - m : 32));
+  return __builtin_amdgcn_make_buffer_rsrc(static_cast<char*>(const_cast<void*>(c)) + m * N * E, 0, rows * int(N) * E, kRsrcWord3);
+}
+
+template <int TM, int TN>
+__device__ __forceinline__ void f4_store_bf16(const F4Args& g, f32x16 (&acc)[TM][TN], int m0, int n0, int lane) {
+  const int h = lane / 32, n = n0 + 8 * h;
+  const uint32_t off = uint32_t(lane % 32) * uint32_t(g.N) * 2 + uint32_t(n) * 2;
+  static_for<TM>([&](auto ic_) {
+    constexpr int i = decltype(ic_)::value;
+    const __amdgpu_buffer_rsrc_t rs = f4_rows<2>(g.c, m0 + 32 * i, g.M, g.N);
+    static_for<TN * 2>([&](auto jc) {
+      constexpr int j = decltype(jc)::value / 2, q = decltype(jc)::value % 2 * 2;
+      if constexpr (q == 0) f4_pin(acc[i][j]);
+      uint32_t w[2][2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int d = 0; d < 2; ++d) {
+          bf16x2 v;
+          v[0] = static_cast<__bf16>(acc[i][j][4 * (q + e) + 2 * d]);
+          v[1] = static_cast<__bf16>(acc[i][j][4 * (q + e) + 2 * d + 1]);
+          w[e][d] = __builtin_bit_cast(uint32_t, v);
+        }
+      const auto s0 = __builtin_amdgcn_permlane32_swap(w[0][0], w[1][0], false, false);
+      const auto s1 = __builtin_amdgcn_permlane32_swap(w[0][1], w[1][1], false, false);
+      const u32x4 o = {s0[0], s1[0], s0[1], s1[1]};
+      constexpr int c = j * 32 + 8 * q;
+      __builtin_amdgcn_raw_buffer_store_b128(o, rs, n + c < g.N ? off + c * 2 : kOOB, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  });
+}
+
+// fp32: added to C, or, with K split, stored to the split's plane, which the reduce kernel launched next
+// on the stream adds up in split order.  Old values are loaded two blocks ahead.
+template <bool ADD, int TM, int TN>
+__device__ __forceinline__ void f4_store_f32(const F4Args& g, float* c, f32x16 (&acc)[TM][TN], int m0, int n0, int lane) {
+  const int n = n0 + 4 * (lane / 32);
+  const uint32_t off = uint32_t(lane % 32) * uint32_t(g.N) * 4 + uint32_t(n) * 4;
+  constexpr int TB = TN / 2;                                     // batches of two blocks in a row of blocks
+  u32x4 old[2][2][4];
+  auto at = [&](int j, int q) { return n + j * 32 + 8 * q < g.N ? off + (j * 32 + 8 * q) * 4 : kOOB; };
+  auto load = [&](int b, u32x4 (&o)[2][4]) {
+    const __amdgpu_buffer_rsrc_t rs = f4_rows<4>(c, m0 + 32 * (b / TB), g.M, g.N);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        o[j][q] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, at(b % TB * 2 + j, q), 0, 0));
+  };
+  if constexpr (ADD) load(0, old[0]);
+  __builtin_amdgcn_sched_barrier(0);
+  static_for<TM * TB>([&](auto bc) {
+    constexpr int b = decltype(bc)::value, i = b / TB;
+    if constexpr (ADD && b + 1 < TM * TB) load(b + 1, old[(b + 1) & 1]);
+    __builtin_amdgcn_sched_barrier(0);
+    const __amdgpu_buffer_rsrc_t rs = f4_rows<4>(c, m0 + 32 * i, g.M, g.N);
+    static_for<8>([&](auto jc) {
+      constexpr int jj = decltype(jc)::value / 4, j = b % TB * 2 + jj, q = decltype(jc)::value % 4;
+      if constexpr (q == 0) f4_pin(acc[i][j]);
+      u32x4 v;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float x = acc[i][j][4 * q + e];
+        if constexpr (ADD) x += __uint_as_float(old[b & 1][jj][q][e]);
+        v[e] = __float_as_uint(x);
+      }
+      __builtin_amdgcn_raw_buffer_store_b128(v, rs, at(j, q), 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  });
+}
+
+// What a workgroup computes at a time: a tile over the stages [kt0, kt1).
+struct F4Item { int m0, n0, kt0, kt1, split; };
+
+// A workgroup takes several items, and the stages of one follow those of the item before without a
+// gap: during an item's last two stages the loads are the next one's, so only the results' stores
+// stand between the matrix instructions of two items.
 template <int BM, int BN, int WGM, int WGN, bool ACC>
 __global__ void __launch_bounds__(WGM * WGN * 64) gemm_f4(F4Args g) {
-  using L = F4Layout<BM, BN, WGM, WGN, ACC>;
+  using L = F4Layout<BM, BN, WGM, WGN>;
   constexpr int WAVES = WGM * WGN, WM = BM / WGM, WN = BN / WGN, TM = WM / 32, TN = WN / 32;
   using SA = F4Side<BM, WAVES>;
   using SB = F4Side<BN, WAVES>;
@@ -172,29 +270,29 @@ __global__ void __launch_bounds__(WGM * WGN * 64) gemm_f4(F4Args g) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WGN, wn = wave % WGN;
 
-  const int tiles_m = int((g.M + BM - 1) / BM), tiles_n = int((g.N + BN - 1) / BN);
-  const int t = xcd_remap(blockIdx.x, tiles_m * tiles_n);
-  const int group = t / (8 * tiles_n), first_m = group * 8, gsz = min(tiles_m - first_m, 8);
-  const int tm = first_m + (t % (8 * tiles_n)) % gsz, tn = (t % (8 * tiles_n)) / gsz;
-  const int m0 = tm * BM, n0 = tn * BN;
-  const int split = blockIdx.z;
+  // Consecutive workgroups go to the 8 XCDs in turn.  Each XCD takes a contiguous range of the items,
+  // its workgroups side by side in it, so that what runs there at a time shares rows in its L2: 8 tiles
+  // down, then across.
+  const int tiles_m = int((g.M + BM - 1) / BM), tiles_n = int((g.N + BN - 1) / BN), tiles = tiles_m * tiles_n;
   const int nkt = int((g.K + kF4StageK - 1) / kF4StageK);
-  const int kt0 = ACC ? split * g.kt_per_split : 0;
-  const int kt1 = ACC ? min(nkt, kt0 + g.kt_per_split) : nkt;
-
-  SA a;
-  SB b;
-  a.init(g.a, m0, g.M, g.K, lane, wave);
-  b.init(g.b, n0, g.N, g.K, lane, wave);
-  // row q of A's then B's rows belongs to thread q % threads; every wave's rows are of one operand
-  F4Scales sc[L::kRows];
-  const uint32_t rows_a = uint32_t(min(g.M - m0, int64_t(BM))), rows_b = uint32_t(min(g.N - n0, int64_t(BN)));
-#pragma unroll
-  for (int n = 0; n < L::kRows; ++n) {
-    const int q0 = n * WAVES * 64 + wave * 64;
-    if (q0 < BM) sc[n].init(g.sa, m0, rows_a, q0 + lane, g.K);
-    else sc[n].init(g.sb, n0, rows_b, q0 - BM + lane, g.K);
-  }
+  auto item = [&](int x) {
+    F4Item it;
+    it.split = ACC ? x / tiles : 0;
+    const int t = ACC ? x % tiles : x;
+    const int group = t / (8 * tiles_n), first_m = group * 8, gsz = min(tiles_m - first_m, 8);
+    it.m0 = (first_m + (t % (8 * tiles_n)) % gsz) * BM;
+    it.n0 = (t % (8 * tiles_n)) / gsz * BN;
+    it.kt0 = ACC ? it.split * g.kt_per_split : 0;
+    it.kt1 = ACC ? min(nkt, it.kt0 + g.kt_per_split) : nkt;
+    it.m0 = __builtin_amdgcn_readfirstlane(it.m0);
+    it.n0 = __builtin_amdgcn_readfirstlane(it.n0);
+    return it;
+  };
+  const int items = tiles * (ACC ? g.splits : 1), xcd = blockIdx.x % kXCD;
+  const int per = items / kXCD, rem = items % kXCD;
+  const int end = (xcd + 1) * per + min(xcd + 1, rem), stride = (int(gridDim.x) - xcd + kXCD - 1) / kXCD;
+  int x = xcd * per + min(xcd, rem) + int(blockIdx.x) / kXCD;
+  if (x >= end) return;
 
   // fragment addresses: row r's chunk 2 ks + h sits in slot (2 ks + h) ^ swz(r) of the row's eight
   const int fr = lane & 31, h = lane >> 5;
@@ -202,36 +300,53 @@ __global__ void __launch_bounds__(WGM * WGN * 64) gemm_f4(F4Args g) {
   const uint32_t fb0 = lds + BM * kF4Row + uint32_t(wn * WN + fr) * kF4Row + uint32_t((h ^ f4_swz(fr)) << 4);
   const uint32_t sel = h ? 0x07050301u : 0x06040200u;
 
-  auto load_scales = [&](int kt) {
-#pragma unroll
-    for (int n = 0; n < L::kRows; ++n) sc[n].load(kt);
-  };
-  auto store_scales = [&](int kt) {
+  // row q of A's then B's rows belongs to thread q % threads; every wave's rows are of one operand
+  F4Scales sc[L::kRows];
+  bool cut = false;                                              // the group held passes the rows' end
+  auto load_scales = [&](const F4Item& it, int kt) {
+    const int l = here(lane);
 #pragma unroll
     for (int n = 0; n < L::kRows; ++n) {
-      const uint32_t c = lds + L::kCache;
-      if (kt * kF4Blocks + 8 * kF4Blocks <= int(g.K / 32)) sc[n].template store<false>(c, n * WAVES * 64 + tid, kt);
-      else sc[n].template store<true>(c, n * WAVES * 64 + tid, kt);
+      const int q0 = n * WAVES * 64 + wave * 64;
+      if (q0 < BM) sc[n].template load<BM>(g.sa, it.m0, int(g.M), q0 + l, g.K, kt);
+      else sc[n].template load<BN>(g.sb, it.n0, int(g.N), q0 - BM + l, g.K, kt);
+    }
+    cut = (kt + 8) * kF4Blocks > int(g.K / 32);
+  };
+  auto store_scales = [&]() {
+    const int t = here(tid);
+#pragma unroll
+    for (int n = 0; n < L::kRows; ++n) {
+      if (cut) sc[n].template store<true>(lds + L::kCache, n * WAVES * 64 + t);
+      else sc[n].template store<false>(lds + L::kCache, n * WAVES * 64 + t);
     }
   };
-  auto read_scales = [&](int r, int kt) { return lds_read<i32x2>(lds + L::kCache + f4_scale_at(r, (kt - kt0) & 7)); };
+  auto read_scales = [&](int r, int u) { return lds_read<i32x2>(lds + L::kCache + f4_scale_at(r, u)); };
   auto make_scales = [&](i32x2 w) -> int { return f4_pick(w[0], w[1], sel); };
   const int ar = wm * WM + fr, br = BM + wn * WN + fr;          // this lane's first fragment rows, A's and B's
 
   f32x16 acc[TM][TN];
-#pragma unroll
-  for (int i = 0; i < TM; ++i)
-#pragma unroll
-    for (int j = 0; j < TN; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
 
-  // One stage, in slot P = (kt - kt0) % 2.  No branch stands inside (the loads past the last stage
-  // read out of range, the reads past it are not used): the fixed order below holds within a basic block.
+  // the operands of the item being loaded, its next stage and its end
+  SA a;
+  SB b;
+  a.init(g.K, lane, wave);
+  b.init(g.K, lane, wave);
+  int lkt = 0, lend = 0;
+  auto load_from = [&](const F4Item& it) {
+    a.set_rows(g.a, it.m0, int(g.M), g.K);
+    b.set_rows(g.b, it.n0, int(g.N), g.K);
+    lkt = it.kt0;
+    lend = it.kt1;
+  };
+
+  // One stage, in slot P.  u: the next stage's place in its scale group.  No branch stands inside (loads
+  // past the last stage read out of range, reads past it are not used): the fixed order below holds
+  // within a basic block.
   constexpr int kReads = TM + TN, kMfma = TM * TN, kLoads = SA::kLoads + SB::kLoads;
   i32x4 fa[2][TM], fb[2][TN];
   int sca[TM], scb[TN];
-  auto stage = [&](int kt, auto par) {
+  auto stage = [&](int u, auto par) __attribute__((always_inline)) {
     constexpr int P = decltype(par)::value;
     const uint32_t cur = P * L::kSlot, nxt = L::kSlot - cur;
     i32x2 na[TM], nb[TN];
@@ -243,19 +358,20 @@ __global__ void __launch_bounds__(WGM * WGN * 64) gemm_f4(F4Args g) {
         wait_lgkm0();
         wait_vmcnt<0>();
         bare_barrier();
-        oa = kt + 2 < kt1 ? a.at(kt + 2) : kOOB;
-        ob = kt + 2 < kt1 ? b.at(kt + 2) : kOOB;
+        oa = lkt < lend ? a.at(lkt) : kOOB;
+        ob = lkt < lend ? b.at(lkt) : kOOB;
+        ++lkt;
       }
       const uint32_t ra = (ks == 3 ? fa0 + nxt : (fa0 ^ uint32_t((ks + 1) << 5)) + cur);
       const uint32_t rb = (ks == 3 ? fb0 + nxt : (fb0 ^ uint32_t((ks + 1) << 5)) + cur);
       // side operations of this step: fragment reads of the next one; in the last step also the next
-      // stage's scales and the loads of the stage after it
+      // stage's scales and the loads of the stage after that
       auto read = [&](auto nc) {
         constexpr int n = decltype(nc)::value;
         if constexpr (n < TN) fb[p ^ 1][n] = lds_read<i32x4>(rb + n * 32 * kF4Row);
         else if constexpr (n < kReads) fa[p ^ 1][n - TN] = lds_read<i32x4>(ra + (n - TN) * 32 * kF4Row);
-        else if constexpr (ks == 3 && n < kReads + TN) nb[n - kReads] = read_scales(br + (n - kReads) * 32, kt + 1);
-        else if constexpr (ks == 3 && n < 2 * kReads) na[n - kReads - TN] = read_scales(ar + (n - kReads - TN) * 32, kt + 1);
+        else if constexpr (ks == 3 && n < kReads + TN) nb[n - kReads] = read_scales(br + (n - kReads) * 32, u);
+        else if constexpr (ks == 3 && n < 2 * kReads) na[n - kReads - TN] = read_scales(ar + (n - kReads - TN) * 32, u);
       };
       auto load = [&](auto nc) {
         constexpr int n = decltype(nc)::value;
@@ -267,8 +383,8 @@ __global__ void __launch_bounds__(WGM * WGN * 64) gemm_f4(F4Args g) {
       static_for<kMfma>([&](auto mc) {
         // odd rows run j backwards, so every MFMA shares an operand with the one before it
         constexpr int n = decltype(mc)::value, i = n / TN, j = (i & 1) ? TN - 1 - n % TN : n % TN;
-        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f4_operand(fb[p][j]), f4_operand(fa[p][i]), acc[i][j],
-                                                                    kF4Fmt, kF4Fmt, ks, scb[j], ks, sca[i]);
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f4_operand(fb[p][j]), f4_operand(fa[p][i]),
+                                                                    acc[i][j], kF4Fmt, kF4Fmt, ks, scb[j], ks, sca[i]);
         static_for<kReadsPer>([&](auto rc) { read(ic<n * kReadsPer + decltype(rc)::value>{}); });
         static_for<kLoadsPer>([&](auto rc) { load(ic<n * kLoadsPer + decltype(rc)::value>{}); });
         __builtin_amdgcn_sched_barrier(0);
@@ -280,58 +396,87 @@ __global__ void __launch_bounds__(WGM * WGN * 64) gemm_f4(F4Args g) {
     for (int i = 0; i < TM; ++i) sca[i] = make_scales(na[i]);
   };
 
-  if (kt0 < kt1) {
-    auto load_stage = [&](int kt, uint32_t slot) {
-      const uint32_t oa = kt < kt1 ? a.at(kt) : kOOB, ob = kt < kt1 ? b.at(kt) : kOOB;
+  F4Item cur = item(x);
+  auto load_stage = [&](uint32_t slot) {
+    const uint32_t oa = lkt < lend ? a.at(lkt) : kOOB, ob = lkt < lend ? b.at(lkt) : kOOB;
+    ++lkt;
 #pragma unroll
-      for (int it = 0; it < SA::kLoads; ++it) a.load(slot, oa, it, wave);
+    for (int it = 0; it < SA::kLoads; ++it) a.load(slot, oa, it, wave);
 #pragma unroll
-      for (int it = 0; it < SB::kLoads; ++it) b.load(slot + BM * kF4Row, ob, it, wave);
-    };
-    load_scales(kt0);
-    load_stage(kt0, lds);
-    wait_vmcnt<0>();
-    load_stage(kt0 + 1, lds + L::kSlot);
-    store_scales(kt0);
-    wait_lgkm0();
-    bare_barrier();
+    for (int it = 0; it < SB::kLoads; ++it) b.load(slot + BM * kF4Row, ob, it, wave);
+  };
+  load_scales(cur, cur.kt0);
+  load_from(cur);
+  load_stage(lds);
+  wait_vmcnt<0>();
+  load_stage(lds + L::kSlot);
+  store_scales();
+  wait_lgkm0();
+  bare_barrier();
 #pragma unroll
-    for (int j = 0; j < TN; ++j) fb[0][j] = lds_read<i32x4>(fb0 + j * 32 * kF4Row);
+  for (int j = 0; j < TN; ++j) fb[0][j] = lds_read<i32x4>(fb0 + j * 32 * kF4Row);
 #pragma unroll
-    for (int i = 0; i < TM; ++i) fa[0][i] = lds_read<i32x4>(fa0 + i * 32 * kF4Row);
+  for (int i = 0; i < TM; ++i) fa[0][i] = lds_read<i32x4>(fa0 + i * 32 * kF4Row);
 #pragma unroll
-    for (int j = 0; j < TN; ++j) scb[j] = make_scales(read_scales(br + j * 32, kt0));
+  for (int j = 0; j < TN; ++j) scb[j] = make_scales(read_scales(br + j * 32, 0));
 #pragma unroll
-    for (int i = 0; i < TM; ++i) sca[i] = make_scales(read_scales(ar + i * 32, kt0));
+  for (int i = 0; i < TM; ++i) sca[i] = make_scales(read_scales(ar + i * 32, 0));
 
-    // an odd last stage is followed by one of zeros: with one exit the accumulators stay in place
-    for (int kt = kt0; kt < kt1; kt += 2) {
-      const int u = (kt - kt0) & 7;
-      if (u == 0) load_scales(kt + 8);
-      stage(kt, ic<0>{});
-      if (u == 6) {
-        // the group's last scales are in registers once every wave is here; the next group's landed long
-        // ago and is read after the coming stage's barrier
+  for (;;) {
+    x += stride;
+    const bool more = x < end;
+    const F4Item nx = item(more ? x : x - stride);
+    // Stages in pairs: an odd last one is followed by one of zeros (an empty K is a pair of zeros), so
+    // that the accumulators stay in place.
+    const int nk = max(2, (cur.kt1 - cur.kt0 + 1) & ~1);
+    // a zero that is made here: a constant one is kept in registers of its own and copied
+    const float zero = __int_as_float(here(0));
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = zero;
+    for (int k = 0; k < nk; k += 2) {
+      const bool last = k + 2 == nk;
+      if ((k & 7) == 0) {
+        if (k + 8 < nk) load_scales(cur, cur.kt0 + k + 8);
+        else load_scales(nx, nx.kt0);
+      }
+      if (last) {
+        load_from(nx);
+        if (!more) lend = lkt;
+      }
+      stage((k + 1) & 7, ic<0>{});
+      if (last || (k & 7) == 6) {
+        // the group's last scales are in registers once every wave is here; those of the next landed
+        // before the stage's barrier, and are read after the coming stage's
         wait_lgkm0();
         bare_barrier();
-        store_scales(kt + 2);
+        store_scales();
       }
-      stage(kt + 1, ic<1>{});
+      stage(last ? 0 : (k + 2) & 7, ic<1>{});
     }
+    const int l = here(lane);
+    const int m = cur.m0 + wm * WM, n = cur.n0 + wn * WN;
+    if constexpr (!ACC) f4_store_bf16<TM, TN>(g, acc, m, n, l);
+    else if (g.splits == 1) f4_store_f32<true, TM, TN>(g, static_cast<float*>(g.c), acc, m, n, l);
+    else f4_store_f32<false, TM, TN>(g, g.ws + int64_t(cur.split) * g.M * g.N, acc, m, n, l);
+    if (!more) break;
+    cur = nx;
   }
-  wait_vmcnt<0>();
-  __syncthreads();    // every wave is past its last operand read: the slots become epilogue space
-  store_tile<WM, WN, TM, TN, ACC>(g, acc, smem, m0 + wm * WM, n0 + wn * WN, split, lane, wave);
+  wait_vmcnt<0>();   // loads past the end still write zeros to LDS
 }
 
 template <int BM, int BN, int WGM, int WGN, bool ACC>
 int launch_f4(hipStream_t st, const F4Args& g) {
-  constexpr int lds = F4Layout<BM, BN, WGM, WGN, ACC>::kLds;
+  constexpr int lds = F4Layout<BM, BN, WGM, WGN>::kLds;
+  constexpr int kResident = 256 * (160 * 1024 / lds);            // workgroups on the 256 CUs at a time
   auto kfn = gemm_f4<BM, BN, WGM, WGN, ACC>;
   static std::atomic<uint64_t> attr{0};
   if (smem_attr_once(reinterpret_cast<const void*>(kfn), lds, attr)) return -5;
-  const int64_t tiles = (g.M + BM - 1) / BM * ((g.N + BN - 1) / BN);
-  hipLaunchKernelGGL(kfn, dim3(unsigned(tiles), 1, ACC ? g.splits : 1), dim3(WGM * WGN * 64), lds, st, g);
+  const int64_t items = (g.M + BM - 1) / BM * ((g.N + BN - 1) / BN) * (ACC ? g.splits : 1);
+  hipLaunchKernelGGL(kfn, dim3(unsigned(items < kResident ? items : kResident)), dim3(WGM * WGN * 64), lds, st, g);
   return hipGetLastError() == hipSuccess ? 0 : -5;
 }
 

@@ -10,7 +10,7 @@ namespace {
 
 constexpr int64_t kMaxExtent = int64_t(1) << 31;
 constexpr int64_t kMaxTiles = int64_t(1) << 31;        // workgroups of one launch
-constexpr int64_t kMaxK = int64_t(1) << 23;            // contraction extent: a tile's rows stay within 32-bit offsets
+constexpr int64_t kMaxFeatures = int64_t(1) << 23;     // rows of a tile stay within 32-bit offsets
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -18,7 +18,7 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 int check_product(int64_t T, int64_t in, int64_t out, int64_t k) {
   if (T < 0 || in < 0 || out < 0) return SL_EINVAL;
   if (T >= kMaxExtent || in >= kMaxExtent || out >= kMaxExtent) return SL_ESHAPE;
-  if (in % 8 || out % 8 || k % 32 || k > kMaxK) return SL_ESHAPE;
+  if (in % 8 || out % 8 || k % 32 || in > kMaxFeatures || out > kMaxFeatures || k > kMaxFeatures) return SL_ESHAPE;
   return SL_OK;
 }
 
@@ -43,9 +43,8 @@ int product(void* stream, const uint8_t* a, const uint8_t* sa, const uint8_t* b,
   if (st) return st;
   F4Args g{};
   g.a = a; g.b = b; g.sa = sa; g.sb = sb; g.c = c;
-  g.M = M; g.N = N; g.K = K; g.ldc = N;
+  g.M = M; g.N = N; g.K = K;
   g.splits = 1;
-  g.alpha = 1.0f;
   g.cfg = pick_config(M, N);
   return f4_gemm(static_cast<hipStream_t>(stream), g) == 0 ? SL_OK : SL_EHIP;
 }
@@ -55,7 +54,7 @@ int product(void* stream, const uint8_t* a, const uint8_t* sa, const uint8_t* b,
 // stages (an even number) to a split and at most 16 splits.
 F4Args wgrad_plan(int64_t T, int64_t in, int64_t out) {
   F4Args g{};
-  g.M = out; g.N = in; g.K = T; g.ldc = in;
+  g.M = out; g.N = in; g.K = T;
   const int64_t t256 = ntiles(out, in, 256, 256), t128 = ntiles(out, in, 256, 128), nkt = (T + kF4StageK - 1) / kF4StageK;
   const int forced = block_scaled_config();
   g.cfg = forced >= 0 ? forced : (t256 <= 144 && t128 >= 240 && t128 <= 288) ? 2 : 0;
@@ -68,7 +67,6 @@ F4Args wgrad_plan(int64_t T, int64_t in, int64_t out) {
   per += per & 1;                        // the kernel starts at an even stage
   g.kt_per_split = int(per);
   g.splits = int((nkt + per - 1) / per);
-  g.alpha = 1.0f;
   return g;
 }
 

@@ -119,9 +119,10 @@ def test_product_validation(name, dims):
     assert f(None, A, A, A, A, A, 16, *dims(48, 64)) == ESHAPE                    # contracted % 32
     assert f(None, A, A, A, A, A, 16, *dims(64, 12)) == ESHAPE                    # other % 8
     assert f(None, A, A, A, A, A, 16, *dims(1 << 24, 64)) == ESHAPE
+    assert f(None, A, A, A, A, A, 16, *dims(64, 1 << 24)) == ESHAPE
     assert f(None, A, A, A, A, A, -1, *dims(64, 64)) == EINVAL
     assert f(None, A, A, A, A, A, 1 << 31, *dims(64, 64)) == ESHAPE
-    assert f(None, A, A, A, A, A, (1 << 31) - 1, *dims(64, (1 << 31) - 8)) == ESHAPE   # too many tiles
+    assert f(None, A, A, A, A, A, (1 << 31) - 1, *dims(64, 1 << 23)) == ESHAPE        # too many tiles
     assert f(None, A, A, A, None, A, 16, *dims(64, 64)) == EINVAL
     assert f(None, MIS, A, A, A, A, 16, *dims(64, 64)) == EALIGN
     assert f(None, A, A, MIS, A, A, 16, *dims(64, 64)) == EALIGN
