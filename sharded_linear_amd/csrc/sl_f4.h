@@ -44,6 +44,14 @@ constexpr int kF4StageK = 256;                  // k elements of one stage
 int f4_gemm(hipStream_t st, const F4Args& g);
 int f4_accum(hipStream_t st, const F4Args& g);
 
+// Y[T][N] = X . W^T for few rows T: X bf16 (xs null) or MXFP4, W MXFP4, both blocked along K; T below 2^20.
+struct F4RowsArgs {
+  const void *x, *xs, *w, *ws;
+  void* y;
+  int64_t T, N, K;
+};
+int f4_rows(hipStream_t st, const F4RowsArgs& g);
+
 // The SL_TUNE_F8_CONFIG knob: a forced tile configuration of the block-scaled products, or -1 (sl_gemm.hip).
 int block_scaled_config();
 // main_grad[M][N] += the planes of ws in split order (sl_gemm.hip).

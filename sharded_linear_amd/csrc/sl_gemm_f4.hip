@@ -271,17 +271,19 @@ __global__ void __launch_bounds__(WGM * WGN * 64) gemm_f4(F4Args g) {
   const int wm = wave / WGN, wn = wave % WGN;
 
   // Consecutive workgroups go to the 8 XCDs in turn.  Each XCD takes a contiguous range of the items,
-  // its workgroups side by side in it, so that what runs there at a time shares rows in its L2: 8 tiles
-  // down, then across.
+  // its workgroups side by side in it, so that what runs there at a time shares rows in its L2: 6 tiles
+  // down, then across (over 8 down, 2-3 % shorter with bf16 results and 5-11 % in accumulating 8192 x 8192;
+  // 4 and 16 down are no better).
+  constexpr int kDown = 6;
   const int tiles_m = int((g.M + BM - 1) / BM), tiles_n = int((g.N + BN - 1) / BN), tiles = tiles_m * tiles_n;
   const int nkt = int((g.K + kF4StageK - 1) / kF4StageK);
   auto item = [&](int x) {
     F4Item it;
     it.split = ACC ? x / tiles : 0;
     const int t = ACC ? x % tiles : x;
-    const int group = t / (8 * tiles_n), first_m = group * 8, gsz = min(tiles_m - first_m, 8);
-    it.m0 = (first_m + (t % (8 * tiles_n)) % gsz) * BM;
-    it.n0 = (t % (8 * tiles_n)) / gsz * BN;
+    const int group = t / (kDown * tiles_n), first_m = group * kDown, gsz = min(tiles_m - first_m, kDown);
+    it.m0 = (first_m + (t % (kDown * tiles_n)) % gsz) * BM;
+    it.n0 = (t % (kDown * tiles_n)) / gsz * BN;
     it.kt0 = ACC ? it.split * g.kt_per_split : 0;
     it.kt1 = ACC ? min(nkt, it.kt0 + g.kt_per_split) : nkt;
     it.m0 = __builtin_amdgcn_readfirstlane(it.m0);

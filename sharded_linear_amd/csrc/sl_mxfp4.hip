@@ -33,6 +33,9 @@ int pick_config(int64_t M, int64_t N) {
   return ntiles(M, N, 256, 256) >= 200 ? 0 : 1;
 }
 
+// Rows up to which a product reads the weight directly.
+constexpr int64_t kFewRows = 64, kFewRowsBf16 = 256;
+
 // C[M][N] = A . B^T (bf16) over K
 int product(void* stream, const uint8_t* a, const uint8_t* sa, const uint8_t* b, const uint8_t* sb, void* c, int64_t M,
             int64_t N, int64_t K) {
@@ -41,6 +44,11 @@ int product(void* stream, const uint8_t* a, const uint8_t* sa, const uint8_t* b,
   if (!aligned16(c) || !aligned16(a) || !aligned16(b)) return SL_EALIGN;
   const int st = check_grid(M, N);
   if (st) return st;
+  if (M <= kFewRows && block_scaled_config() < 0) {
+    const F4RowsArgs r{a, sa, b, sb, c, M, N, K};
+    // an empty K may come without scales, and X without scales is bf16
+    return f4_rows(static_cast<hipStream_t>(stream), K ? r : F4RowsArgs{c, c, c, c, c, M, N, 0}) == 0 ? SL_OK : SL_EHIP;
+  }
   F4Args g{};
   g.a = a; g.b = b; g.sa = sa; g.sb = sb; g.c = c;
   g.M = M; g.N = N; g.K = K;
@@ -140,7 +148,7 @@ extern "C" int sl_linear_wgrad_accum_mxfp4(void* stream, const uint8_t* dYqT, co
 // ---- bf16 activations with MXFP4 weights ------------------------------------------------------
 
 extern "C" size_t sl_mxfp4w_fwd_workspace_bytes(int64_t T, int64_t in, int64_t out) {
-  if (check_product(T, in, out, in) || T == 0 || in == 0 || out == 0) return 0;
+  if (check_product(T, in, out, in) || T <= kFewRowsBf16 || in == 0 || out == 0) return 0;
   return size_t(out) * size_t(in) * 2;
 }
 
@@ -156,6 +164,8 @@ extern "C" int sl_linear_fwd_mxfp4w(void* stream, const void* X, const uint8_t* 
   if (T == 0 || out == 0) return SL_OK;
   if (!Y || (in > 0 && (!X || !Wq || !Ws))) return SL_EINVAL;
   if (!aligned16(X) || !aligned16(Wq) || !aligned16(Y)) return SL_EALIGN;
+  if (T <= kFewRowsBf16)
+    return f4_rows(static_cast<hipStream_t>(stream), F4RowsArgs{X, nullptr, Wq, Ws, Y, T, out, in}) == 0 ? SL_OK : SL_EHIP;
   const size_t need = sl_mxfp4w_fwd_workspace_bytes(T, in, out);
   if (need && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return SL_EWORKSPACE;
   if (in > 0 && f4_dequantize(static_cast<hipStream_t>(stream), Wq, Ws, workspace, out, in)) return SL_EHIP;
