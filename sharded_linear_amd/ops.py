@@ -25,6 +25,8 @@ def _stream(dev):
 
 
 def _want(t, name, dtype, shape, dev):
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
     if t.dtype != dtype:
@@ -349,14 +351,24 @@ def sl_linear_dgrad_nvfp4w(dY, Wm, w_scale: float, dX=None):
 # ---- MXFP4 --------------------------------------------------------------------------------------
 # Matrices [r, k] as packed codes [r, k/2] and scales [r, k/32] (uint8), k a multiple of 32.
 
+# A token's forward runs a few microseconds, so the calls below take the short way: pointers as ints, the
+# stream's handle without a Stream object, and no allocation beyond the result.
+
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
 def _launch(name, dev, *args):
     """Calls the entry point on the current stream of ``dev``, with ``dev`` current."""
     fn = getattr(lib(), name)
-    if dev.index is None or dev.index == torch.cuda.current_device():
-        st = fn(_stream(dev), *args)
+    if dev.index == torch.cuda.current_device():
+        st = fn(_raw_stream(dev.index), *args)
     else:
         with torch.cuda.device(dev):
-            st = fn(_stream(dev), *args)
+            st = fn(_raw_stream(dev.index), *args)
     if st:
         check(name, st)
 
@@ -364,11 +376,13 @@ def _launch(name, dev, *args):
 def _scratch(dev, need, workspace):
     """(tensor, bytes) of the caller's workspace, or of one of this library's: the stream's shared one, or
     under graph capture a new one, which belongs to the graph alone."""
-    if workspace is None and need:
+    if workspace is None:
+        if not need:
+            return None, 0
         with torch.cuda.device(dev):
             workspace = (torch.empty(need, dtype=U8, device=dev) if torch.cuda.is_current_stream_capturing()
                          else wgrad_workspace(dev, need))
-    return workspace, workspace.numel() * workspace.element_size() if workspace is not None else 0
+    return workspace, workspace.numel() * workspace.element_size()
 
 
 def _want_mxfp4(q, s, names, dev):
@@ -424,8 +438,8 @@ def sl_mxfp4_quantize(x, rows=True, cols=True, seed=None, out=None):
         _want(offset, "seed", torch.int64, offset.shape, dev)
     elif seed is not None:
         key = int(seed) & 0xFFFFFFFFFFFFFFFF
-    _launch("sl_mxfp4_quantize", dev, _ptr(x), R, C, _ptr(qr), _ptr(sr), _ptr(qc), _ptr(sc),
-            int(seed is not None), key, _ptr(offset))
+    _launch("sl_mxfp4_quantize", dev, _addr(x), R, C, _addr(qr), _addr(sr), _addr(qc), _addr(sc),
+            int(seed is not None), key, _addr(offset))
     return qr, sr, qc, sc
 
 
@@ -436,7 +450,7 @@ def sl_mxfp4_dequantize(q, s, out=None):
     if out is None:
         out = torch.empty((R, K), dtype=BF16, device=dev)
     _want(out, "out", BF16, (R, K), dev)
-    _launch("sl_mxfp4_dequantize", dev, _ptr(q), _ptr(s), _ptr(out), R, K)
+    _launch("sl_mxfp4_dequantize", dev, _addr(q), _addr(s), _addr(out), R, K)
     return out
 
 
@@ -448,8 +462,9 @@ def sl_linear_fwd_mxfp4(Xq, Xs, Wq, Ws, Y=None):
     _same(n_in, k, "the contracted extents of Xq and Wq")
     if Y is None:
         Y = torch.empty((T, n_out), dtype=BF16, device=dev)
-    _want(Y, "Y", BF16, (T, n_out), dev)
-    _launch("sl_linear_fwd_mxfp4", dev, _ptr(Xq), _ptr(Xs), _ptr(Wq), _ptr(Ws), _ptr(Y), T, n_in, n_out)
+    else:
+        _want(Y, "Y", BF16, (T, n_out), dev)
+    _launch("sl_linear_fwd_mxfp4", dev, _addr(Xq), _addr(Xs), _addr(Wq), _addr(Ws), _addr(Y), T, n_in, n_out)
     return Y
 
 
@@ -461,8 +476,9 @@ def sl_linear_dgrad_mxfp4(dYq, dYs, WqT, WsT, dX=None):
     _same(n_out, k, "the contracted extents of dYq and WqT")
     if dX is None:
         dX = torch.empty((T, n_in), dtype=BF16, device=dev)
-    _want(dX, "dX", BF16, (T, n_in), dev)
-    _launch("sl_linear_dgrad_mxfp4", dev, _ptr(dYq), _ptr(dYs), _ptr(WqT), _ptr(WsT), _ptr(dX), T, n_in, n_out)
+    else:
+        _want(dX, "dX", BF16, (T, n_in), dev)
+    _launch("sl_linear_dgrad_mxfp4", dev, _addr(dYq), _addr(dYs), _addr(WqT), _addr(WsT), _addr(dX), T, n_in, n_out)
     return dX
 
 
@@ -478,8 +494,8 @@ def sl_linear_wgrad_accum_mxfp4(dYqT, dYsT, XqT, XsT, main_grad, workspace=None)
     _same(T, k, "the contracted extents of dYqT and XqT")
     _want(main_grad, "main_grad", F32, (n_out, n_in), dev)
     workspace, nbytes = _scratch(dev, sl_mxfp4_wgrad_workspace_bytes(T, n_in, n_out), workspace)
-    _launch("sl_linear_wgrad_accum_mxfp4", dev, _ptr(dYqT), _ptr(dYsT), _ptr(XqT), _ptr(XsT), _ptr(main_grad), T, n_in,
-            n_out, _ptr(workspace), nbytes)
+    _launch("sl_linear_wgrad_accum_mxfp4", dev, _addr(dYqT), _addr(dYsT), _addr(XqT), _addr(XsT), _addr(main_grad), T, n_in,
+            n_out, _addr(workspace), nbytes)
     return main_grad
 
 
@@ -495,9 +511,10 @@ def sl_linear_fwd_mxfp4w(X, Wq, Ws, Y=None, workspace=None):
     _want(X, "X", BF16, (T, n_in), dev)
     if Y is None:
         Y = torch.empty((T, n_out), dtype=BF16, device=dev)
-    _want(Y, "Y", BF16, (T, n_out), dev)
+    else:
+        _want(Y, "Y", BF16, (T, n_out), dev)
     workspace, nbytes = _scratch(dev, sl_mxfp4w_fwd_workspace_bytes(T, n_in, n_out), workspace)
-    _launch("sl_linear_fwd_mxfp4w", dev, _ptr(X), _ptr(Wq), _ptr(Ws), _ptr(Y), T, n_in, n_out, _ptr(workspace), nbytes)
+    _launch("sl_linear_fwd_mxfp4w", dev, _addr(X), _addr(Wq), _addr(Ws), _addr(Y), T, n_in, n_out, _addr(workspace), nbytes)
     return Y
 
 
@@ -513,8 +530,9 @@ def sl_linear_dgrad_mxfp4w(dY, Wq, Ws, dX=None, workspace=None):
     _want(dY, "dY", BF16, (T, n_out), dev)
     if dX is None:
         dX = torch.empty((T, n_in), dtype=BF16, device=dev)
-    _want(dX, "dX", BF16, (T, n_in), dev)
+    else:
+        _want(dX, "dX", BF16, (T, n_in), dev)
     workspace, nbytes = _scratch(dev, sl_mxfp4w_dgrad_workspace_bytes(T, n_in, n_out), workspace)
-    _launch("sl_linear_dgrad_mxfp4w", dev, _ptr(dY), _ptr(Wq), _ptr(Ws), _ptr(dX), T, n_in, n_out, _ptr(workspace),
+    _launch("sl_linear_dgrad_mxfp4w", dev, _addr(dY), _addr(Wq), _addr(Ws), _addr(dX), T, n_in, n_out, _addr(workspace),
             nbytes)
     return dX
