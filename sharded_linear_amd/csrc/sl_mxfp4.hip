@@ -90,6 +90,7 @@ extern "C" int sl_mxfp4_quantize(void* stream, const void* x, int64_t rows, int6
   if (!x) return SL_EINVAL;
   if (!aligned16(x) || (q_rows && !aligned16(q_rows)) || (q_cols && !aligned16(q_cols))) return SL_EALIGN;
   if (reinterpret_cast<uintptr_t>(seed_offset) & 7u) return SL_EALIGN;
+  if (ntiles(rows, cols, 128, 128) >= kMaxTiles) return SL_ESHAPE;
   const F4QuantArgs a{x, rows, cols, q_rows, s_rows, q_cols, s_cols, rounding == SL_ROUND_STOCHASTIC, seed, seed_offset};
   return f4_quantize(static_cast<hipStream_t>(stream), a) == 0 ? SL_OK : SL_EHIP;
 }

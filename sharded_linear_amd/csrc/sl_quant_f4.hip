@@ -20,6 +20,7 @@
 
 #include <cstdint>
 
+#include "sl_device.h"
 #include "sl_f4.h"
 #include "sl_mx.h"
 
@@ -106,47 +107,129 @@ __device__ __forceinline__ uint32_t mx4_codes(uint32_t w0, uint32_t w1, uint32_t
 
 constexpr uint32_t kNonFinite = 0x7F80u;       // bf16 magnitudes from here on are infinities and NaNs
 
-// One thread casts one 32-element block: consecutive threads take consecutive blocks of a row, or
-// (columnwise) consecutive columns of one block row.
-template <bool SR, bool COL>
-__global__ void __launch_bounds__(256) mx4_quant_blocks(const uint16_t* x, int64_t R, int64_t C, uint8_t* q, uint8_t* s,
-                                                         uint64_t seed, const uint64_t* seed_offset) {
-  const uint64_t key = seed + (SR && seed_offset ? *seed_offset : 0);
-  const int64_t nb = ((COL ? R : C) + 31) / 32, lines = COL ? C : R, total = nb * lines;
-  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < total; i += int64_t(gridDim.x) * 256) {
-    const int64_t line = COL ? i % C : i / nb, b = COL ? i / C : i % nb;
-    uint32_t w[16];
-    uint16_t d[32];
+// Scale byte of a block, and its exponent (unused where the block has no codes: zeros, or not finite).
+template <bool SR>
+__device__ __forceinline__ uint32_t mx4_scale(uint32_t amax, int& X) {
+  X = mx4_exponent<SR>(amax);
+  return amax >= kNonFinite ? 255u : amax ? uint32_t(X + 127) : 0u;
+}
+
+// One workgroup casts RT x 128 elements.  Each thread loads eight 16-byte chunks, 16 adjacent lanes to
+// a tile row, so that a quad of lanes holds a row block: it shares the block's amax through two DPP
+// permutes and each lane stores its chunk's 8 codes.  For the columnwise copy the elements, and with
+// stochastic rounding their draws, are staged in LDS and read back transposed (ds_read_b64_tr_b16),
+// a 32-row block of one column to a thread; the codes go back through LDS and leave as whole lines of
+// q_cols, RT / 2 bytes a column.
+constexpr int kQC = 128;                 // tile columns
+constexpr int kQS = kQC + 16;            // LDS row stride in elements: 4 rows x 4 column quads of a transposing read in distinct banks
+
+template <int RT, bool SR, bool ROWS, bool COLS>
+__global__ void __launch_bounds__(2 * RT) mx4_quant_tile(F4QuantArgs a) {
+  __shared__ __attribute__((aligned(16))) uint16_t tile[COLS ? RT * kQS : 8];
+  __shared__ __attribute__((aligned(16))) uint16_t dtile[COLS && SR ? RT * kQS : 8];
+  const int64_t ntc = (a.C + kQC - 1) / kQC;
+  const int b = xcd_remap(int(blockIdx.x), int(gridDim.x));     // neighbours in a row of tiles share an XCD's L2
+  const int64_t r0 = b / ntc * RT, c0 = b % ntc * kQC;
+  const int t = threadIdx.x, ch = t & 15;
+  const uint64_t key = a.seed + (SR && a.seed_offset ? *a.seed_offset : 0);
+  const int64_t nbr = (a.C + 31) / 32, nbc = (a.R + 31) / 32;   // blocks of a row, of a column
+  const uint16_t* x = static_cast<const uint16_t*>(a.x);
+  uint4 raw[8];
 #pragma unroll
-    for (int e = 0; e < 32; ++e) {
-      const int64_t r = COL ? b * 32 + e : line, c = COL ? line : b * 32 + e;
-      const uint32_t v = r < R && c < C ? x[r * C + c] : 0;
-      w[e / 2] = e & 1 ? w[e / 2] | (v << 16) : v;
-      if constexpr (SR) {
-        const int64_t at = r * C + c;
-        const uint4 p = philox7(uint64_t(at) / 8, key);
-        const uint32_t word = (at & 4) ? ((at & 2) ? p.w : p.z) : ((at & 2) ? p.y : p.x);
-        d[e] = uint16_t(at & 1 ? word >> 16 : word);
+  for (int k = 0; k < 8; ++k) {                                 // C % 8 == 0: a chunk is inside or outside
+    const int64_t gr = r0 + (t >> 4) + RT / 8 * k, gc = c0 + 8 * ch;
+    raw[k] = gr < a.R && gc < a.C ? *reinterpret_cast<const uint4*>(x + gr * a.C + gc) : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int row = (t >> 4) + RT / 8 * k;
+    const int64_t gr = r0 + row, gc = c0 + 8 * ch;
+    uint4 d = make_uint4(0, 0, 0, 0);
+    if constexpr (SR) d = philox7(uint64_t(gr * (a.C / 8) + gc / 8), key);
+    if constexpr (COLS) {
+      reinterpret_cast<uint4*>(tile + row * kQS)[ch] = raw[k];
+      if constexpr (SR) reinterpret_cast<uint4*>(dtile + row * kQS)[ch] = d;
+    }
+    if constexpr (ROWS) {
+      const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+      const uint32_t amax = quad_max(mag_max(w));                // every lane takes part
+      int X;
+      const uint32_t s = mx4_scale<SR>(amax, X);
+      uint32_t q = mx4_codes<SR>(w[0], w[1], w[2], w[3], X, d);
+      if (amax == 0 || amax >= kNonFinite) q = 0;
+      if (gr < a.R && gc < nbr * 32) {
+        reinterpret_cast<uint32_t*>(a.qr)[gr * (nbr * 4) + gc / 8] = q;
+        if ((ch & 3) == 0) a.sr[gr * nbr + gc / 32] = uint8_t(s);
       }
     }
-    const uint32_t amax = mag_max(w);
-    uint32_t out[4] = {0, 0, 0, 0}, scale = 0;
-    if (amax >= kNonFinite) {
-      scale = 255;
-    } else if (amax) {
-      const int X = mx4_exponent<SR>(amax);
-      scale = uint32_t(X + 127);
+  }
+  if constexpr (COLS) {
+    constexpr int kLine = RT / 2;                               // bytes of a column's codes
+    __syncthreads();
+    uint32_t q[2][4], s[2];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+    for (int h = 0; h < 2; ++h) {
+      // Task idx: column idx % 128, rows 32 rb .. 32 rb + 31.  Lane 4 j + i of a 16-lane group addresses
+      // 4 adjacent columns (quad i of the group's 16) of row j and receives 4 rows of its own column.
+      const int idx = t + 2 * RT * h, rb = idx >> 7;
+      const int s16 = t & 15, jr = s16 >> 2, qc4 = s16 & 3;
+      const int at = (rb * 32 + jr) * kQS + ((idx & (kQC - 1)) & ~15) + 4 * qc4;
+      uint32_t v[16], d[16];
+#pragma unroll
+      for (int r4 = 0; r4 < 8; ++r4) {
+        const uint2 p = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (__attribute__((address_space(3))) i16x4q*)(uintptr_t)lds_addr(tile + at + r4 * 4 * kQS)));
+        v[2 * r4] = p.x;
+        v[2 * r4 + 1] = p.y;
+        if constexpr (SR) {
+          const uint2 e = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (__attribute__((address_space(3))) i16x4q*)(uintptr_t)lds_addr(dtile + at + r4 * 4 * kQS)));
+          d[2 * r4] = e.x;
+          d[2 * r4 + 1] = e.y;
+        }
+      }
+      const uint32_t amax = mag_max(v);
+      int X;
+      s[h] = mx4_scale<SR>(amax, X);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
         uint4 r = make_uint4(0, 0, 0, 0);
-        if constexpr (SR)
-          r = make_uint4(d[8 * j] | (d[8 * j + 1] << 16), d[8 * j + 2] | (d[8 * j + 3] << 16),
-                         d[8 * j + 4] | (d[8 * j + 5] << 16), d[8 * j + 6] | (d[8 * j + 7] << 16));
-        out[j] = mx4_codes<SR>(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3], X, r);
+        if constexpr (SR) r = make_uint4(d[4 * e], d[4 * e + 1], d[4 * e + 2], d[4 * e + 3]);
+        q[h][e] = mx4_codes<SR>(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3], X, r);
+        if (amax == 0 || amax >= kNonFinite) q[h][e] = 0;
       }
     }
-    reinterpret_cast<uint4*>(q)[line * nb + b] = make_uint4(out[0], out[1], out[2], out[3]);
-    s[line * nb + b] = uint8_t(scale);
+    __syncthreads();
+    uint8_t* const qbuf = reinterpret_cast<uint8_t*>(tile);
+    uint8_t* const sbuf = qbuf + kQC * kLine;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int idx = t + 2 * RT * h, col = idx & (kQC - 1), rb = idx >> 7;
+      // 16-byte chunk rb of a column's line sits in slot rb ^ (col / 2): 16 adjacent columns in distinct banks
+      *reinterpret_cast<uint4*>(qbuf + col * kLine + ((rb ^ (col >> (RT == 256 ? 0 : 1))) & (kLine / 16 - 1)) * 16) =
+          make_uint4(q[h][0], q[h][1], q[h][2], q[h][3]);
+      sbuf[col * (RT / 32) + rb] = uint8_t(s[h]);
+    }
+    __syncthreads();
+    const int nrb = int(nbc - r0 / 32 < RT / 32 ? nbc - r0 / 32 : RT / 32);   // row blocks of this tile
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int idx = t + 2 * RT * h, col = idx / (kLine / 16), c = idx % (kLine / 16);
+      const int64_t gc = c0 + col;
+      if (gc < a.C && c < nrb)
+        *reinterpret_cast<uint4*>(a.qc + (gc * nbc + r0 / 32 + c) * 16) = *reinterpret_cast<const uint4*>(
+            qbuf + col * kLine + ((c ^ (col >> (RT == 256 ? 0 : 1))) & (kLine / 16 - 1)) * 16);
+    }
+    if (t < kQC && c0 + t < a.C) {
+      uint8_t* const dst = a.sc + (c0 + t) * nbc + r0 / 32;
+      if (nrb == RT / 32 && (reinterpret_cast<uintptr_t>(dst) & 3) == 0) {
+#pragma unroll
+        for (int e = 0; e < RT / 128; ++e)
+          reinterpret_cast<uint32_t*>(dst)[e] = reinterpret_cast<const uint32_t*>(sbuf)[t * (RT / 128) + e];
+      } else {
+        for (int e = 0; e < nrb; ++e) dst[e] = sbuf[t * (RT / 32) + e];
+      }
+    }
   }
 }
 
@@ -183,26 +266,25 @@ __global__ void __launch_bounds__(256) mx4_dequant_bf16(const uint32_t* q, const
   }
 }
 
-template <bool SR, bool COL>
-int launch_quant(hipStream_t st, const F4QuantArgs& a, uint8_t* q, uint8_t* s) {
-  const int64_t total = ((COL ? a.R : a.C) + 31) / 32 * (COL ? a.C : a.R);
-  int64_t blocks = (total + 255) / 256;
-  if (blocks > 65536) blocks = 65536;
-  hipLaunchKernelGGL((mx4_quant_blocks<SR, COL>), dim3(unsigned(blocks)), dim3(256), 0, st,
-                     static_cast<const uint16_t*>(a.x), a.R, a.C, q, s, a.seed, a.seed_offset);
+template <int RT, bool SR, bool ROWS, bool COLS>
+int launch_quant(hipStream_t st, const F4QuantArgs& a) {
+  const int64_t tiles = (a.C + kQC - 1) / kQC * ((a.R + RT - 1) / RT);
+  hipLaunchKernelGGL((mx4_quant_tile<RT, SR, ROWS, COLS>), dim3(unsigned(tiles)), dim3(2 * RT), 0, st, a);
   return hipGetLastError() == hipSuccess ? 0 : -5;
+}
+
+template <bool SR>
+int dispatch_quant(hipStream_t st, const F4QuantArgs& a) {
+  if (a.qr && a.qc) return launch_quant<128, SR, true, true>(st, a);
+  if (a.qr) return launch_quant<128, SR, true, false>(st, a);
+  return launch_quant<128, SR, false, true>(st, a);
 }
 
 }  // namespace sl2
 
 int f4_quantize(hipStream_t st, const F4QuantArgs& a) {
-  if (a.R == 0 || a.C == 0) return 0;
-  if (a.qr) {
-    const int r = a.stochastic ? sl2::launch_quant<true, false>(st, a, a.qr, a.sr) : sl2::launch_quant<false, false>(st, a, a.qr, a.sr);
-    if (r) return r;
-  }
-  if (a.qc) return a.stochastic ? sl2::launch_quant<true, true>(st, a, a.qc, a.sc) : sl2::launch_quant<false, true>(st, a, a.qc, a.sc);
-  return 0;
+  if (a.R == 0 || a.C == 0 || (!a.qr && !a.qc)) return 0;
+  return a.stochastic ? sl2::dispatch_quant<true>(st, a) : sl2::dispatch_quant<false>(st, a);
 }
 
 int f4_dequantize(hipStream_t st, const uint8_t* q, const uint8_t* s, void* out, int64_t rows, int64_t cols) {
