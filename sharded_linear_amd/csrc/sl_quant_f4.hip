@@ -53,14 +53,23 @@ __device__ __forceinline__ uint32_t e2m1_nearest(float x, float mult) {
   return uint32_t(n < 7.f ? n : 7.f) | ((__float_as_uint(x) >> 28) & 8u);
 }
 
-// The same, stochastic with the draw r.  From 1 on, the codes order like the fp32 bits with one
-// mantissa bit left, so adding the draw below that bit and cutting there is the rule above (a bf16's
-// mantissa has no bits below the draw's); below 1 the step is fixed.
-__device__ __forceinline__ uint32_t e2m1_stochastic(float x, float mult, uint32_t r) {
-  const float v = __builtin_fabsf(x) * mult;
-  const uint32_t big = ((__float_as_uint(v) + (r << 6)) >> 22) - 252u;     // bits of 1.0 are 254 << 22
-  const uint32_t small = (uint32_t(v * 131072.f) + r) >> 16;
-  return (v >= 1.f ? big : small) | ((__float_as_uint(x) >> 28) & 8u);
+// The sign bits of 8 elements, two to a word, at bit 3 of nibbles 0..7.
+__device__ __forceinline__ uint32_t signs8(const uint32_t (&w)[4]) {
+  const uint32_t a = __builtin_amdgcn_perm(w[1], w[0], 0x07030501u);      // high bytes: elements 0, 2, 1, 3
+  const uint32_t b = __builtin_amdgcn_perm(w[3], w[2], 0x07030501u);
+  const uint32_t even = __builtin_amdgcn_perm(b, a, 0x05040100u) & 0x80808080u;
+  const uint32_t odd = __builtin_amdgcn_perm(b, a, 0x07060302u) & 0x80808080u;
+  return (even >> 4) | odd;
+}
+
+// The magnitude's code of x with |x| / 2^X = v, stochastic; r6: the draw times 2^6.  From 1 on, the codes
+// order like the fp32 bits of v with one mantissa bit left (bits 22 and up, whose low three are the
+// code where the bits are those of 2^18 v), so adding the draw below that bit and cutting there is the rule (a
+// bf16's mantissa has no bits below the draw's); below 1 the step is fixed and 2^18 v an integer's worth.
+__device__ __forceinline__ uint32_t e2m1_stochastic(float x, int X, uint32_t r6) {
+  const float v = __builtin_ldexpf(__builtin_fabsf(x), 18 - X);
+  const uint32_t big = __float_as_uint(v) + r6, small = (uint32_t(v) << 5) + r6;
+  return (v >= 262144.f ? big : small) >> 22;               // above the code's 3 bits, bit 25 is 0 and the others are cut off
 }
 
 // Shared exponent of a block whose largest magnitude has the bf16 bits amax (finite, not zero).  A
@@ -77,15 +86,15 @@ __device__ __forceinline__ int mx4_exponent(uint32_t amax) {
 template <bool SR>
 __device__ __forceinline__ uint32_t mx4_codes(uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3, int X, uint4 r) {
   const uint32_t w[4] = {w0, w1, w2, w3};
-  const float mult = __uint_as_float(uint32_t(127 - X) << 23);          // 2^-X, X in -127 .. 126
   uint32_t q = 0;
   if constexpr (SR) {
     const uint32_t d[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      q |= e2m1_stochastic(bf16_lo(w[i]), mult, d[i] & 0xFFFFu) << (8 * i);
-      q |= e2m1_stochastic(bf16_hi(w[i]), mult, d[i] >> 16) << (8 * i + 4);
+    for (int i = 0; i < 4; ++i) {                             // each code enters at the top
+      q = __builtin_amdgcn_alignbit(e2m1_stochastic(bf16_lo(w[i]), X, (d[i] << 6) & 0x3FFFC0u), q, 4);
+      q = __builtin_amdgcn_alignbit(e2m1_stochastic(bf16_hi(w[i]), X, (d[i] >> 10) & 0x3FFFC0u), q, 4);
     }
+    q |= signs8(w);
   } else {
     if (X > -127) {
       // one instruction for two elements; checked on every bf16 pattern against the rule
@@ -95,6 +104,7 @@ __device__ __forceinline__ uint32_t mx4_codes(uint32_t w0, uint32_t w1, uint32_t
       q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, __builtin_bit_cast(bf16x2, w[2]), scale, 2);
       q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, __builtin_bit_cast(bf16x2, w[3]), scale, 3);
     } else {                                                // 2^-127 is no normal fp32 scale
+      const float mult = __uint_as_float(0x7F000000u);        // 2^127
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         q |= e2m1_nearest(bf16_lo(w[i]), mult) << (8 * i);
@@ -114,66 +124,67 @@ __device__ __forceinline__ uint32_t mx4_scale(uint32_t amax, int& X) {
   return amax >= kNonFinite ? 255u : amax ? uint32_t(X + 127) : 0u;
 }
 
-// One workgroup casts RT x 128 elements.  Each thread loads eight 16-byte chunks, 16 adjacent lanes to
+// One workgroup casts 128 x 128 elements.  Each thread loads eight 16-byte chunks, 16 adjacent lanes to
 // a tile row, so that a quad of lanes holds a row block: it shares the block's amax through two DPP
 // permutes and each lane stores its chunk's 8 codes.  For the columnwise copy the elements, and with
-// stochastic rounding their draws, are staged in LDS and read back transposed (ds_read_b64_tr_b16),
-// a 32-row block of one column to a thread; the codes go back through LDS and leave as whole lines of
-// q_cols, RT / 2 bytes a column.
-constexpr int kQC = 128;                 // tile columns
+// stochastic rounding their draws, are staged in LDS, half the rows at a time, and read back transposed
+// (ds_read_b64_tr_b16), a 32-row block of one column to a thread; the codes go back through LDS and
+// leave 64 bytes a column.
+constexpr int kQC = 128, kQH = 64;       // tile columns, rows of half a tile
 constexpr int kQS = kQC + 16;            // LDS row stride in elements: 4 rows x 4 column quads of a transposing read in distinct banks
 
-template <int RT, bool SR, bool ROWS, bool COLS>
-__global__ void __launch_bounds__(2 * RT) mx4_quant_tile(F4QuantArgs a) {
-  __shared__ __attribute__((aligned(16))) uint16_t tile[COLS ? RT * kQS : 8];
-  __shared__ __attribute__((aligned(16))) uint16_t dtile[COLS && SR ? RT * kQS : 8];
+template <bool SR, bool ROWS, bool COLS>
+__global__ void __launch_bounds__(256) mx4_quant_tile(F4QuantArgs a) {
+  __shared__ __attribute__((aligned(16))) uint16_t tile[COLS ? kQH * kQS : 8];
+  __shared__ __attribute__((aligned(16))) uint16_t dtile[COLS && SR ? kQH * kQS : 8];
   const int64_t ntc = (a.C + kQC - 1) / kQC;
   const int b = xcd_remap(int(blockIdx.x), int(gridDim.x));     // neighbours in a row of tiles share an XCD's L2
-  const int64_t r0 = b / ntc * RT, c0 = b % ntc * kQC;
+  const int64_t r0 = b / ntc * (2 * kQH), c0 = b % ntc * kQC;
   const int t = threadIdx.x, ch = t & 15;
   const uint64_t key = a.seed + (SR && a.seed_offset ? *a.seed_offset : 0);
   const int64_t nbr = (a.C + 31) / 32, nbc = (a.R + 31) / 32;   // blocks of a row, of a column
   const uint16_t* x = static_cast<const uint16_t*>(a.x);
+  // chunk k of this thread: row r0 + t / 16 + 16 k, columns gc .. gc + 7
+  const int64_t gr0 = r0 + (t >> 4), gc = c0 + 8 * ch, at0 = gr0 * (a.C / 8) + gc / 8, qat0 = gr0 * nbr + gc / 32;
+  const int left = int(a.R - gr0 < 128 ? a.R - gr0 : 128);      // rows from the first on
   uint4 raw[8];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {                                 // C % 8 == 0: a chunk is inside or outside
-    const int64_t gr = r0 + (t >> 4) + RT / 8 * k, gc = c0 + 8 * ch;
-    raw[k] = gr < a.R && gc < a.C ? *reinterpret_cast<const uint4*>(x + gr * a.C + gc) : make_uint4(0, 0, 0, 0);
-  }
+  for (int k = 0; k < 8; ++k)                                   // C % 8 == 0: a chunk is inside or outside
+    raw[k] = 16 * k < left && gc < a.C ? reinterpret_cast<const uint4*>(x)[at0 + k * (2 * a.C)] : make_uint4(0, 0, 0, 0);
+  uint32_t q[2][4], s[2];                                       // columnwise codes and scales, a block from each half
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const int row = (t >> 4) + RT / 8 * k;
-    const int64_t gr = r0 + row, gc = c0 + 8 * ch;
-    uint4 d = make_uint4(0, 0, 0, 0);
-    if constexpr (SR) d = philox7(uint64_t(gr * (a.C / 8) + gc / 8), key);
-    if constexpr (COLS) {
-      reinterpret_cast<uint4*>(tile + row * kQS)[ch] = raw[k];
-      if constexpr (SR) reinterpret_cast<uint4*>(dtile + row * kQS)[ch] = d;
-    }
-    if constexpr (ROWS) {
-      const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
-      const uint32_t amax = quad_max(mag_max(w));                // every lane takes part
-      int X;
-      const uint32_t s = mx4_scale<SR>(amax, X);
-      uint32_t q = mx4_codes<SR>(w[0], w[1], w[2], w[3], X, d);
-      if (amax == 0 || amax >= kNonFinite) q = 0;
-      if (gr < a.R && gc < nbr * 32) {
-        reinterpret_cast<uint32_t*>(a.qr)[gr * (nbr * 4) + gc / 8] = q;
-        if ((ch & 3) == 0) a.sr[gr * nbr + gc / 32] = uint8_t(s);
+  for (int h = 0; h < 2; ++h) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int row = (t >> 4) + 16 * k;
+      const int n = 4 * h + k;
+      const uint4 v = raw[4 * h + k];
+      uint4 d = make_uint4(0, 0, 0, 0);
+      if constexpr (SR) d = philox7(uint64_t(at0 + n * (2 * a.C)), key);
+      if constexpr (COLS) {
+        reinterpret_cast<uint4*>(tile + row * kQS)[ch] = v;
+        if constexpr (SR) reinterpret_cast<uint4*>(dtile + row * kQS)[ch] = d;
+      }
+      if constexpr (ROWS) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        const uint32_t amax = quad_max(mag_max(w));              // every lane takes part
+        int X;
+        const uint32_t sc = mx4_scale<SR>(amax, X);
+        uint32_t c = mx4_codes<SR>(w[0], w[1], w[2], w[3], X, d);
+        if (amax == 0 || amax >= kNonFinite) c = 0;
+        if (16 * n < left && gc < nbr * 32) {
+          const int64_t at = qat0 + n * (16 * nbr);
+          reinterpret_cast<uint32_t*>(a.qr)[at * 4 + (ch & 3)] = c;
+          if ((ch & 3) == 0) a.sr[at] = uint8_t(sc);
+        }
       }
     }
-  }
-  if constexpr (COLS) {
-    constexpr int kLine = RT / 2;                               // bytes of a column's codes
-    __syncthreads();
-    uint32_t q[2][4], s[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      // Task idx: column idx % 128, rows 32 rb .. 32 rb + 31.  Lane 4 j + i of a 16-lane group addresses
-      // 4 adjacent columns (quad i of the group's 16) of row j and receives 4 rows of its own column.
-      const int idx = t + 2 * RT * h, rb = idx >> 7;
+    if constexpr (COLS) {
+      __syncthreads();
+      // Thread t: column t % 128, rows 32 (t / 128) .. of this half.  Lane 4 j + i of a 16-lane group
+      // addresses 4 adjacent columns (quad i of the group's 16) of row j and receives 4 rows of its own column.
       const int s16 = t & 15, jr = s16 >> 2, qc4 = s16 & 3;
-      const int at = (rb * 32 + jr) * kQS + ((idx & (kQC - 1)) & ~15) + 4 * qc4;
+      const int at = ((t >> 7) * 32 + jr) * kQS + ((t & (kQC - 1)) & ~15) + 4 * qc4;
       uint32_t v[16], d[16];
 #pragma unroll
       for (int r4 = 0; r4 < 8; ++r4) {
@@ -198,37 +209,33 @@ __global__ void __launch_bounds__(2 * RT) mx4_quant_tile(F4QuantArgs a) {
         q[h][e] = mx4_codes<SR>(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3], X, r);
         if (amax == 0 || amax >= kNonFinite) q[h][e] = 0;
       }
+      __syncthreads();
     }
-    __syncthreads();
+  }
+  if constexpr (COLS) {
+    // 16-byte chunk rb of a column's 64-byte line sits in slot rb ^ (col / 2): 8 adjacent columns in distinct banks
     uint8_t* const qbuf = reinterpret_cast<uint8_t*>(tile);
-    uint8_t* const sbuf = qbuf + kQC * kLine;
+    uint8_t* const sbuf = qbuf + kQC * 64;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int idx = t + 2 * RT * h, col = idx & (kQC - 1), rb = idx >> 7;
-      // 16-byte chunk rb of a column's line sits in slot rb ^ (col / 2): 16 adjacent columns in distinct banks
-      *reinterpret_cast<uint4*>(qbuf + col * kLine + ((rb ^ (col >> (RT == 256 ? 0 : 1))) & (kLine / 16 - 1)) * 16) =
-          make_uint4(q[h][0], q[h][1], q[h][2], q[h][3]);
-      sbuf[col * (RT / 32) + rb] = uint8_t(s[h]);
+      const int col = t & (kQC - 1), rb = 2 * h + (t >> 7);
+      *reinterpret_cast<uint4*>(qbuf + col * 64 + ((rb ^ (col >> 1)) & 3) * 16) = make_uint4(q[h][0], q[h][1], q[h][2], q[h][3]);
+      sbuf[col * 4 + rb] = uint8_t(s[h]);
     }
     __syncthreads();
-    const int nrb = int(nbc - r0 / 32 < RT / 32 ? nbc - r0 / 32 : RT / 32);   // row blocks of this tile
+    const int nrb = int(nbc - r0 / 32 < 4 ? nbc - r0 / 32 : 4);   // row blocks of this tile
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int idx = t + 2 * RT * h, col = idx / (kLine / 16), c = idx % (kLine / 16);
+      const int idx = t + 256 * h, col = idx >> 2, c = idx & 3;
       const int64_t gc = c0 + col;
       if (gc < a.C && c < nrb)
-        *reinterpret_cast<uint4*>(a.qc + (gc * nbc + r0 / 32 + c) * 16) = *reinterpret_cast<const uint4*>(
-            qbuf + col * kLine + ((c ^ (col >> (RT == 256 ? 0 : 1))) & (kLine / 16 - 1)) * 16);
+        *reinterpret_cast<uint4*>(a.qc + (gc * nbc + r0 / 32 + c) * 16) =
+            *reinterpret_cast<const uint4*>(qbuf + col * 64 + ((c ^ (col >> 1)) & 3) * 16);
     }
     if (t < kQC && c0 + t < a.C) {
       uint8_t* const dst = a.sc + (c0 + t) * nbc + r0 / 32;
-      if (nrb == RT / 32 && (reinterpret_cast<uintptr_t>(dst) & 3) == 0) {
-#pragma unroll
-        for (int e = 0; e < RT / 128; ++e)
-          reinterpret_cast<uint32_t*>(dst)[e] = reinterpret_cast<const uint32_t*>(sbuf)[t * (RT / 128) + e];
-      } else {
-        for (int e = 0; e < nrb; ++e) dst[e] = sbuf[t * (RT / 32) + e];
-      }
+      if (nrb == 4 && (reinterpret_cast<uintptr_t>(dst) & 3) == 0) *reinterpret_cast<uint32_t*>(dst) = reinterpret_cast<const uint32_t*>(sbuf)[t];
+      else for (int e = 0; e < nrb; ++e) dst[e] = sbuf[t * 4 + e];
     }
   }
 }
@@ -266,18 +273,18 @@ __global__ void __launch_bounds__(256) mx4_dequant_bf16(const uint32_t* q, const
   }
 }
 
-template <int RT, bool SR, bool ROWS, bool COLS>
+template <bool SR, bool ROWS, bool COLS>
 int launch_quant(hipStream_t st, const F4QuantArgs& a) {
-  const int64_t tiles = (a.C + kQC - 1) / kQC * ((a.R + RT - 1) / RT);
-  hipLaunchKernelGGL((mx4_quant_tile<RT, SR, ROWS, COLS>), dim3(unsigned(tiles)), dim3(2 * RT), 0, st, a);
+  const int64_t tiles = (a.C + kQC - 1) / kQC * ((a.R + 2 * kQH - 1) / (2 * kQH));
+  hipLaunchKernelGGL((mx4_quant_tile<SR, ROWS, COLS>), dim3(unsigned(tiles)), dim3(256), 0, st, a);
   return hipGetLastError() == hipSuccess ? 0 : -5;
 }
 
 template <bool SR>
 int dispatch_quant(hipStream_t st, const F4QuantArgs& a) {
-  if (a.qr && a.qc) return launch_quant<128, SR, true, true>(st, a);
-  if (a.qr) return launch_quant<128, SR, true, false>(st, a);
-  return launch_quant<128, SR, false, true>(st, a);
+  if (a.qr && a.qc) return launch_quant<SR, true, true>(st, a);
+  if (a.qr) return launch_quant<SR, true, false>(st, a);
+  return launch_quant<SR, false, true>(st, a);
 }
 
 }  // namespace sl2
