@@ -60,6 +60,23 @@ __device__ __forceinline__ void wait_vmcnt() {
 // s_waitcnt lgkmcnt(0) with vmcnt and expcnt unconstrained: this wave's LDS reads are complete.
 __device__ __forceinline__ void wait_lgkm0() { __builtin_amdgcn_s_waitcnt(0xC07F); }
 
+// A barrier alone: no counter is waited for, and no memory access moves across it.
+__device__ __forceinline__ void bare_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+__device__ __forceinline__ i32x8 f4_operand(i32x4 v) {           // the 4-bit forms read the lower four registers
+  return __builtin_shufflevector(v, v, 0, 1, 2, 3, -1, -1, -1, -1);
+}
+// A barrier behind which every wave sees the LDS writes before it (and DMA loads that each wave has waited for).
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("" ::: "memory");
+  wait_lgkm0();
+  bare_barrier();
+}
+
 // Raw buffer descriptor over one operand (gfx9 layout: base, stride 0, num_records = byte
 // extent, format word).  Offsets outside the extent -- including kOOB, above every extent the
 // host admits -- read zeros instead of touching memory.
@@ -70,6 +87,14 @@ __device__ __forceinline__ i32x4 rsrc(const void* base, uint32_t bytes) {
   r[1] = int(uint32_t(a >> 32) & 0xFFFFu);
   r[2] = int(bytes);
   r[3] = kRsrcWord3;
+  return r;
+}
+
+// The same, of values that are wave-uniform without the compiler's knowing it.
+__device__ __forceinline__ i32x4 rsrc_uniform(const void* base, uint32_t bytes) {
+  i32x4 r = rsrc(base, bytes);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) r[e] = __builtin_amdgcn_readfirstlane(r[e]);
   return r;
 }
 

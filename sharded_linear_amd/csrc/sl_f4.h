@@ -51,6 +51,10 @@ struct F4RowsArgs {
   int64_t T, N, K;
 };
 int f4_rows(hipStream_t st, const F4RowsArgs& g);
+// The same with bf16 X for any T (w4_tile_fwd), and Y[T][N] = X[T][K] . W[K][N] with W blocked along N
+// (w4_tile_dgrad).
+int w4_tile_fwd(hipStream_t st, const F4RowsArgs& g);
+int w4_tile_dgrad(hipStream_t st, const F4RowsArgs& g);
 
 // The SL_TUNE_F8_CONFIG knob: a forced tile configuration of the block-scaled products, or -1 (sl_gemm.hip).
 int block_scaled_config();

@@ -40,17 +40,6 @@ template <class T>
 __device__ __forceinline__ T lds_read(uint32_t a) {
   return *reinterpret_cast<const __attribute__((address_space(3))) T*>(uintptr_t(a));
 }
-// A barrier alone: no counter is waited for, and no memory access moves across it.
-__device__ __forceinline__ void bare_barrier() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_sched_barrier(0);
-}
-__device__ __forceinline__ i32x8 f4_operand(i32x4 v) {           // the 4-bit forms read the lower four registers
-  return __builtin_shufflevector(v, v, 0, 1, 2, 3, -1, -1, -1, -1);
-}
-
 // Block scales are 8 bytes a row and stage, far less than the 128-byte lines they lie in: direct loads
 // to LDS of 16 bytes a row and two stages moved a line for every 16 bytes and cost 335 of a stage's 3150
 // cycles, and where rows of scales start at odd addresses (4-byte pieces) 2100 of 5300.  So each thread
@@ -79,9 +68,7 @@ struct F4Side {
   // a descriptor over the tile's rows: offsets fit 32 bits whatever the matrix's size, and rows past the
   // end read zeros
   __device__ __forceinline__ void set_rows(const void* codes, int row0, int all, int64_t K) {
-    rc = rsrc(static_cast<const char*>(codes) + int64_t(row0) * (K / 2), uint32_t(min(all - row0, R)) * uint32_t(K / 2));
-#pragma unroll
-    for (int e = 0; e < 4; ++e) rc[e] = __builtin_amdgcn_readfirstlane(rc[e]);
+    rc = rsrc_uniform(static_cast<const char*>(codes) + int64_t(row0) * (K / 2), uint32_t(min(all - row0, R)) * uint32_t(K / 2));
   }
   __device__ __forceinline__ void init(int64_t K, int lane, int wave) {
     nb = uint32_t(K / 32);

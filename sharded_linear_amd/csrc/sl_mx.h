@@ -29,10 +29,18 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t m) {
   return o > m ? o : m;
 }
 
-// An E8M0 scale byte as fp32: 2^(s - 127), s = 0 as the subnormal 2^-127, s = 255 as NaN.
+// An E8M0 scale byte as fp32: 2^(s - 127), s = 0 as the subnormal 2^-127, s = 255 as NaN; the two set the
+// top mantissa bit.
 __device__ __forceinline__ float e8m0_to_f32(uint32_t s) {
-  if (s == 0xFFu) return __builtin_bit_cast(float, 0x7FC00000u);             // NaN scale
-  return s ? __builtin_bit_cast(float, s << 23) : __builtin_bit_cast(float, 0x00400000u);  // 2^-127
+  return __builtin_bit_cast(float, (s << 23) | (((s + 1) & 0xFEu) == 0 ? 0x00400000u : 0u));
+}
+
+// 8 E2M1 codes (nibbles 0..7 of a word) times a scale, exact.
+typedef __bf16 bf16x8_mx __attribute__((ext_vector_type(8)));
+__device__ __forceinline__ bf16x8_mx f4_to_bf16x8(uint32_t codes, float scale) {
+  const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 0), b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 1);
+  const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 2), d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 3);
+  return bf16x8_mx{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
 }  // namespace sl2

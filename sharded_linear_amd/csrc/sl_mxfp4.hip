@@ -34,7 +34,9 @@ int pick_config(int64_t M, int64_t N) {
 }
 
 // Rows up to which a product reads the weight directly.
-constexpr int64_t kFewRows = 64, kFewRowsBf16 = 256;
+constexpr int64_t kFewRows = 64, kFewRowsBf16 = 32;
+// Rows from which a bf16 copy of the weight pays for itself.
+constexpr int64_t kManyRowsFwd = 1024, kManyRowsDgrad = 1024;
 
 // C[M][N] = A . B^T (bf16) over K
 int product(void* stream, const uint8_t* a, const uint8_t* sa, const uint8_t* b, const uint8_t* sb, void* c, int64_t M,
@@ -149,12 +151,12 @@ extern "C" int sl_linear_wgrad_accum_mxfp4(void* stream, const uint8_t* dYqT, co
 // ---- bf16 activations with MXFP4 weights ------------------------------------------------------
 
 extern "C" size_t sl_mxfp4w_fwd_workspace_bytes(int64_t T, int64_t in, int64_t out) {
-  if (check_product(T, in, out, in) || T <= kFewRowsBf16 || in == 0 || out == 0) return 0;
+  if (check_product(T, in, out, in) || T < kManyRowsFwd || in == 0 || out == 0) return 0;
   return size_t(out) * size_t(in) * 2;
 }
 
 extern "C" size_t sl_mxfp4w_dgrad_workspace_bytes(int64_t T, int64_t in, int64_t out) {
-  if (check_product(T, in, out, in) || T == 0 || in == 0 || out == 0) return 0;
+  if (check_product(T, in, out, in) || T < kManyRowsDgrad || in == 0 || out == 0) return 0;
   return size_t(out) * size_t(in) * 2;
 }
 
@@ -165,8 +167,11 @@ extern "C" int sl_linear_fwd_mxfp4w(void* stream, const void* X, const uint8_t* 
   if (T == 0 || out == 0) return SL_OK;
   if (!Y || (in > 0 && (!X || !Wq || !Ws))) return SL_EINVAL;
   if (!aligned16(X) || !aligned16(Wq) || !aligned16(Y)) return SL_EALIGN;
-  if (T <= kFewRowsBf16)
-    return f4_rows(static_cast<hipStream_t>(stream), F4RowsArgs{X, nullptr, Wq, Ws, Y, T, out, in}) == 0 ? SL_OK : SL_EHIP;
+  if (T < kManyRowsFwd) {
+    const F4RowsArgs g{X, nullptr, Wq, Ws, Y, T, out, in};
+    const hipStream_t hs = static_cast<hipStream_t>(stream);
+    return (T <= kFewRowsBf16 ? f4_rows(hs, g) : w4_tile_fwd(hs, g)) == 0 ? SL_OK : SL_EHIP;
+  }
   const size_t need = sl_mxfp4w_fwd_workspace_bytes(T, in, out);
   if (need && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return SL_EWORKSPACE;
   if (in > 0 && f4_dequantize(static_cast<hipStream_t>(stream), Wq, Ws, workspace, out, in)) return SL_EHIP;
@@ -180,6 +185,8 @@ extern "C" int sl_linear_dgrad_mxfp4w(void* stream, const void* dY, const uint8_
   if (T == 0 || in == 0) return SL_OK;
   if (!dX || (out > 0 && (!dY || !Wq || !Ws))) return SL_EINVAL;
   if (!aligned16(dY) || !aligned16(Wq) || !aligned16(dX)) return SL_EALIGN;
+  if (T < kManyRowsDgrad)
+    return w4_tile_dgrad(static_cast<hipStream_t>(stream), F4RowsArgs{dY, nullptr, Wq, Ws, dX, T, in, out}) == 0 ? SL_OK : SL_EHIP;
   const size_t need = sl_mxfp4w_dgrad_workspace_bytes(T, in, out);
   if (need && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return SL_EWORKSPACE;
   if (out > 0 && f4_dequantize(static_cast<hipStream_t>(stream), Wq, Ws, workspace, out, in)) return SL_EHIP;

@@ -24,12 +24,6 @@ namespace sl2 {
 
 constexpr int kRowWaves = 8;
 
-__device__ __forceinline__ bf16x8 f4_to_bf16x8(uint32_t codes, float scale) {
-  const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 0), b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 1);
-  const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 2), d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 3);
-  return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
-}
-
 // The scales of blocks b .. b + 4 U - 1 (b < nb) of a row of nb, four to a word; 0 past the row's end.
 // One load, whatever the address; where it would pass the end, it ends there and is shifted.
 template <int U>
