@@ -304,16 +304,18 @@ int sl_linear_dgrad_nvfp4w(void* stream, const void* dY, const void* Wm, float w
  *   dgrad: dX[T,in]           = deq(dYq)[T,out] . deq(WqT)[in,out]^T   out % 32 == 0
  *   wgrad: main_grad[out,in] += deq(dYqT)[out,T] . deq(XqT)[in,T]^T    T % 32 == 0, fp32, in place
  * (the contracted extent is the padded one that sl_mxfp4_quantize writes; the others follow the
- * conventions above; in, out or a contracted extent above 2^23 is SL_ESHAPE).  The weight gradient
- * takes a device workspace of at least sl_mxfp4_wgrad_workspace_bytes(T, in, out) bytes (fp32 split-K planes; 0 when the shape needs no
- * split, workspace may then be NULL): its initial contents do not matter, and calls that may run
- * concurrently need distinct workspaces.  main_grad is read and written only inside [out, in].
+ * conventions above; in, out or a contracted extent above 2^23 is SL_ESHAPE).  Each
+ * takes a device workspace of at least its query's bytes (16-byte aligned; fp32 split-K planes; 0 when the shape
+ * needs no split, workspace may then be NULL): its initial contents do not matter, and calls that may
+ * run concurrently need distinct workspaces.  main_grad is read and written only inside [out, in].
  *
  * bf16 activations with MXFP4 weights blocked along in (in % 32 == 0), for serving and for frozen
  * weights; every dequantised weight must be a finite bf16 value or a NaN:
  *   fwd:   Y[T,out] = X[T,in] . deq(Wq)[out,in]^T        dgrad: dX[T,in] = dY[T,out] . deq(Wq)
- * Each takes a device workspace of at least its query's bytes (0 for the forms that read the codes
- * directly, few tokens among them; workspace may then be NULL), with the rules above.
+ * Their workspaces follow the same rules: split-K planes, or for many tokens a bf16 copy of the weight.
+ * Up to 32 tokens only the last of these products (dgrad through Wq) may need one.
+ * The SL_TUNE_F8_CONFIG knob forces the tiles of the products of two MXFP4 operands too (0: 256x256,
+ * 1: 128x128, 2: as 0), from one token on; it is read by the queries as by the calls.
  * --------------------------------------------------------------------------------------------- */
 enum { SL_ROUND_NEAREST = 0, SL_ROUND_STOCHASTIC = 1 };
 int sl_mxfp4_quantize(void* stream, const void* x, int64_t rows, int64_t cols, uint8_t* q_rows,
@@ -321,10 +323,14 @@ int sl_mxfp4_quantize(void* stream, const void* x, int64_t rows, int64_t cols, u
                       uint64_t seed, const uint64_t* seed_offset);
 int sl_mxfp4_dequantize(void* stream, const uint8_t* q, const uint8_t* s, void* out, int64_t rows,
                         int64_t cols);
+size_t sl_mxfp4_fwd_workspace_bytes(int64_t T, int64_t in, int64_t out);
 int sl_linear_fwd_mxfp4(void* stream, const uint8_t* Xq, const uint8_t* Xs, const uint8_t* Wq,
-                        const uint8_t* Ws, void* Y, int64_t T, int64_t in, int64_t out);
+                        const uint8_t* Ws, void* Y, int64_t T, int64_t in, int64_t out,
+                        void* workspace, size_t workspace_bytes);
+size_t sl_mxfp4_dgrad_workspace_bytes(int64_t T, int64_t in, int64_t out);
 int sl_linear_dgrad_mxfp4(void* stream, const uint8_t* dYq, const uint8_t* dYs, const uint8_t* WqT,
-                          const uint8_t* WsT, void* dX, int64_t T, int64_t in, int64_t out);
+                          const uint8_t* WsT, void* dX, int64_t T, int64_t in, int64_t out,
+                          void* workspace, size_t workspace_bytes);
 size_t sl_mxfp4_wgrad_workspace_bytes(int64_t T, int64_t in, int64_t out);
 int sl_linear_wgrad_accum_mxfp4(void* stream, const uint8_t* dYqT, const uint8_t* dYsT,
                                 const uint8_t* XqT, const uint8_t* XsT, float* main_grad, int64_t T,

@@ -10,7 +10,7 @@ from .ops import (sl_grad_buffer_zero, sl_linear_dgrad, sl_linear_dgrad_mxfp8, s
                   sl_mxfp8_workspace_bytes, sl_wgrad_workspace_bytes, sl_nvfp4_materialize, sl_mxfp8_dequantize,
                   sl_linear_fwd_nvfp4w, sl_linear_dgrad_nvfp4w, sl_set_tuning, tuning,
                   sl_linear_wgrad_accum_noalloc, sl_mxfp4_quantize, sl_mxfp4_dequantize, sl_linear_fwd_mxfp4,
-                  sl_linear_dgrad_mxfp4, sl_linear_wgrad_accum_mxfp4, sl_mxfp4_wgrad_workspace_bytes,
+                  sl_linear_dgrad_mxfp4, sl_linear_wgrad_accum_mxfp4, sl_mxfp4_fwd_workspace_bytes, sl_mxfp4_dgrad_workspace_bytes, sl_mxfp4_wgrad_workspace_bytes,
                   sl_linear_fwd_mxfp4w, sl_linear_dgrad_mxfp4w, sl_mxfp4w_fwd_workspace_bytes,
                   sl_mxfp4w_dgrad_workspace_bytes)
 from .buffer import ParamAndGradBuffer, sl_bucket_divisor, sl_default_bucket_size, sl_layout_build
@@ -26,6 +26,6 @@ __all__ = [
     "sl_default_bucket_size", "sl_bucket_divisor", "LinearWithGradAccumulation",
     "linear_with_grad_accumulation", "LinearMXFP4WithGradAccumulation", "linear_mxfp4_with_grad_accumulation",
     "sl_mxfp4_quantize", "sl_mxfp4_dequantize", "sl_linear_fwd_mxfp4", "sl_linear_dgrad_mxfp4",
-    "sl_linear_wgrad_accum_mxfp4", "sl_mxfp4_wgrad_workspace_bytes", "sl_linear_fwd_mxfp4w", "sl_linear_dgrad_mxfp4w",
+    "sl_linear_wgrad_accum_mxfp4", "sl_mxfp4_fwd_workspace_bytes", "sl_mxfp4_dgrad_workspace_bytes", "sl_mxfp4_wgrad_workspace_bytes", "sl_linear_fwd_mxfp4w", "sl_linear_dgrad_mxfp4w",
     "sl_mxfp4w_fwd_workspace_bytes", "sl_mxfp4w_dgrad_workspace_bytes",
 ]

@@ -49,8 +49,10 @@ PROTOTYPES = {
     "sl_linear_dgrad_nvfp4w": (ctypes.c_int, [c_vp, c_vp, c_vp, ctypes.c_float, c_vp, c_i64, c_i64, c_i64]),
     "sl_mxfp4_quantize": (ctypes.c_int, [c_vp, c_vp, c_i64, c_i64, c_vp, c_vp, c_vp, c_vp, c_i32, c_u64, c_vp]),
     "sl_mxfp4_dequantize": (ctypes.c_int, [c_vp, c_vp, c_vp, c_vp, c_i64, c_i64]),
-    "sl_linear_fwd_mxfp4": (ctypes.c_int, [c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64]),
-    "sl_linear_dgrad_mxfp4": (ctypes.c_int, [c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64]),
+    "sl_mxfp4_fwd_workspace_bytes": (c_sz, [c_i64, c_i64, c_i64]),
+    "sl_linear_fwd_mxfp4": (ctypes.c_int, [c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_vp, c_sz]),
+    "sl_mxfp4_dgrad_workspace_bytes": (c_sz, [c_i64, c_i64, c_i64]),
+    "sl_linear_dgrad_mxfp4": (ctypes.c_int, [c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_vp, c_sz]),
     "sl_mxfp4_wgrad_workspace_bytes": (c_sz, [c_i64, c_i64, c_i64]),
     "sl_linear_wgrad_accum_mxfp4": (ctypes.c_int, [c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64,
                                                    c_vp, c_sz]),

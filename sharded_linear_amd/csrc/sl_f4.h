@@ -28,7 +28,7 @@ int f4_quantize(hipStream_t st, const F4QuantArgs& a);
 // bf16 out[rows][cols] of codes q and scales s; cols % 32 == 0.
 int f4_dequantize(hipStream_t st, const uint8_t* q, const uint8_t* s, void* out, int64_t rows, int64_t cols);
 
-// C[M][N] = A . B^T of two MXFP4 operands A[M][K], B[N][K]: bf16 C, or fp32 C += (accum), unsplit or
+// C[M][N] = A . B^T of two MXFP4 operands A[M][K], B[N][K]: bf16 C, or fp32 C += (f4_accum), unsplit or
 // with the partial sums of each split of K in its plane of ws[splits][M][N].  N % 8 == 0.
 struct F4Args {
   const void *a, *b;    // codes
@@ -38,7 +38,7 @@ struct F4Args {
   float* ws;
   int splits;           // splits of K, of kt_per_split stages each (accumulating product only)
   int kt_per_split;
-  int cfg;              // tile configuration: 0 256x256, 1 128x128, 2 256x128
+  int cfg;              // tile configuration: 0 256x256, 1 128x128
 };
 constexpr int kF4StageK = 256;                  // k elements of one stage
 int f4_gemm(hipStream_t st, const F4Args& g);
@@ -49,12 +49,20 @@ struct F4RowsArgs {
   const void *x, *xs, *w, *ws;
   void* y;
   int64_t T, N, K;
+  // w4_tile_*: K in `splits` ranges of steps_per_split steps of kW4StepK, none empty; with more than one, their
+  // f32 sums in part[splits][T][N]
+  float* part;
+  int splits, steps_per_split;
 };
 int f4_rows(hipStream_t st, const F4RowsArgs& g);
 // The same with bf16 X for any T (w4_tile_fwd), and Y[T][N] = X[T][K] . W[K][N] with W blocked along N
-// (w4_tile_dgrad).
+// (w4_tile_dgrad), in tiles of kW4TileT rows by kW4TileN columns.
+constexpr int kW4TileT = 64, kW4TileN = 128, kW4StepK = 128;
 int w4_tile_fwd(hipStream_t st, const F4RowsArgs& g);
 int w4_tile_dgrad(hipStream_t st, const F4RowsArgs& g);
+
+// bf16 y[n] = the sum of the planes part[splits][n] in order, rounded once; n % 4 == 0 (sl_gemm_f4.hip).
+int f4_join(hipStream_t st, void* y, const float* part, int64_t n, int splits);
 
 // The SL_TUNE_F8_CONFIG knob: a forced tile configuration of the block-scaled products, or -1 (sl_gemm.hip).
 int block_scaled_config();

@@ -471,15 +471,27 @@ int launch_f4(hipStream_t st, const F4Args& g) {
 
 template <bool ACC>
 int dispatch_f4(hipStream_t st, const F4Args& g) {
-  switch (g.cfg) {
-    case 0: return launch_f4<256, 256, 2, 2, ACC>(st, g);
-    case 1: return launch_f4<128, 128, 2, 2, ACC>(st, g);
-    case 2: return launch_f4<256, 128, 2, 2, ACC>(st, g);
-    default: return -1;
-  }
+  return g.cfg == 0 ? launch_f4<256, 256, 2, 2, ACC>(st, g) : launch_f4<128, 128, 2, 2, ACC>(st, g);
+}
+
+// y = the splits' sums in order, rounded once
+__global__ void __launch_bounds__(256) join_f4(const float* part, __bf16* y, int64_t n4, int splits) {
+  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= n4) return;
+  f32x4v v = reinterpret_cast<const f32x4v*>(part)[i];
+  for (int s = 1; s < splits; ++s) v += reinterpret_cast<const f32x4v*>(part)[s * n4 + i];
+  bf16x4 o;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) o[e] = static_cast<__bf16>(v[e]);
+  reinterpret_cast<bf16x4*>(y)[i] = o;
 }
 
 }  // namespace sl2
+
+int f4_join(hipStream_t st, void* y, const float* part, int64_t n, int splits) {
+  hipLaunchKernelGGL(sl2::join_f4, dim3(unsigned((n / 4 + 255) / 256)), dim3(256), 0, st, part, static_cast<__bf16*>(y), n / 4, splits);
+  return hipGetLastError() == hipSuccess ? 0 : -5;
+}
 
 int f4_gemm(hipStream_t st, const F4Args& g) { return sl2::dispatch_f4<false>(st, g); }
 

@@ -385,6 +385,9 @@ def _scratch(dev, need, workspace):
     return workspace, workspace.numel() * workspace.element_size()
 
 
+_FEW = 32  # tokens up to which the MXFP4 products need no workspace (the gradient through a frozen weight apart)
+
+
 def _want_mxfp4(q, s, names, dev):
     """Checks codes and scales against each other; returns (rows, k)."""
     if not isinstance(q, torch.Tensor) or q.dim() != 2:
@@ -454,7 +457,11 @@ def sl_mxfp4_dequantize(q, s, out=None):
     return out
 
 
-def sl_linear_fwd_mxfp4(Xq, Xs, Wq, Ws, Y=None):
+def sl_mxfp4_fwd_workspace_bytes(T: int, n_in: int, n_out: int) -> int:
+    return int(lib().sl_mxfp4_fwd_workspace_bytes(T, n_in, n_out))
+
+
+def sl_linear_fwd_mxfp4(Xq, Xs, Wq, Ws, Y=None, workspace=None):
     """Y[T,out] = deq(Xq, Xs)[T,in] . deq(Wq, Ws)[out,in]^T (bf16 out)."""
     dev = _device(Xq)
     T, n_in = _want_mxfp4(Xq, Xs, ("Xq", "Xs"), dev)
@@ -464,11 +471,18 @@ def sl_linear_fwd_mxfp4(Xq, Xs, Wq, Ws, Y=None):
         Y = torch.empty((T, n_out), dtype=BF16, device=dev)
     else:
         _want(Y, "Y", BF16, (T, n_out), dev)
-    _launch("sl_linear_fwd_mxfp4", dev, _addr(Xq), _addr(Xs), _addr(Wq), _addr(Ws), _addr(Y), T, n_in, n_out)
+    need = sl_mxfp4_fwd_workspace_bytes(T, n_in, n_out) if T > _FEW else 0
+    workspace, nbytes = _scratch(dev, need, workspace)
+    _launch("sl_linear_fwd_mxfp4", dev, _addr(Xq), _addr(Xs), _addr(Wq), _addr(Ws), _addr(Y), T, n_in, n_out,
+            _addr(workspace), nbytes)
     return Y
 
 
-def sl_linear_dgrad_mxfp4(dYq, dYs, WqT, WsT, dX=None):
+def sl_mxfp4_dgrad_workspace_bytes(T: int, n_in: int, n_out: int) -> int:
+    return int(lib().sl_mxfp4_dgrad_workspace_bytes(T, n_in, n_out))
+
+
+def sl_linear_dgrad_mxfp4(dYq, dYs, WqT, WsT, dX=None, workspace=None):
     """dX[T,in] = deq(dYq, dYs)[T,out] . deq(WqT, WsT)[in,out]^T (bf16 out)."""
     dev = _device(dYq)
     T, n_out = _want_mxfp4(dYq, dYs, ("dYq", "dYs"), dev)
@@ -478,7 +492,10 @@ def sl_linear_dgrad_mxfp4(dYq, dYs, WqT, WsT, dX=None):
         dX = torch.empty((T, n_in), dtype=BF16, device=dev)
     else:
         _want(dX, "dX", BF16, (T, n_in), dev)
-    _launch("sl_linear_dgrad_mxfp4", dev, _addr(dYq), _addr(dYs), _addr(WqT), _addr(WsT), _addr(dX), T, n_in, n_out)
+    need = sl_mxfp4_dgrad_workspace_bytes(T, n_in, n_out) if T > _FEW else 0
+    workspace, nbytes = _scratch(dev, need, workspace)
+    _launch("sl_linear_dgrad_mxfp4", dev, _addr(dYq), _addr(dYs), _addr(WqT), _addr(WsT), _addr(dX), T, n_in, n_out,
+            _addr(workspace), nbytes)
     return dX
 
 
@@ -513,7 +530,8 @@ def sl_linear_fwd_mxfp4w(X, Wq, Ws, Y=None, workspace=None):
         Y = torch.empty((T, n_out), dtype=BF16, device=dev)
     else:
         _want(Y, "Y", BF16, (T, n_out), dev)
-    workspace, nbytes = _scratch(dev, sl_mxfp4w_fwd_workspace_bytes(T, n_in, n_out), workspace)
+    need = sl_mxfp4w_fwd_workspace_bytes(T, n_in, n_out) if T > _FEW else 0
+    workspace, nbytes = _scratch(dev, need, workspace)
     _launch("sl_linear_fwd_mxfp4w", dev, _addr(X), _addr(Wq), _addr(Ws), _addr(Y), T, n_in, n_out, _addr(workspace), nbytes)
     return Y
 

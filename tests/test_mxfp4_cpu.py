@@ -115,21 +115,37 @@ def test_dequantize_validation():
 @pytest.mark.parametrize("name,dims", [("sl_linear_fwd_mxfp4", lambda k, n: (k, n)), ("sl_linear_dgrad_mxfp4", lambda k, n: (n, k))])
 def test_product_validation(name, dims):
     """dims(contracted, other) -> (in, out)"""
-    f = getattr(_lib.lib(), name)
-    assert f(None, A, A, A, A, A, 16, *dims(48, 64)) == ESHAPE                    # contracted % 32
-    assert f(None, A, A, A, A, A, 16, *dims(64, 12)) == ESHAPE                    # other % 8
-    assert f(None, A, A, A, A, A, 16, *dims(1 << 24, 64)) == ESHAPE
-    assert f(None, A, A, A, A, A, 16, *dims(64, 1 << 24)) == ESHAPE
-    assert f(None, A, A, A, A, A, -1, *dims(64, 64)) == EINVAL
-    assert f(None, A, A, A, A, A, 1 << 31, *dims(64, 64)) == ESHAPE
-    assert f(None, A, A, A, A, A, (1 << 31) - 1, *dims(64, 1 << 23)) == ESHAPE        # too many tiles
-    assert f(None, A, A, A, None, A, 16, *dims(64, 64)) == EINVAL
-    assert f(None, MIS, A, A, A, A, 16, *dims(64, 64)) == EALIGN
-    assert f(None, A, A, MIS, A, A, 16, *dims(64, 64)) == EALIGN
-    assert f(None, A, A, A, A, MIS, 16, *dims(64, 64)) == EALIGN
-    assert f(None, A, A, A, A, None, 16, *dims(0, 64)) == EINVAL
-    assert f(None, None, None, None, None, None, 0, *dims(64, 64)) == OK
-    assert f(None, None, None, None, None, None, 16, *dims(64, 0)) == OK
+    L = _lib.lib()
+    f, ws = getattr(L, name), getattr(L, f"sl_mxfp4_{name.split('_')[2]}_workspace_bytes")
+    assert f(None, A, A, A, A, A, 16, *dims(48, 64), None, 0) == ESHAPE                    # contracted % 32
+    assert f(None, A, A, A, A, A, 16, *dims(64, 12), None, 0) == ESHAPE                    # other % 8
+    assert f(None, A, A, A, A, A, 16, *dims(1 << 24, 64), None, 0) == ESHAPE
+    assert f(None, A, A, A, A, A, 16, *dims(64, 1 << 24), None, 0) == ESHAPE
+    assert f(None, A, A, A, A, A, -1, *dims(64, 64), None, 0) == EINVAL
+    assert f(None, A, A, A, A, A, 1 << 31, *dims(64, 64), None, 0) == ESHAPE
+    assert f(None, A, A, A, A, A, (1 << 31) - 1, *dims(64, 1 << 23), None, 0) == ESHAPE        # too many tiles
+    assert f(None, A, A, A, None, A, 16, *dims(64, 64), None, 0) == EINVAL
+    assert f(None, MIS, A, A, A, A, 16, *dims(64, 64), None, 0) == EALIGN
+    assert f(None, A, A, MIS, A, A, 16, *dims(64, 64), None, 0) == EALIGN
+    assert f(None, A, A, A, A, MIS, 16, *dims(64, 64), None, 0) == EALIGN
+    assert f(None, A, A, A, A, None, 16, *dims(0, 64), None, 0) == EINVAL
+    assert f(None, None, None, None, None, None, 0, *dims(64, 64), None, 0) == OK
+    assert f(None, None, None, None, None, None, 16, *dims(64, 0), None, 0) == OK
+    assert ws(16, *dims(48, 64)) == 0 and ws(0, *dims(64, 64)) == 0 and ws(1, *dims(8192, 64)) == 0
+    need = ws(200, *dims(8192, 64))                                               # few tiles, a long sum: split
+    assert need and need % (200 * 64 * 4) == 0
+    assert f(None, A, A, A, A, A, 200, *dims(8192, 64), None, 0) == EWORKSPACE
+    assert f(None, A, A, A, A, A, 200, *dims(8192, 64), A, need - 1) == EWORKSPACE
+    assert f(None, A, A, A, A, A, 200, *dims(8192, 64), MIS, need) == EWORKSPACE
+
+
+@pytest.mark.parametrize("cfg", [-1, 0, 1])
+def test_few_tokens_need_no_workspace(cfg):
+    L = _lib.lib()
+    with sl.tuning(f8=cfg):
+        for T in (1, 32):
+            assert L.sl_mxfp4_fwd_workspace_bytes(T, 16384, 64) == 0 and L.sl_mxfp4_dgrad_workspace_bytes(T, 64, 16384) == 0
+            assert L.sl_mxfp4w_fwd_workspace_bytes(T, 16384, 64) == 0
 
 
 def test_wgrad_validation():
@@ -145,6 +161,7 @@ def test_wgrad_validation():
     assert L.sl_mxfp4_wgrad_workspace_bytes(48, 64, 64) == 0 and L.sl_mxfp4_wgrad_workspace_bytes(0, 64, 64) == 0
     for T, n_in, n_out in [(8192, 2048, 1536), (4096, 256, 256), (64, 64, 64)]:
         need = L.sl_mxfp4_wgrad_workspace_bytes(T, n_in, n_out)
+        assert need or T != 4096
         assert need % (n_in * n_out * 4) == 0
         if need:
             assert w(None, A, A, A, A, A, T, n_in, n_out, None, 0) == EWORKSPACE
@@ -165,11 +182,12 @@ def test_mxfp4w_validation(which):
     assert f(None, A, MIS, A, A, 16, 64, 64, A, 1 << 40) == EALIGN
     assert f(None, None, None, None, None, 0, 64, 64, None, 0) == OK
     assert ws(16, 48, 64) == 0 and ws(0, 64, 64) == 0
-    need = ws(8192, 2048, 8192)
-    if need:
-        assert f(None, A, A, A, A, 8192, 2048, 8192, None, 0) == EWORKSPACE
-        assert f(None, A, A, A, A, 8192, 2048, 8192, A, need - 1) == EWORKSPACE
-        assert f(None, A, A, A, A, 8192, 2048, 8192, MIS, need) == EWORKSPACE
+    for T, n_in, n_out, unit in [(8192, 2048, 8192, 2048 * 8192 * 2), (100, 4096, 4096, 100 * 4096 * 4)]:
+        need = ws(T, n_in, n_out)                                                 # a bf16 weight; planes of a split sum
+        assert need and need % unit == 0
+        assert f(None, A, A, A, A, T, n_in, n_out, None, 0) == EWORKSPACE
+        assert f(None, A, A, A, A, T, n_in, n_out, A, need - 1) == EWORKSPACE
+        assert f(None, A, A, A, A, T, n_in, n_out, MIS, need) == EWORKSPACE
 
 
 def test_python_refuses_cpu_tensors():

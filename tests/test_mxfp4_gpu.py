@@ -195,7 +195,7 @@ def _bf16_exact(ref):
 # (M, N, K): one row to many, extents that fill no tile, contracted extents with whole and part groups of scales
 PRODUCTS = [(1, 8, 32), (1, 256, 2048), (2, 40, 96), (5, 1000, 1056), (16, 264, 4096), (17, 520, 544), (33, 72, 5504),
             (64, 256, 512), (65, 776, 288), (100, 1544, 1024), (128, 128, 32), (129, 136, 160), (200, 4096, 160),
-            (256, 256, 512), (257, 264, 544), (300, 2056, 1056), (1000, 776, 1056), (513, 1032, 2080), (2048, 1536, 96)]
+            (256, 256, 512), (257, 264, 544), (300, 2056, 1056), (72, 136, 4128), (130, 264, 5504), (65, 1160, 2336), (1000, 776, 1056), (513, 1032, 2080), (2048, 1536, 96)]
 
 
 @pytest.mark.parametrize("M,N,K", PRODUCTS)
@@ -303,7 +303,8 @@ def test_empty_extents():
 @pytest.mark.parametrize("T,n_in,n_out", [(1, 32, 8), (1, 2048, 512), (2, 96, 40), (3, 1056, 1000), (8, 4096, 264),
                                           (15, 544, 520), (16, 5504, 72), (17, 160, 136), (32, 1024, 776), (33, 288, 2056),
                                           (48, 2048, 128), (64, 512, 264), (65, 544, 136), (200, 1056, 4096),
-                                          (256, 256, 256), (257, 2080, 520), (1000, 1056, 776), (2049, 512, 1032)])
+                                          (256, 256, 256), (257, 2080, 520), (3, 96, 9000), (40, 8192, 136), (100, 5504, 72),
+                                          (300, 96, 5504), (1000, 1056, 776), (1023, 2080, 2056), (2049, 512, 1032)])
 def test_fwd_and_dgrad_mxfp4w(T, n_in, n_out):
     say(f"case mxfp4w T={T} in={n_in} out={n_out}")
     w = _operand(n_out, n_in, n_in)
@@ -342,6 +343,25 @@ def test_mxfp4w_non_finite(T):
     dX = host_f64(sl.sl_linear_dgrad_mxfp4w(dev_bf16(synth.f32_to_bf16_bits(dy)), *_dev(w)))
     assert (dX[0, :2] == np.inf).all() and (dX[0, 2:4] == -np.inf).all()
     assert np.isfinite(dX[1:]).all()
+
+
+@pytest.mark.parametrize("cfg,M,N,K", [(0, 1, 8, 32), (0, 4104, 4104, 544), (0, 264, 520, 8224), (1, 3, 1000, 96), (1, 2824, 2952, 288),
+                                       (1, 136, 72, 16416), (2, 264, 264, 800)])
+def test_forced_tiles(cfg, M, N, K):
+    """Either tile size on any shape: more tiles than workgroups, odd numbers of stages, split sums."""
+    say(f"case mxfp4 tiles {cfg} {M}x{N}x{K}")
+    a, b = _exact_operand(M, K, M), _exact_operand(N, K, N + 1)
+    ref = mxfp4.product(a, b)[0]
+    a, b = _dev(a), _dev(b)
+    with sl.tuning(f8=cfg):
+        Y = sl.sl_linear_fwd_mxfp4(*a, *b)
+        assert np.array_equal(host_f64(Y), bf16_bits_to_f64(_bf16_exact(ref)))
+        g = torch.ones(((M + 7) // 8 * 8, N), device="cuda")
+        pad = [torch.zeros((g.shape[0], t.shape[1]), dtype=torch.uint8, device="cuda") for t in a]
+        for p, t in zip(pad, a):
+            p[:M] = t
+        sl.sl_linear_wgrad_accum_mxfp4(*pad, *b, g)
+    assert np.array_equal(host_f64(g)[:M], ref + 1) and (g[M:] == 1).all()
 
 
 def test_results_repeat():
