@@ -10,6 +10,8 @@ from __future__ import annotations
 
 import torch
 
+from torch.autograd.function import once_differentiable
+
 from .ops import (sl_linear_dgrad, sl_linear_dgrad_mxfp4, sl_linear_fwd, sl_linear_fwd_mxfp4, sl_linear_wgrad_accum,
                   sl_linear_wgrad_accum_mxfp4, sl_mxfp4_quantize)
 
@@ -61,6 +63,7 @@ class LinearMXFP4WithGradAccumulation(torch.autograd.Function):
         return y.view(*input.shape[:-1], weight.shape[0])
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_output):
         weight, xc, xcs, wc, wcs = ctx.saved_tensors
         dy = grad_output.reshape(-1, grad_output.shape[-1]).contiguous()

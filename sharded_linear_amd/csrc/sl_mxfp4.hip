@@ -81,12 +81,13 @@ F4Args wgrad_plan(int64_t T, int64_t in, int64_t out) {
 }
 
 // bf16 rows by an MXFP4 weight: whether a bf16 copy of the weight and the bf16 product beat the tiles that expand
-// the weight as they read it.  Those do T / 64 times the work on the weight, and their second round of workgroups on
-// the chip costs more than the copy.  Input gradient (one workgroup a CU): T 512 by [11008, 4096], 256 tiles, 76 us
-// against 117; T 512 by [4096, 5504], 344 tiles, 60 against 52.  Forward (two a CU): T 512 by [11008, 4096], 688
-// tiles, 64 against 71; T 768, 1032 tiles, 102 against 89.
+// the weight as they read it, T / 64 times.  They do for many rows, and in between where the tiles take more than one
+// round on the chip.  Input gradient (one workgroup a CU): T 512 by [11008, 4096], 256 tiles, 76 us against 117; T 384
+// by [4096, 5504], 258 tiles, 58 against 52; T 200, 172 tiles, 31 against 52.  Forward (two a CU): T 512 by
+// [11008, 4096], 688 tiles, 64 against 71; T 768, 1032 tiles, 102 against 89; T 1000 by [4096, 5504], 512 tiles, 61
+// against 65.
 bool w4_by_copy(int64_t T, int64_t N, bool dgrad) {
-  return T >= 1024 || ntiles(T, N, kW4TileT, kW4TileN) > (dgrad ? 256 : 700);
+  return T >= 1024 || (T > (dgrad ? 256 : 640) && ntiles(T, N, kW4TileT, kW4TileN) > (dgrad ? 256 : 512));
 }
 
 // Split of K of those tiles, to one workgroup a CU and at least 8 steps to a split: T 64 by [8192, 2048], input

@@ -145,7 +145,7 @@ def test_few_tokens_need_no_workspace(cfg):
     with sl.tuning(f8=cfg):
         for T in (1, 32):
             assert L.sl_mxfp4_fwd_workspace_bytes(T, 16384, 64) == 0 and L.sl_mxfp4_dgrad_workspace_bytes(T, 64, 16384) == 0
-            assert L.sl_mxfp4w_fwd_workspace_bytes(T, 16384, 64) == 0
+            assert L.sl_mxfp4w_fwd_workspace_bytes(T, 16384, 64) == 0 and L.sl_mxfp4w_fwd_workspace_bytes(T, 64, 1 << 18) == 0
 
 
 def test_wgrad_validation():

@@ -291,6 +291,13 @@ def test_empty_extents():
     assert sl.sl_linear_fwd_mxfp4w(bf(0, 64), u(8, 32), u(8, 2)).shape == (0, 8)
     dX = torch.full((4, 64), 3.0, dtype=torch.bfloat16, device="cuda")
     assert not sl.sl_linear_dgrad_mxfp4w(bf(4, 0), u(0, 32), u(0, 2), dX).any()
+    for T in (100, 1100):
+        Y = torch.full((T, 8), 3.0, dtype=torch.bfloat16, device="cuda")
+        assert not sl.sl_linear_fwd_mxfp4w(bf(T, 0), u(8, 0), u(8, 0), Y).any()
+        Y.fill_(3.0)
+        assert not sl.sl_linear_fwd_mxfp4(u(T, 0), u(T, 0), u(8, 0), u(8, 0), Y).any()
+        dX = torch.full((T, 64), 3.0, dtype=torch.bfloat16, device="cuda")
+        assert not sl.sl_linear_dgrad_mxfp4w(bf(T, 0), u(0, 32), u(0, 2), dX).any()
     g = torch.ones((8, 16), device="cuda")
     sl.sl_linear_wgrad_accum_mxfp4(u(8, 0), u(8, 0), u(16, 0), u(16, 0), g)
     assert (g == 1).all()
@@ -563,6 +570,62 @@ def test_graph_replay():
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert torch.equal(a, b), k
+
+
+def test_two_graphs_of_split_products():
+    """Two captured graphs, each with split sums, replayed side by side on two streams: neither uses the other's planes."""
+    say("case mxfp4 two graphs")
+    cases = []
+    for k in range(2):
+        a, b, x = _dev(_operand(104, 8192, 10 + k)), _dev(_operand(72, 8192, 20 + k)), dev_bf16(_bits(100, 8192, k))
+        dy, wt, g = dev_bf16(_bits(100, 4096, 5 + k)), _dev(_operand(4096, 96, 30 + k)), torch.zeros((104, 72), device="cuda")
+
+        def run(a=a, b=b, x=x, dy=dy, wt=wt, g=g):
+            g.zero_()
+            sl.sl_linear_wgrad_accum_mxfp4(*a, *b, g)
+            return (sl.sl_linear_fwd_mxfp4(*a, *b), sl.sl_linear_fwd_mxfp4w(x, *b), sl.sl_linear_dgrad_mxfp4w(dy, *wt), g)
+
+        want = [t.clone() for t in run()]
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs = run()
+        cases.append((graph, outs, want))
+    assert sl.sl_mxfp4_fwd_workspace_bytes(104, 8192, 72) and sl.sl_mxfp4w_fwd_workspace_bytes(100, 8192, 72)
+    assert sl.sl_mxfp4w_dgrad_workspace_bytes(100, 96, 4096) and sl.sl_mxfp4_wgrad_workspace_bytes(8192, 72, 104)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(3):
+        torch.cuda.synchronize()
+        for (graph, outs, _want), s in zip(cases, streams):
+            with torch.cuda.stream(s):
+                for o in outs[:3]:
+                    o.fill_(float("nan"))
+                graph.replay()
+        torch.cuda.synchronize()
+        for _graph, outs, want in cases:
+            for o, w in zip(outs, want):
+                assert torch.equal(o, w)
+
+
+@pytest.mark.parametrize("T", [1, 5, 70])
+def test_many_features(T):
+    """More features than the chip has room for tiles at a time, as of a vocabulary, by few tokens."""
+    say(f"case mxfp4 vocabulary T={T}")
+    n_in, n_out = 64, 131080
+    w, xb = _exact_operand(n_out, n_in, 1), _bits(T, n_in, T)
+    _close(sl.sl_linear_fwd_mxfp4w(dev_bf16(xb), *_dev(w)), *mxfp4.product(_f64(xb), w), n_in)
+    a = _exact_operand(T, n_in, 2)
+    assert np.array_equal(host_f64(sl.sl_linear_fwd_mxfp4(*_dev(a), *_dev(w))), bf16_bits_to_f64(_bf16_exact(mxfp4.product(a, w)[0])))
+
+
+def test_second_derivatives_are_refused():
+    say("case mxfp4 second derivative")
+    xb, wb, yb, w = _layer(32, 64, 32, 5)
+    x = dev_bf16(xb).requires_grad_()
+    y = sl.linear_mxfp4_with_grad_accumulation(x, w)
+    (dx,) = torch.autograd.grad(y, x, dev_bf16(yb).requires_grad_(), create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        dx.sum().backward()
 
 
 def test_backward_capture():
