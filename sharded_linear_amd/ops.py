@@ -382,6 +382,8 @@ def _scratch(dev, need, workspace):
         with torch.cuda.device(dev):
             workspace = (torch.empty(need, dtype=U8, device=dev) if torch.cuda.is_current_stream_capturing()
                          else wgrad_workspace(dev, need))
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {dev}")
     return workspace, workspace.numel() * workspace.element_size()
 
 

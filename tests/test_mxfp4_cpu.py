@@ -148,6 +148,12 @@ def test_few_tokens_need_no_workspace(cfg):
             assert L.sl_mxfp4w_fwd_workspace_bytes(T, 16384, 64) == 0 and L.sl_mxfp4w_fwd_workspace_bytes(T, 64, 1 << 18) == 0
 
 
+def test_workspaces_of_another_device_are_refused():
+    for ws in (torch.zeros(64, dtype=torch.uint8), torch.zeros((8, 8), dtype=torch.uint8)[:, :4]):
+        with pytest.raises(ValueError, match="workspace"):
+            sl.ops._scratch(torch.device("cuda", 0) if ws.is_contiguous() else ws.device, 32, ws)
+
+
 def test_wgrad_validation():
     L = _lib.lib()
     w = L.sl_linear_wgrad_accum_mxfp4
