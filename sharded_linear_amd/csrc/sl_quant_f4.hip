@@ -121,39 +121,46 @@ constexpr uint32_t kNonFinite = 0x7F80u;       // bf16 magnitudes from here on a
 template <bool SR>
 __device__ __forceinline__ uint32_t mx4_scale(uint32_t amax, int& X) {
   X = mx4_exponent<SR>(amax);
+  if (!SR && amax == 0) X = 0;                              // padding need not take the way of the smallest blocks
   return amax >= kNonFinite ? 255u : amax ? uint32_t(X + 127) : 0u;
 }
 
-// One workgroup casts 128 x 128 elements.  Each thread loads eight 16-byte chunks, 16 adjacent lanes to
-// a tile row, so that a quad of lanes holds a row block: it shares the block's amax through two DPP
-// permutes and each lane stores its chunk's 8 codes.  For the columnwise copy the elements, and with
-// stochastic rounding their draws, are staged in LDS, half the rows at a time, and read back transposed
-// (ds_read_b64_tr_b16), a 32-row block of one column to a thread; the codes go back through LDS and
-// leave 64 bytes a column.
+// One workgroup casts 64 H x 128 elements.  Each thread loads four 16-byte chunks of every 64 rows, 16
+// adjacent lanes to a tile row, so that a quad of lanes holds a row block: it shares the block's amax
+// through two DPP permutes and each lane stores its chunk's 8 codes.  For the columnwise copy the elements,
+// and with stochastic rounding their draws, are staged in LDS, 64 rows at a time, and read back transposed
+// (ds_read_b64_tr_b16), a 32-row block of one column to a thread; the codes go back through LDS and leave
+// 32 H bytes a column.  Nearest is bound by HBM ([8192, 4096] both copies 20.0 us, 5130 GB/s; [8192, 11008]
+// 62 us, 4410 GB/s), stochastic by the generator's and the encoding's instructions ([8192, 11008] 91 us).
+//
+// H = 1 up to this many tiles of 128 rows, 4 to a CU, so that more CUs work at a time: [1536, 2048] both
+// copies 5.2 us against 5.9, [8192, 2048] (1024 tiles) 12.5 against 13.0, stochastic 21.3 against 23.9;
+// [8192, 4096] 21.0 against 20.0, and [8192, 11008], whose columns then leave in half lines, 83 against 62.
+constexpr int64_t kSmallTiles = 1024;
 constexpr int kQC = 128, kQH = 64;       // tile columns, rows of half a tile
 constexpr int kQS = kQC + 16;            // LDS row stride in elements: 4 rows x 4 column quads of a transposing read in distinct banks
 
-template <bool SR, bool ROWS, bool COLS>
+template <bool SR, bool ROWS, bool COLS, int H>
 __global__ void __launch_bounds__(256) mx4_quant_tile(F4QuantArgs a) {
   __shared__ __attribute__((aligned(16))) uint16_t tile[COLS ? kQH * kQS : 8];
   __shared__ __attribute__((aligned(16))) uint16_t dtile[COLS && SR ? kQH * kQS : 8];
   const int64_t ntc = (a.C + kQC - 1) / kQC;
   const int b = xcd_remap(int(blockIdx.x), int(gridDim.x));     // neighbours in a row of tiles share an XCD's L2
-  const int64_t r0 = b / ntc * (2 * kQH), c0 = b % ntc * kQC;
+  const int64_t r0 = b / ntc * (H * kQH), c0 = b % ntc * kQC;
   const int t = threadIdx.x, ch = t & 15;
   const uint64_t key = a.seed + (SR && a.seed_offset ? *a.seed_offset : 0);
   const int64_t nbr = (a.C + 31) / 32, nbc = (a.R + 31) / 32;   // blocks of a row, of a column
   const uint16_t* x = static_cast<const uint16_t*>(a.x);
   // chunk k of this thread: row r0 + t / 16 + 16 k, columns gc .. gc + 7
   const int64_t gr0 = r0 + (t >> 4), gc = c0 + 8 * ch, at0 = gr0 * (a.C / 8) + gc / 8, qat0 = gr0 * nbr + gc / 32;
-  const int left = int(a.R - gr0 < 128 ? a.R - gr0 : 128);      // rows from the first on
-  uint4 raw[8];
+  const int left = int(a.R - gr0 < H * kQH ? a.R - gr0 : H * kQH);      // rows from the first on
+  uint4 raw[4 * H];
 #pragma unroll
-  for (int k = 0; k < 8; ++k)                                   // C % 8 == 0: a chunk is inside or outside
+  for (int k = 0; k < 4 * H; ++k)                                   // C % 8 == 0: a chunk is inside or outside
     raw[k] = 16 * k < left && gc < a.C ? reinterpret_cast<const uint4*>(x)[at0 + k * (2 * a.C)] : make_uint4(0, 0, 0, 0);
-  uint32_t q[2][4], s[2];                                       // columnwise codes and scales, a block from each half
+  uint32_t q[H][4], s[H];                                       // columnwise codes and scales, a block from each half
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
+  for (int h = 0; h < H; ++h) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int row = (t >> 4) + 16 * k;
@@ -217,13 +224,13 @@ __global__ void __launch_bounds__(256) mx4_quant_tile(F4QuantArgs a) {
     uint8_t* const qbuf = reinterpret_cast<uint8_t*>(tile);
     uint8_t* const sbuf = qbuf + kQC * 64;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < H; ++h) {
       const int col = t & (kQC - 1), rb = 2 * h + (t >> 7);
       *reinterpret_cast<uint4*>(qbuf + col * 64 + ((rb ^ (col >> 1)) & 3) * 16) = make_uint4(q[h][0], q[h][1], q[h][2], q[h][3]);
       sbuf[col * 4 + rb] = uint8_t(s[h]);
     }
     __syncthreads();
-    const int nrb = int(nbc - r0 / 32 < 4 ? nbc - r0 / 32 : 4);   // row blocks of this tile
+    const int nrb = int(nbc - r0 / 32 < 2 * H ? nbc - r0 / 32 : 2 * H);   // row blocks of this tile
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int idx = t + 256 * h, col = idx >> 2, c = idx & 3;
@@ -273,11 +280,17 @@ __global__ void __launch_bounds__(256) mx4_dequant_bf16(const uint32_t* q, const
   }
 }
 
+template <bool SR, bool ROWS, bool COLS, int H>
+int launch_tiles(hipStream_t st, const F4QuantArgs& a) {
+  const int64_t tiles = (a.C + kQC - 1) / kQC * ((a.R + H * kQH - 1) / (H * kQH));
+  hipLaunchKernelGGL((mx4_quant_tile<SR, ROWS, COLS, H>), dim3(unsigned(tiles)), dim3(256), 0, st, a);
+  return hipGetLastError() == hipSuccess ? 0 : -5;
+}
+
 template <bool SR, bool ROWS, bool COLS>
 int launch_quant(hipStream_t st, const F4QuantArgs& a) {
   const int64_t tiles = (a.C + kQC - 1) / kQC * ((a.R + 2 * kQH - 1) / (2 * kQH));
-  hipLaunchKernelGGL((mx4_quant_tile<SR, ROWS, COLS>), dim3(unsigned(tiles)), dim3(256), 0, st, a);
-  return hipGetLastError() == hipSuccess ? 0 : -5;
+  return tiles <= kSmallTiles ? launch_tiles<SR, ROWS, COLS, 1>(st, a) : launch_tiles<SR, ROWS, COLS, 2>(st, a);
 }
 
 template <bool SR>
