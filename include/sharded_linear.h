@@ -315,7 +315,7 @@ int sl_linear_dgrad_nvfp4w(void* stream, const void* dY, const void* Wm, float w
  * Their workspaces follow the same rules: split-K planes, or for many tokens a bf16 copy of the weight.
  * Up to 32 tokens only the last of these products (dgrad through Wq) may need one.
  * The SL_TUNE_F8_CONFIG knob forces the tiles of the products of two MXFP4 operands too (0: 256x256,
- * 1: 128x128, 2: as 0), from one token on; it is read by the queries as by the calls.
+ * 1: 128x128, 2: 128x128 staged four deep), from one token on; it is read by the queries as by the calls.
  * --------------------------------------------------------------------------------------------- */
 enum { SL_ROUND_NEAREST = 0, SL_ROUND_STOCHASTIC = 1 };
 int sl_mxfp4_quantize(void* stream, const void* x, int64_t rows, int64_t cols, uint8_t* q_rows,

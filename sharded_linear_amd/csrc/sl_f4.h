@@ -38,7 +38,7 @@ struct F4Args {
   float* ws;
   int splits;           // splits of K, of kt_per_split stages each (accumulating product only)
   int kt_per_split;
-  int cfg;              // tile configuration: 0 256x256, 1 128x128
+  int cfg;              // tile configuration: 0 256x256, 1 128x128, 2 128x128 staged four deep
 };
 constexpr int kF4StageK = 256;                  // k elements of one stage
 int f4_gemm(hipStream_t st, const F4Args& g);

@@ -6,7 +6,7 @@
 // 16-byte chunk and exactly one scale block, whose scale byte the same lane supplies (any byte of a
 // register, chosen by the instruction).
 //
-// Both operands go HBM -> LDS directly, 256 k elements (128 bytes of a row) to a stage, two stages
+// Both operands go HBM -> LDS directly, 256 k elements (128 bytes of a row) to a stage, S stages
 // deep, with 16-byte chunks XOR-swizzled by row.  At the fp4 rate a 256 x 256 tile's k step of 64
 // takes 512 cycles of its four matrix units; with four waves of 128 x 128 it reads 32 KiB of
 // fragments in that time and writes 16 KiB, 75 % of the LDS's 128 bytes a cycle, where eight waves of
@@ -46,12 +46,12 @@ __device__ __forceinline__ T lds_read(uint32_t a) {
 // loads its rows' scales of 8 stages (64 bytes a row) into registers ahead of time, and they go to
 // LDS together when the 8 stages before them are done.  On the way a row's bytes are shifted into place
 // and cut at the row's end, so any K and any address takes the same path.
-template <int BM, int BN, int WGM, int WGN>
+template <int BM, int BN, int WGM, int WGN, int S>
 struct F4Layout {
   static constexpr int WAVES = WGM * WGN;
   static constexpr int kSlot = (BM + BN) * kF4Row;
   static constexpr int kRows = (BM + BN + WAVES * 64 - 1) / (WAVES * 64);   // rows of scales of a thread
-  static constexpr int kCache = 2 * kSlot;
+  static constexpr int kCache = S * kSlot;
   static constexpr int kLds = kCache + kRows * WAVES * 64 * 8 * kF4Blocks;
   static_assert(kLds <= 160 * 1024, "LDS");
 };
@@ -242,11 +242,11 @@ __device__ __forceinline__ void f4_store_f32(const F4Args& g, float* c, f32x16 (
 struct F4Item { int m0, n0, kt0, kt1, split; };
 
 // A workgroup takes several items, and the stages of one follow those of the item before without a
-// gap: during an item's last two stages the loads are the next one's, so only the results' stores
+// gap: during an item's last S stages the loads are the next one's, so only the results' stores
 // stand between the matrix instructions of two items.
-template <int BM, int BN, int WGM, int WGN, bool ACC>
+template <int BM, int BN, int WGM, int WGN, int S, bool ACC>
 __global__ void __launch_bounds__(WGM * WGN * 64) gemm_f4(F4Args g) {
-  using L = F4Layout<BM, BN, WGM, WGN>;
+  using L = F4Layout<BM, BN, WGM, WGN, S>;
   constexpr int WAVES = WGM * WGN, WM = BM / WGM, WN = BN / WGN, TM = WM / 32, TN = WN / 32;
   using SA = F4Side<BM, WAVES>;
   using SB = F4Side<BN, WAVES>;
@@ -329,15 +329,18 @@ __global__ void __launch_bounds__(WGM * WGN * 64) gemm_f4(F4Args g) {
     lend = it.kt1;
   };
 
-  // One stage, in slot P.  u: the next stage's place in its scale group.  No branch stands inside (loads
+  // One stage, in slot P of two, or in the slot at `slot`.  u: the next stage's place in its scale group.  No branch stands inside (loads
   // past the last stage read out of range, reads past it are not used): the fixed order below holds
   // within a basic block.
   constexpr int kReads = TM + TN, kMfma = TM * TN, kLoads = SA::kLoads + SB::kLoads;
   i32x4 fa[2][TM], fb[2][TN];
   int sca[TM], scb[TN];
+  uint32_t slot = 0;
   auto stage = [&](int u, auto par) __attribute__((always_inline)) {
     constexpr int P = decltype(par)::value;
-    const uint32_t cur = P * L::kSlot, nxt = L::kSlot - cur;
+    const uint32_t cur = S == 2 ? uint32_t(P * L::kSlot) : slot;
+    const uint32_t nxt = S == 2 ? L::kSlot - cur : cur == (S - 1) * L::kSlot ? 0 : cur + L::kSlot;
+    slot = nxt;
     i32x2 na[TM], nb[TN];
     static_for<4>([&](auto kc) {
       constexpr int ks = decltype(kc)::value, p = ks & 1;
@@ -345,7 +348,7 @@ __global__ void __launch_bounds__(WGM * WGN * 64) gemm_f4(F4Args g) {
       if constexpr (ks == 3) {
         // this wave has read all of its slot, and its loads of the next stage have landed
         wait_lgkm0();
-        wait_vmcnt<0>();
+        wait_vmcnt<(S - 2) * kLoads>();
         bare_barrier();
         oa = lkt < lend ? a.at(lkt) : kOOB;
         ob = lkt < lend ? b.at(lkt) : kOOB;
@@ -386,19 +389,20 @@ __global__ void __launch_bounds__(WGM * WGN * 64) gemm_f4(F4Args g) {
   };
 
   F4Item cur = item(x);
-  auto load_stage = [&](uint32_t slot) {
+  auto load_stage = [&](uint32_t to) {
     const uint32_t oa = lkt < lend ? a.at(lkt) : kOOB, ob = lkt < lend ? b.at(lkt) : kOOB;
     ++lkt;
 #pragma unroll
-    for (int it = 0; it < SA::kLoads; ++it) a.load(slot, oa, it, wave);
+    for (int it = 0; it < SA::kLoads; ++it) a.load(to, oa, it, wave);
 #pragma unroll
-    for (int it = 0; it < SB::kLoads; ++it) b.load(slot + BM * kF4Row, ob, it, wave);
+    for (int it = 0; it < SB::kLoads; ++it) b.load(to + BM * kF4Row, ob, it, wave);
   };
   load_scales(cur, cur.kt0);
   load_from(cur);
   load_stage(lds);
   wait_vmcnt<0>();
-  load_stage(lds + L::kSlot);
+#pragma unroll
+  for (int i = 1; i < S; ++i) load_stage(lds + i * L::kSlot);
   store_scales();
   wait_lgkm0();
   bare_barrier();
@@ -417,7 +421,7 @@ __global__ void __launch_bounds__(WGM * WGN * 64) gemm_f4(F4Args g) {
     const F4Item nx = item(more ? x : x - stride);
     // Stages in pairs: an odd last one is followed by one of zeros (an empty K is a pair of zeros), so
     // that the accumulators stay in place.
-    const int nk = max(2, (cur.kt1 - cur.kt0 + 1) & ~1);
+    const int nk = max(S, (cur.kt1 - cur.kt0 + 1) & ~1);
     // a zero that is made here: a constant one is kept in registers of its own and copied
     const float zero = __int_as_float(here(0));
 #pragma unroll
@@ -432,7 +436,7 @@ __global__ void __launch_bounds__(WGM * WGN * 64) gemm_f4(F4Args g) {
         if (k + 8 < nk) load_scales(cur, cur.kt0 + k + 8);
         else load_scales(nx, nx.kt0);
       }
-      if (last) {
+      if (k + S == nk) {                                         // from this stage on the loads are the next item's
         load_from(nx);
         if (!more) lend = lkt;
       }
@@ -457,11 +461,11 @@ __global__ void __launch_bounds__(WGM * WGN * 64) gemm_f4(F4Args g) {
   wait_vmcnt<0>();   // loads past the end still write zeros to LDS
 }
 
-template <int BM, int BN, int WGM, int WGN, bool ACC>
+template <int BM, int BN, int WGM, int WGN, int S, bool ACC>
 int launch_f4(hipStream_t st, const F4Args& g) {
-  constexpr int lds = F4Layout<BM, BN, WGM, WGN>::kLds;
+  constexpr int lds = F4Layout<BM, BN, WGM, WGN, S>::kLds;
   constexpr int kResident = 256 * (160 * 1024 / lds);            // workgroups on the 256 CUs at a time
-  auto kfn = gemm_f4<BM, BN, WGM, WGN, ACC>;
+  auto kfn = gemm_f4<BM, BN, WGM, WGN, S, ACC>;
   static std::atomic<uint64_t> attr{0};
   if (smem_attr_once(reinterpret_cast<const void*>(kfn), lds, attr)) return -5;
   const int64_t items = (g.M + BM - 1) / BM * ((g.N + BN - 1) / BN) * (ACC ? g.splits : 1);
@@ -471,7 +475,11 @@ int launch_f4(hipStream_t st, const F4Args& g) {
 
 template <bool ACC>
 int dispatch_f4(hipStream_t st, const F4Args& g) {
-  return g.cfg == 0 ? launch_f4<256, 256, 2, 2, ACC>(st, g) : launch_f4<128, 128, 2, 2, ACC>(st, g);
+  switch (g.cfg) {
+    case 0: return launch_f4<256, 256, 2, 2, 2, ACC>(st, g);
+    case 1: return launch_f4<128, 128, 2, 2, 2, ACC>(st, g);
+    default: return launch_f4<128, 128, 2, 2, 4, ACC>(st, g);
+  }
 }
 
 // y = the splits' sums in order, rounded once

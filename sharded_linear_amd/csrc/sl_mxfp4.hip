@@ -31,12 +31,6 @@ int64_t ntiles(int64_t M, int64_t N, int bm, int bn) { return (M + bm - 1) / bm 
 // sl_tile_w4.hip, by [4096, 5504] 13.2 against 13.6; 48 rows 20.6 against 18.1 and 21.3 against 14.5.
 constexpr int64_t kFewRows = 64, kFewRowsBf16 = 32;
 
-// A forced tile configuration, or -1.  There are two: the knob's third stands for the first.
-int forced_config() {
-  const int c = block_scaled_config();
-  return c == 2 ? 0 : c;
-}
-
 // Splits of K over `stages` for a grid of `tiles`: up to `slots` workgroups, at least `least` stages to a split (an
 // even number: the kernel starts at an even stage) and at most 16 splits.
 void split_k(F4Args& g, int64_t tiles, int64_t slots, int least) {
@@ -51,6 +45,14 @@ void split_k(F4Args& g, int64_t tiles, int64_t slots, int least) {
   g.splits = stages ? int((stages + per - 1) / per) : 1;
 }
 
+// 128x128 tiles two stages deep, of which two workgroups fit on a CU, or four stages deep, one to a CU: where there
+// is about one to a CU anyway and its sum is long.  [1536, 2048] over 8192 tokens, 192 tiles of 32 stages, 29.2 us
+// against 32.6; [2048, 4096] (512 tiles) 58.0 against 53.1; [1024, 1024] over 4096 (256 of 4 stages) the same.
+int small_tiles(const F4Args& g, int64_t tiles) {
+  const int64_t items = tiles * g.splits, stages = (g.K + kF4StageK - 1) / kF4StageK;
+  return items > 128 && items <= 256 && stages >= 16 * g.splits ? 2 : 1;
+}
+
 size_t planes_bytes(const F4Args& g) { return g.splits > 1 ? size_t(g.splits) * size_t(g.M) * size_t(g.N) * 4 : 0; }
 
 // Tiles of a bf16 result: 256x256 where they fill most of the 256 CUs, else 128x128 (2048 rows by [4096, 4096], 128
@@ -60,10 +62,11 @@ size_t planes_bytes(const F4Args& g) { return g.splits > 1 ? size_t(g.splits) * 
 F4Args product_plan(int64_t M, int64_t N, int64_t K) {
   F4Args g{};
   g.M = M; g.N = N; g.K = K;
-  const int forced = forced_config();
+  const int forced = block_scaled_config();
   g.cfg = forced >= 0 ? forced : ntiles(M, N, 256, 256) >= 200 ? 0 : 1;
   const int64_t tiles = g.cfg == 0 ? ntiles(M, N, 256, 256) : ntiles(M, N, 128, 128);
   split_k(g, tiles, M > kFewRows && K > 31 * kF4StageK ? 256 : 0, 8);
+  if (forced < 0 && g.cfg == 1) g.cfg = small_tiles(g, tiles);
   return g;
 }
 
@@ -73,10 +76,11 @@ F4Args wgrad_plan(int64_t T, int64_t in, int64_t out) {
   F4Args g{};
   g.M = out; g.N = in; g.K = T;
   const int64_t t256 = ntiles(out, in, 256, 256);
-  const int forced = forced_config();
+  const int forced = block_scaled_config();
   g.cfg = forced >= 0 ? forced : t256 > 128 ? 0 : 1;
   const int64_t tiles = g.cfg == 0 ? t256 : ntiles(out, in, 128, 128);
   split_k(g, tiles, 256 + tiles / 2, 4);
+  if (forced < 0 && g.cfg == 1) g.cfg = small_tiles(g, tiles);
   return g;
 }
 

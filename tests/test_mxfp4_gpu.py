@@ -353,7 +353,8 @@ def test_mxfp4w_non_finite(T):
 
 
 @pytest.mark.parametrize("cfg,M,N,K", [(0, 1, 8, 32), (0, 4104, 4104, 544), (0, 264, 520, 8224), (1, 3, 1000, 96), (1, 2824, 2952, 288),
-                                       (1, 136, 72, 16416), (2, 264, 264, 800)])
+                                       (1, 136, 72, 16416), (2, 1, 8, 32), (2, 264, 264, 800), (2, 2056, 2184, 288),
+                                       (2, 2056, 2184, 1056), (2, 136, 72, 16416), (2, 2824, 2952, 1312)])
 def test_forced_tiles(cfg, M, N, K):
     """Either tile size on any shape: more tiles than workgroups, odd numbers of stages, split sums."""
     say(f"case mxfp4 tiles {cfg} {M}x{N}x{K}")
