@@ -16,6 +16,10 @@
 // fragments of a stage's last step are in registers before its MFMAs start, so the barrier that
 // hands the stage's slot over stands there, and the first fragments of the next stage and the loads of the
 // stage after it are issued between that last step's MFMAs.
+//
+// Measured: [8192, 4096] over 11008 184 us, 4.0 PFLOP/s; [8192, 8192] over 2048 85 us, 3.2 PFLOP/s, of which the
+// results' 134 MB take 26; accumulating [11008, 4096] over 8192 237 us.  A loop of these MFMAs alone holds 6.4
+// PFLOP/s (1.5-1.6 GHz, the power limit), this one without its loads 4.2-4.5.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>

@@ -12,6 +12,9 @@
 //     registers (exact).  For that the four lanes of a row trade dwords, so that each holds 8 elements of
 //     every block: X is then read 64 contiguous bytes to a row, as W is.  With the codes left where they
 //     are loaded, X came in 16-byte pieces 64 bytes apart, four times the cache accesses.
+//
+// Measured: one token by [8192, 2048] 4.7 us with bf16 X, by [6144, 4096] 5.3 us with MXFP4 X (2.5 TB/s); 16 tokens
+// by [11008, 4096] with bf16 X 10.6 us (2.3 TB/s).
 #include <hip/hip_runtime.h>
 
 #include <cstdint>

@@ -619,6 +619,49 @@ def test_many_features(T):
     assert np.array_equal(host_f64(sl.sl_linear_fwd_mxfp4(*_dev(a), *_dev(w))), bf16_bits_to_f64(_bf16_exact(mxfp4.product(a, w)[0])))
 
 
+def _device_operand(rows, k, seed):
+    """Random codes under scale 1, made on the device."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return (torch.randint(0, 256, (rows, k // 2), dtype=torch.uint8, device="cuda", generator=g),
+            torch.full((rows, k // 32), 127, dtype=torch.uint8, device="cuda"))
+
+
+def test_products_large_index():
+    """Results, weights and gradients past 2^31 elements: their ends are those of the same product of the last rows alone.
+    Sums of multiples of 1/4 below 2^22 are exact, so the kernels that the sizes choose agree to the bit."""
+    say("case mxfp4 large products")
+    a, b = _device_operand(300008, 64, 1), _device_operand(7304, 64, 2)
+    Y = sl.sl_linear_fwd_mxfp4(*a, *b)
+    assert Y.numel() > 2**31
+    assert torch.equal(Y[-50:], sl.sl_linear_fwd_mxfp4(a[0][-50:], a[1][-50:], *b))
+    assert torch.equal(Y[:50], sl.sl_linear_fwd_mxfp4(a[0][:50], a[1][:50], *b))
+    del Y
+    X = torch.randint(-1, 2, (300008, 64), device="cuda").bfloat16()
+    Y = sl.sl_linear_fwd_mxfp4w(X, *b)
+    assert torch.equal(Y[-50:], sl.sl_linear_fwd_mxfp4w(X[-50:], *b))
+    del Y, X
+    a, b = _device_operand(32776, 32, 3), _device_operand(65544, 32, 4)
+    g = torch.ones((32776, 65544), device="cuda")
+    sl.sl_linear_wgrad_accum_mxfp4(*a, *b, g)
+    end = torch.ones((264, 65544), device="cuda")
+    sl.sl_linear_wgrad_accum_mxfp4(a[0][-264:], a[1][-264:], *b, end)
+    assert torch.equal(g[-264:], end)
+    del g, end
+    n_out, n_in = 131080, 65568                                    # more than 2^32 bytes of codes
+    w = _device_operand(n_out, n_in, 5)
+    assert w[0].numel() > 2**32
+    last = w[0][-256:], w[1][-256:]
+    for T in (2, 70):
+        X = torch.randint(-1, 2, (T, n_in), device="cuda").bfloat16()
+        assert torch.equal(sl.sl_linear_fwd_mxfp4w(X, *w)[:, -256:], sl.sl_linear_fwd_mxfp4w(X, *last)), T
+        a = _device_operand(T, n_in, 6)
+        assert torch.equal(sl.sl_linear_fwd_mxfp4(*a, *w)[:, -256:], sl.sl_linear_fwd_mxfp4(*a, *last)), T
+        dY = torch.randint(-1, 2, (T, n_out), device="cuda").bfloat16()
+        cols = w[0][:, -32:].contiguous(), w[1][:, -2:].contiguous()
+        assert torch.equal(sl.sl_linear_dgrad_mxfp4w(dY, *w)[:, -64:], sl.sl_linear_dgrad_mxfp4w(dY, *cols)), T
+
+
 def test_second_derivatives_are_refused():
     say("case mxfp4 second derivative")
     xb, wb, yb, w = _layer(32, 64, 32, 5)
