@@ -62,15 +62,14 @@ __device__ __forceinline__ uint32_t signs8(const uint32_t (&w)[4]) {
   return (even >> 4) | odd;
 }
 
-// The magnitude's code of x with |x| / 2^X = v, stochastic; r6: the draw times 2^6.  From 1 on, the codes
-// order like the fp32 bits of v with one mantissa bit left (bits 22 and up, whose low three are the
-// code where the bits are those of 2^18 v), so adding the draw below that bit and cutting there is the rule (a
-// bf16's mantissa has no bits below the draw's); below 1 the step is fixed and 2^18 v an integer's worth.
-__device__ __forceinline__ uint32_t e2m1_stochastic(float x, int X, uint32_t r6) {
-  const float v = __builtin_ldexpf(__builtin_fabsf(x), 18 - X);
-  const uint32_t big = __float_as_uint(v) + r6, small = (uint32_t(v) << 5) + r6;
-  return (v >= 262144.f ? big : small) >> 22;               // above the code's 3 bits, bit 25 is 0 and the others are cut off
+// The magnitude's code of x with |x| / 2^X = v, stochastic, r its draw.  E2M1's magnitudes in order are the
+// fp32 numbers 0, 2^-127, 2^-126 and 1.5, 2, 3, 4, 6 times 2^-126, which have one mantissa bit and, below
+// 2^-126, the fixed step of a subnormal as E2M1 has below 1: the bits from 22 up are the code.  So the draw is added
+// below that bit of 2^-126 v, which is cut off at 2^-149 (the kernel rounds toward zero), far below the draw's last bit.
+__device__ __forceinline__ uint32_t e2m1_stochastic(float x, int X, uint32_t r) {
+  return (__float_as_uint(__builtin_ldexpf(__builtin_fabsf(x), -126 - X)) + (r << 6)) >> 22;
 }
+__device__ __forceinline__ void round_toward_zero() { __builtin_amdgcn_s_setreg(1 | 1 << 11, 3); }  // MODE bits 0..1: fp32 rounding
 
 // Shared exponent of a block whose largest magnitude has the bf16 bits amax (finite, not zero).  A
 // subnormal amax counts as 2^-127, which the clamp makes right.
@@ -91,8 +90,8 @@ __device__ __forceinline__ uint32_t mx4_codes(uint32_t w0, uint32_t w1, uint32_t
     const uint32_t d[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {                             // each code enters at the top
-      q = __builtin_amdgcn_alignbit(e2m1_stochastic(bf16_lo(w[i]), X, (d[i] << 6) & 0x3FFFC0u), q, 4);
-      q = __builtin_amdgcn_alignbit(e2m1_stochastic(bf16_hi(w[i]), X, (d[i] >> 10) & 0x3FFFC0u), q, 4);
+      q = __builtin_amdgcn_alignbit(e2m1_stochastic(bf16_lo(w[i]), X, d[i] & 0xFFFFu), q, 4);
+      q = __builtin_amdgcn_alignbit(e2m1_stochastic(bf16_hi(w[i]), X, d[i] >> 16), q, 4);
     }
     q |= signs8(w);
   } else {
@@ -131,10 +130,10 @@ __device__ __forceinline__ uint32_t mx4_scale(uint32_t amax, int& X) {
 // and with stochastic rounding their draws, are staged in LDS, 64 rows at a time, and read back transposed
 // (ds_read_b64_tr_b16), a 32-row block of one column to a thread; the codes go back through LDS and leave
 // 32 H bytes a column.  Nearest is bound by HBM ([8192, 4096] both copies 20.0 us, 5130 GB/s; [8192, 11008]
-// 62 us, 4410 GB/s), stochastic by the generator's and the encoding's instructions ([8192, 11008] 91 us).
+// 62 us, 4410 GB/s), stochastic by the generator's and the encoding's instructions ([8192, 11008] 77 us).
 //
 // H = 1 up to this many tiles of 128 rows, 4 to a CU, so that more CUs work at a time: [1536, 2048] both
-// copies 5.2 us against 5.9, [8192, 2048] (1024 tiles) 12.5 against 13.0, stochastic 21.3 against 23.9;
+// copies 5.2 us against 5.9, [8192, 2048] (1024 tiles) 12.5 against 13.0;
 // [8192, 4096] 21.0 against 20.0, and [8192, 11008], whose columns then leave in half lines, 83 against 62.
 constexpr int64_t kSmallTiles = 1024;
 constexpr int kQC = 128, kQH = 64;       // tile columns, rows of half a tile
@@ -158,6 +157,7 @@ __global__ void __launch_bounds__(256) mx4_quant_tile(F4QuantArgs a) {
 #pragma unroll
   for (int k = 0; k < 4 * H; ++k)                                   // C % 8 == 0: a chunk is inside or outside
     raw[k] = 16 * k < left && gc < a.C ? reinterpret_cast<const uint4*>(x)[at0 + k * (2 * a.C)] : make_uint4(0, 0, 0, 0);
+  if constexpr (SR) round_toward_zero();                        // behind the index division, which uses fp32 itself
   uint32_t q[H][4], s[H];                                       // columnwise codes and scales, a block from each half
 #pragma unroll
   for (int h = 0; h < H; ++h) {

@@ -79,6 +79,23 @@ def test_cast_shapes(rows, cols, seed):
     _check_cast(_bits(rows, cols, rows + cols), seed)
 
 
+@pytest.mark.parametrize("scale", [1.0, 2.0 ** 100, 2.0 ** -60, 2.0 ** -123])
+def test_cast_largest_draws_on_the_smallest_values(scale):
+    """Where the draw is 2^16 - 1 a value of one draw's unit rounds up and anything less does not: values on both sides of
+    it, down to what only a cut, not a rounding, of v keeps apart."""
+    say(f"case cast largest draws scale={scale}")
+    rows, cols, key = 1024, 1024, 7
+    at = np.argwhere(mxfp4.draws(rows, cols, key) == 65535)
+    at = at[(at % 32 != 0).all(1)]
+    assert len(at) > 8
+    x = np.zeros((rows, cols), np.float32)
+    x[::32, :], x[:, ::32] = 6, 6                                # v = x in every block, by rows and by columns
+    unit = 2.0 ** -17                                             # of the draw where the step is 0.5
+    for k, (i, j) in enumerate(at):
+        x[i, j] = unit * (255 / 256, 1, 129 / 128, 2.0 ** -9, 127 / 128, 255 / 128, 255 / 1024, -255 / 256)[k % 8]
+    _check_cast(synth.f32_to_bf16_bits((x * np.float32(scale)).astype(np.float32)), key)
+
+
 def test_cast_zero_and_non_finite_blocks():
     say("case cast zero / non-finite blocks")
     b = _bits(96, 96, 3)
