@@ -26,6 +26,8 @@
 
 namespace sl2 {
 
+__device__ __forceinline__ uint32_t xor3(uint32_t a, uint32_t b, uint32_t c) { return __builtin_amdgcn_bitop3_b32(a, b, c, 0x96); }
+
 // 16-bit draws of the 8 elements of group g, two to a word, element 2i in the low half of word i.
 __device__ __forceinline__ uint4 philox7(uint64_t g, uint64_t key) {
   uint32_t c0 = uint32_t(g), c1 = uint32_t(g >> 32), c2 = 0, c3 = 0;
@@ -33,9 +35,9 @@ __device__ __forceinline__ uint4 philox7(uint64_t g, uint64_t key) {
 #pragma unroll
   for (int i = 0; i < 7; ++i) {
     const uint64_t p0 = uint64_t(0xD2511F53u) * c0, p1 = uint64_t(0xCD9E8D57u) * c2;
-    c0 = uint32_t(p1 >> 32) ^ c1 ^ k0;
+    c0 = xor3(uint32_t(p1 >> 32), c1, k0);
     c1 = uint32_t(p1);
-    c2 = uint32_t(p0 >> 32) ^ c3 ^ k1;
+    c2 = xor3(uint32_t(p0 >> 32), c3, k1);
     c3 = uint32_t(p0);
     k0 += 0x9E3779B9u;
     k1 += 0xBB67AE85u;
@@ -62,12 +64,18 @@ __device__ __forceinline__ uint32_t signs8(const uint32_t (&w)[4]) {
   return (even >> 4) | odd;
 }
 
-// The magnitude's code of x with |x| / 2^X = v, stochastic, r its draw.  E2M1's magnitudes in order are the
+// The magnitude's code of x with |x| / 2^X = v, stochastic.  E2M1's magnitudes in order are the
 // fp32 numbers 0, 2^-127, 2^-126 and 1.5, 2, 3, 4, 6 times 2^-126, which have one mantissa bit and, below
 // 2^-126, the fixed step of a subnormal as E2M1 has below 1: the bits from 22 up are the code.  So the draw is added
 // below that bit of 2^-126 v, which is cut off at 2^-149 (the kernel rounds toward zero), far below the draw's last bit.
-__device__ __forceinline__ uint32_t e2m1_stochastic(float x, int X, uint32_t r) {
-  return (__float_as_uint(__builtin_ldexpf(__builtin_fabsf(x), -126 - X)) + (r << 6)) >> 22;
+// draws: two of them, HI the upper one's, taken as it is by a 16-bit multiply-add.
+template <bool HI>
+__device__ __forceinline__ uint32_t e2m1_stochastic(float x, int X, uint32_t draws) {
+  const uint32_t v = __float_as_uint(__builtin_ldexpf(__builtin_fabsf(x), -126 - X));
+  uint32_t s;
+  if constexpr (HI) asm("v_mad_u32_u16 %0, %1, 64, %2 op_sel:[1,0,0,0]" : "=v"(s) : "v"(draws), "v"(v));
+  else asm("v_mad_u32_u16 %0, %1, 64, %2" : "=v"(s) : "v"(draws), "v"(v));
+  return s >> 22;
 }
 __device__ __forceinline__ void round_toward_zero() { __builtin_amdgcn_s_setreg(1 | 1 << 11, 3); }  // MODE bits 0..1: fp32 rounding
 
@@ -90,8 +98,8 @@ __device__ __forceinline__ uint32_t mx4_codes(uint32_t w0, uint32_t w1, uint32_t
     const uint32_t d[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {                             // each code enters at the top
-      q = __builtin_amdgcn_alignbit(e2m1_stochastic(bf16_lo(w[i]), X, d[i] & 0xFFFFu), q, 4);
-      q = __builtin_amdgcn_alignbit(e2m1_stochastic(bf16_hi(w[i]), X, d[i] >> 16), q, 4);
+      q = __builtin_amdgcn_alignbit(e2m1_stochastic<false>(bf16_lo(w[i]), X, d[i]), q, 4);
+      q = __builtin_amdgcn_alignbit(e2m1_stochastic<true>(bf16_hi(w[i]), X, d[i]), q, 4);
     }
     q |= signs8(w);
   } else {
@@ -130,7 +138,7 @@ __device__ __forceinline__ uint32_t mx4_scale(uint32_t amax, int& X) {
 // and with stochastic rounding their draws, are staged in LDS, 64 rows at a time, and read back transposed
 // (ds_read_b64_tr_b16), a 32-row block of one column to a thread; the codes go back through LDS and leave
 // 32 H bytes a column.  Nearest is bound by HBM ([8192, 4096] both copies 20.0 us, 5130 GB/s; [8192, 11008]
-// 62 us, 4410 GB/s), stochastic by the generator's and the encoding's instructions ([8192, 11008] 77 us).
+// 62 us, 4410 GB/s), stochastic by the generator's and the encoding's instructions ([8192, 11008] 75 us).
 //
 // H = 1 up to this many tiles of 128 rows, 4 to a CU, so that more CUs work at a time: [1536, 2048] both
 // copies 5.2 us against 5.9, [8192, 2048] (1024 tiles) 12.5 against 13.0;
