@@ -313,7 +313,7 @@ int sl_linear_dgrad_nvfp4w(void* stream, const void* dY, const void* Wm, float w
  * weights; every dequantised weight must be a finite bf16 value or a NaN:
  *   fwd:   Y[T,out] = X[T,in] . deq(Wq)[out,in]^T        dgrad: dX[T,in] = dY[T,out] . deq(Wq)
  * Their workspaces follow the same rules: split-K planes, or for many tokens a bf16 copy of the weight.
- * Up to 32 tokens only the last of these products (dgrad through Wq) may need one.
+ * Up to 16 tokens only the last of these products (dgrad through Wq) may need one.
  * The SL_TUNE_F8_CONFIG knob forces the tiles of the products of two MXFP4 operands too (0: 256x256,
  * 1: 128x128, 2: 128x128 staged four deep), from one token on; it is read by the queries as by the calls.
  * --------------------------------------------------------------------------------------------- */

@@ -44,7 +44,7 @@ constexpr int kF4StageK = 256;                  // k elements of one stage
 int f4_gemm(hipStream_t st, const F4Args& g);
 int f4_accum(hipStream_t st, const F4Args& g);
 
-// Y[T][N] = X . W^T for few rows T: X bf16 (xs null) or MXFP4, W MXFP4, both blocked along K; T below 2^20.
+// Y[T][N] = X . W^T for few rows T: X bf16 (xs null) or MXFP4, W MXFP4, both blocked along K; up to 32 rows of bf16.
 struct F4RowsArgs {
   const void *x, *xs, *w, *ws;
   void* y;

@@ -27,9 +27,11 @@ int check_grid(int64_t M, int64_t N) { return (M + 63) / 64 * ((N + 63) / 64) < 
 int64_t ntiles(int64_t M, int64_t N, int bm, int bn) { return (M + bm - 1) / bm * ((N + bn - 1) / bn); }
 
 // Rows up to which a product goes to the few-row kernel.  MXFP4 rows: 64 by [11008, 4096] 12.0 us there, 12.7 in
-// 128x128 tiles; by [8192, 2048] 6.1 against 8.2.  bf16 rows: 32 by [11008, 4096] 14.4 us there, 17.8 in the tiles of
-// sl_tile_w4.hip, by [4096, 5504] 13.2 against 13.6; 48 rows 20.6 against 18.1 and 21.3 against 14.5.
-constexpr int64_t kFewRows = 64, kFewRowsBf16 = 32;
+// 128x128 tiles; by [8192, 2048] 6.1 against 8.2.  bf16 rows, of which every workgroup reads all: 16 by [4096, 11008]
+// 15.2 us there, 15.7 in the tiles of sl_tile_w4.hip; 32 by [11008, 4096] 14.7 against 17.5, by [4096, 5504] 13.3
+// against 13.5, by [2048, 8192] 18.7 against 13.2; 48 by [11008, 4096] 20.6 against 18.1.
+constexpr int64_t kFewRows = 64;
+bool few_rows_bf16(int64_t T, int64_t K) { return T <= 16 || (T <= 32 && K <= 6144); }
 
 // Splits of K over `stages` for a grid of `tiles`: up to `slots` workgroups, at least `least` stages to a split (an
 // even number: the kernel starts at an even stage) and at most 16 splits.
@@ -228,7 +230,7 @@ size_t w4_workspace(int64_t T, int64_t in, int64_t out, bool dgrad) {
   if (check_product(T, in, out, in) || T == 0 || in == 0 || out == 0) return 0;
   const int64_t N = dgrad ? in : out;
   if (w4_by_copy(T, N, dgrad)) return size_t(out) * size_t(in) * 2;
-  if (!dgrad && T <= kFewRowsBf16) return 0;
+  if (!dgrad && few_rows_bf16(T, in)) return 0;
   const F4RowsArgs g = w4_args(nullptr, nullptr, nullptr, nullptr, T, N, dgrad ? out : in);
   return g.splits > 1 ? size_t(g.splits) * size_t(T) * size_t(N) * 4 : 0;
 }
@@ -247,7 +249,7 @@ int w4_product(void* stream, const void* x, const uint8_t* Wq, const uint8_t* Ws
   if (!w4_by_copy(T, N, dgrad)) {
     F4RowsArgs g = w4_args(x, Wq, Ws, y, T, N, K);
     g.part = static_cast<float*>(workspace);
-    return (dgrad ? w4_tile_dgrad(hs, g) : T <= kFewRowsBf16 ? f4_rows(hs, g) : w4_tile_fwd(hs, g)) == 0 ? SL_OK : SL_EHIP;
+    return (dgrad ? w4_tile_dgrad(hs, g) : few_rows_bf16(T, K) ? f4_rows(hs, g) : w4_tile_fwd(hs, g)) == 0 ? SL_OK : SL_EHIP;
   }
   if (K > 0 && f4_dequantize(hs, Wq, Ws, workspace, out, in)) return SL_EHIP;
   return (dgrad ? sl_linear_dgrad : sl_linear_fwd)(stream, x, workspace, y, T, in, out);

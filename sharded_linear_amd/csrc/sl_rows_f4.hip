@@ -119,6 +119,7 @@ __global__ void __launch_bounds__(kRowWaves * 64) rows_f4(F4RowsArgs g) {
       }
       if constexpr (!XBF) load_scales(xs[j], 4 * s0, nb, sx[j]);
     }
+    if constexpr (XBF && U == 4) __builtin_amdgcn_sched_barrier(0);     // all on their way before the first is used
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -176,7 +177,9 @@ int launch_rows(hipStream_t st, const F4RowsArgs& g) {
 // R: the 16-row groups of W that give each of the 256 CUs one workgroup.  Fewer would need a second
 // round, more would leave CUs without one: 16 tokens on [11008, 4096] (688 groups) took 17.3, 15.6,
 // 11.3 and 13.0 us with bf16 X and R = 1, 2, 3 and 4, on [6144, 4096] (384) 12.3, 9.1, 11.0 and 12.8.
-// U: 4 steps in flight with MXFP4 X; 2 with bf16 X, whose registers hold 4 KiB a step (1 with 64 tokens).
+// U: 4 steps in flight with MXFP4 X; with bf16 X, whose registers hold 4 KiB a step, 2, and 4 for
+// up to 4 tokens where 2 would need a second round of loads: one token by [4096, 5504] 5.9 us with 2, 5.3 with 4, by
+// [2048, 8192] 7.1 and 6.4, but 8 by [4096, 11008] 11.7 and 12.3.
 template <bool XBF, int TN, int U>
 int dispatch_r(hipStream_t st, const F4RowsArgs& g) {
   const int64_t groups = (g.N + 15) / 16;
@@ -188,9 +191,12 @@ int dispatch_r(hipStream_t st, const F4RowsArgs& g) {
 
 template <bool XBF>
 int dispatch_rows(hipStream_t st, const F4RowsArgs& g) {
-  if (g.T <= 16) return dispatch_r<XBF, 1, XBF ? 2 : 4>(st, g);
-  if (g.T <= 32) return dispatch_r<XBF, 2, XBF ? 2 : 4>(st, g);
-  return dispatch_r<XBF, 4, XBF ? 1 : 4>(st, g);
+  if constexpr (XBF) {                                           // up to 32 rows
+    if (g.T > 16) return dispatch_r<XBF, 2, 2>(st, g);
+    return g.T <= 4 && g.K > kRowWaves * 2 * 128 ? dispatch_r<XBF, 1, 4>(st, g) : dispatch_r<XBF, 1, 2>(st, g);
+  } else {
+    return g.T <= 16 ? dispatch_r<XBF, 1, 4>(st, g) : g.T <= 32 ? dispatch_r<XBF, 2, 4>(st, g) : dispatch_r<XBF, 4, 4>(st, g);
+  }
 }
 
 }  // namespace sl2

@@ -387,7 +387,7 @@ def _scratch(dev, need, workspace):
     return workspace, workspace.numel() * workspace.element_size()
 
 
-_FEW = 32  # tokens up to which the MXFP4 products need no workspace (the gradient through a frozen weight apart)
+_FEW = 16  # tokens up to which the MXFP4 products need no workspace (the gradient through a frozen weight apart)
 
 
 def _want_mxfp4(q, s, names, dev):

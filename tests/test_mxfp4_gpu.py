@@ -327,7 +327,7 @@ def test_empty_extents():
 @pytest.mark.parametrize("T,n_in,n_out", [(1, 32, 8), (1, 2048, 512), (2, 96, 40), (3, 1056, 1000), (8, 4096, 264),
                                           (15, 544, 520), (16, 5504, 72), (17, 160, 136), (32, 1024, 776), (33, 288, 2056),
                                           (48, 2048, 128), (64, 512, 264), (65, 544, 136), (200, 1056, 4096),
-                                          (256, 256, 256), (257, 2080, 520), (3, 96, 9000), (40, 8192, 136), (100, 5504, 72),
+                                          (256, 256, 256), (257, 2080, 520), (3, 96, 9000), (40, 8192, 136), (4, 5504, 264), (32, 6176, 72), (17, 8192, 40), (100, 5504, 72),
                                           (300, 96, 5504), (1000, 1056, 776), (1023, 2080, 2056), (2049, 512, 1032)])
 def test_fwd_and_dgrad_mxfp4w(T, n_in, n_out):
     say(f"case mxfp4w T={T} in={n_in} out={n_out}")
