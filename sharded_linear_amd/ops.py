@@ -113,18 +113,12 @@ def sl_wgrad_workspace_bytes(T: int, n_in: int, n_out: int) -> int:
     return int(lib().sl_wgrad_workspace_bytes(T, n_in, n_out))
 
 
-_WS = {}
-
-
 def wgrad_workspace(dev: torch.device, nbytes: int) -> torch.Tensor:
-    """A workspace of at least ``nbytes`` for the current stream of ``dev`` (contents never
-    matter to the kernels); one buffer per stream is reused and only grows."""
-    key = (dev, torch.cuda.current_stream(dev).cuda_stream)
-    ws = _WS.get(key)
-    if ws is None or ws.numel() < nbytes:
-        ws = torch.zeros(max(nbytes, 256), dtype=U8, device=dev)
-        _WS[key] = ws
-    return ws
+    """A workspace of ``nbytes`` for one call on the current stream of ``dev`` (its contents do not matter to
+    the kernels).  A call fills it in one launch and reads it in the next, and other host threads run
+    meanwhile, so no two calls share one; dropped after the call it goes back to the stream's allocator,
+    which hands it on in stream order, and under graph capture it belongs to the graph."""
+    return torch.empty(nbytes, dtype=U8, device=dev)
 
 
 def sl_linear_wgrad_accum(X: torch.Tensor, dY: torch.Tensor, main_grad: torch.Tensor,
@@ -374,14 +368,11 @@ def _launch(name, dev, *args):
 
 
 def _scratch(dev, need, workspace):
-    """(tensor, bytes) of the caller's workspace, or of one of this library's: the stream's shared one, or
-    under graph capture a new one, which belongs to the graph alone."""
+    """(tensor, bytes) of the caller's workspace, or of one for this call alone."""
     if workspace is None:
         if not need:
             return None, 0
-        with torch.cuda.device(dev):
-            workspace = (torch.empty(need, dtype=U8, device=dev) if torch.cuda.is_current_stream_capturing()
-                         else wgrad_workspace(dev, need))
+        workspace = wgrad_workspace(dev, need)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous and on {dev}")
     return workspace, workspace.numel() * workspace.element_size()
