@@ -44,7 +44,13 @@ def linear_with_grad_accumulation(input: torch.Tensor, weight: torch.Tensor) -> 
 class LinearMXFP4WithGradAccumulation(torch.autograd.Function):
     """The linear step with every product on MXFP4 operands: X, W and dY are cast inside the step, each
     along the axis its product contracts.  What is kept for backward is X's columnwise copy (0.53 bytes an
-    element) and W's."""
+    element) and W's; without gradients neither is made."""
+
+    @classmethod
+    def apply(cls, input, weight, seed=None, weight_mxfp4=None):
+        if not torch.is_grad_enabled():      # needs_input_grad tells of the tensors alone
+            input, weight = input.detach(), weight.detach()
+        return super().apply(input, weight, seed, weight_mxfp4)
 
     @staticmethod
     def forward(ctx, input, weight, seed, weight_mxfp4):

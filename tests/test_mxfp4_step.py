@@ -1,0 +1,58 @@
+"""The MXFP4 step's calls that compute no gradient, and its refusals."""
+import pytest
+import torch
+
+import sharded_linear_amd as sl
+from sharded_linear_amd import autograd
+from tests.gpu_util import say
+
+BF16 = torch.bfloat16
+
+
+@pytest.fixture
+def casts(monkeypatch):
+    """The step without a GPU: its casts and its forward product are noted, not computed."""
+    asked = []
+
+    def quantize(x, rows=True, cols=True, seed=None):
+        asked.append((tuple(x.shape), rows, cols))
+        r, c = x.shape
+        new = lambda *s: torch.zeros(s, dtype=torch.uint8)  # noqa: E731
+        up = lambda n: (n + 31) // 32 * 32  # noqa: E731
+        return ((new(r, up(c) // 2), new(r, up(c) // 32)) if rows else (None, None)) + \
+               ((new(c, up(r) // 2), new(c, up(r) // 32)) if cols else (None, None))
+
+    monkeypatch.setattr(autograd, "sl_mxfp4_quantize", quantize)
+    monkeypatch.setattr(autograd, "sl_linear_fwd_mxfp4", lambda xq, xs, wq, ws: torch.zeros((xq.shape[0], wq.shape[0]), dtype=BF16))
+    return asked
+
+
+@pytest.mark.parametrize("mode", [torch.no_grad, torch.inference_mode])
+def test_evaluation_needs_no_main_grad_and_casts_rows_only(casts, mode):
+    w = torch.nn.Parameter(torch.zeros(16, 64, dtype=BF16))               # no main_grad
+    x = torch.zeros(4, 64, dtype=BF16, requires_grad=True)
+    with mode():
+        for call in (sl.linear_mxfp4_with_grad_accumulation, sl.LinearMXFP4WithGradAccumulation.apply):
+            y = call(x, w, None, None)
+            assert y.shape == (4, 16) and not y.requires_grad
+    assert casts == [((4, 64), True, False), ((16, 64), True, False)] * 2
+    w.main_grad = torch.zeros(16, 64)
+    del casts[:]
+    y = sl.linear_mxfp4_with_grad_accumulation(x, w)                       # with gradients both copies are taken
+    assert y.requires_grad and casts == [((4, 64), True, True), ((16, 64), True, True)]
+
+
+@pytest.mark.gpu
+def test_evaluation_gives_the_forward_of_training():
+    say("case mxfp4 step without gradients")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    x = torch.randn((37, 72), device="cuda", generator=g).to(BF16).requires_grad_()
+    w = torch.nn.Parameter(torch.randn((40, 72), device="cuda", generator=g).to(BF16))
+    with torch.no_grad():
+        bare = sl.linear_mxfp4_with_grad_accumulation(x, w)
+        kept = sl.linear_mxfp4_with_grad_accumulation(x, w, weight_mxfp4=sl.sl_mxfp4_quantize(w, cols=False))
+    w.main_grad = torch.zeros((40, 72), device="cuda")
+    y = sl.linear_mxfp4_with_grad_accumulation(x, w)
+    assert y.requires_grad and not bare.requires_grad
+    assert torch.equal(bare, y) and torch.equal(kept, y)
