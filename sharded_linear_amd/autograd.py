@@ -56,6 +56,8 @@ class LinearMXFP4WithGradAccumulation(torch.autograd.Function):
     def forward(ctx, input, weight, seed, weight_mxfp4):
         if ctx.needs_input_grad[1] and not hasattr(weight, "main_grad"):
             raise ValueError("gradient accumulation fusion needs weight.main_grad (a grad_data view)")
+        if weight.dim() != 2 or input.shape[-1] != weight.shape[1]:
+            raise ValueError(f"input of {input.shape[-1]} features by a weight of shape {tuple(weight.shape)}")
         x2 = input.reshape(-1, input.shape[-1]).contiguous()
         xr, xrs, xc, xcs = sl_mxfp4_quantize(x2, cols=ctx.needs_input_grad[1])
         if weight_mxfp4 is None:

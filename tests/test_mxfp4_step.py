@@ -56,3 +56,12 @@ def test_evaluation_gives_the_forward_of_training():
     y = sl.linear_mxfp4_with_grad_accumulation(x, w)
     assert y.requires_grad and not bare.requires_grad
     assert torch.equal(bare, y) and torch.equal(kept, y)
+
+
+@pytest.mark.parametrize("features", [40, 72])
+def test_an_input_of_other_features_than_the_weight_is_refused(casts, features):
+    """Both pad to the same whole blocks of 32, so the products alone would not tell 40 from 64 or 72 from 96."""
+    w = torch.zeros((16, features // 32 * 32 + 32), dtype=BF16)
+    with pytest.raises(ValueError, match="features"):
+        sl.linear_mxfp4_with_grad_accumulation(torch.zeros((4, features), dtype=BF16), w)
+    assert not casts
