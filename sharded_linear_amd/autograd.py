@@ -41,6 +41,21 @@ def linear_with_grad_accumulation(input: torch.Tensor, weight: torch.Tensor) -> 
     return LinearWithGradAccumulation.apply(input, weight)
 
 
+def _check_copies(copies, n_out, n_in, cols):
+    """Checks (q_rows, s_rows, q_cols, s_cols) against the weight [n_out, n_in] whose copies they are; the
+    columnwise pair is used, and may not be absent, only with ``cols``."""
+    if len(copies) != 4:
+        raise ValueError(f"weight_mxfp4 has {len(copies)} tensors, expected the four of sl_mxfp4_quantize")
+    if cols and (copies[2] is None or copies[3] is None):
+        raise ValueError("the input gradient needs the weight's columnwise MXFP4 copy")
+    out_b, in_b = (n_out + 31) // 32, (n_in + 31) // 32
+    shapes = ((n_out, 16 * in_b), (n_out, in_b), (n_in, 16 * out_b), (n_in, out_b))
+    for k, (t, shape) in enumerate(zip(copies, shapes[:4 if cols else 2])):
+        if t is None or t.shape != shape:
+            raise ValueError(f"weight_mxfp4[{k}] of a weight [{n_out}, {n_in}] has shape {shape}, "
+                             f"got {None if t is None else tuple(t.shape)}")
+
+
 class LinearMXFP4WithGradAccumulation(torch.autograd.Function):
     """The linear step with every product on MXFP4 operands: X, W and dY are cast inside the step, each
     along the axis its product contracts.  What is kept for backward is X's columnwise copy (0.53 bytes an
@@ -58,13 +73,13 @@ class LinearMXFP4WithGradAccumulation(torch.autograd.Function):
             raise ValueError("gradient accumulation fusion needs weight.main_grad (a grad_data view)")
         if weight.dim() != 2 or input.shape[-1] != weight.shape[1]:
             raise ValueError(f"input of {input.shape[-1]} features by a weight of shape {tuple(weight.shape)}")
+        if weight_mxfp4 is not None:
+            _check_copies(weight_mxfp4, *weight.shape, ctx.needs_input_grad[0])
         x2 = input.reshape(-1, input.shape[-1]).contiguous()
         xr, xrs, xc, xcs = sl_mxfp4_quantize(x2, cols=ctx.needs_input_grad[1])
         if weight_mxfp4 is None:
             weight_mxfp4 = sl_mxfp4_quantize(weight.detach(), cols=ctx.needs_input_grad[0])
         wr, wrs, wc, wcs = weight_mxfp4
-        if ctx.needs_input_grad[0] and wc is None:
-            raise ValueError("the input gradient needs the weight's columnwise MXFP4 copy")
         y = sl_linear_fwd_mxfp4(xr, xrs, wr, wrs)
         ctx.save_for_backward(weight, xc, xcs, wc, wcs)
         ctx.seed, ctx.shape = seed, input.shape

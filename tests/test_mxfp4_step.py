@@ -65,3 +65,30 @@ def test_an_input_of_other_features_than_the_weight_is_refused(casts, features):
     with pytest.raises(ValueError, match="features"):
         sl.linear_mxfp4_with_grad_accumulation(torch.zeros((4, features), dtype=BF16), w)
     assert not casts
+
+
+def _copies(out, n_in, out_p, in_p):
+    """Shapes of a weight's four MXFP4 tensors: rowwise [out, in_p], columnwise [n_in, out_p]."""
+    u = lambda *s: torch.zeros(s, dtype=torch.uint8)  # noqa: E731
+    return [u(out, in_p // 2), u(out, in_p // 32), u(n_in, out_p // 2), u(n_in, out_p // 32)]
+
+
+@pytest.mark.parametrize("other", [(24, 72, 32, 96), (40, 64, 64, 64), (40, 104, 64, 128)], ids=["out", "in", "wider"])
+def test_copies_of_another_weight_are_refused(casts, other):
+    w = torch.nn.Parameter(torch.zeros((40, 72), dtype=BF16))
+    w.main_grad = torch.zeros((40, 72))
+    x = torch.zeros((4, 72), dtype=BF16, requires_grad=True)
+    good = _copies(40, 72, 64, 96)
+    assert sl.linear_mxfp4_with_grad_accumulation(x, w, weight_mxfp4=good).shape == (4, 40)
+    bad = _copies(*other)
+    del casts[:]
+    for mixed in (bad, good[:2] + bad[2:], bad[:2] + good[2:], good[:1] + bad[1:2] + good[2:], good[:3]):
+        if all(a.shape == b.shape for a, b in zip(mixed, good)) and len(mixed) == 4:
+            continue
+        with pytest.raises(ValueError, match="weight_mxfp4"):
+            sl.linear_mxfp4_with_grad_accumulation(x, w, weight_mxfp4=mixed)
+    with pytest.raises(ValueError, match="weight_mxfp4"):
+        sl.linear_mxfp4_with_grad_accumulation(x, w, weight_mxfp4=[None, None] + good[2:])
+    with pytest.raises(ValueError, match="columnwise"):
+        sl.linear_mxfp4_with_grad_accumulation(x, w, weight_mxfp4=good[:2] + [None, None])
+    assert not casts
