@@ -280,9 +280,9 @@ int sl_linear_dgrad_nvfp4w(void* stream, const void* dY, const void* Wm, float w
  * sl_mxfp4_quantize: x[rows, cols] bf16 (cols % 8 == 0, 16-byte aligned) into rowwise codes
  * q_rows[rows, Cp/2] + scales s_rows[rows, Cp/32] and/or columnwise ones, stored transposed,
  * q_cols[cols, Rp/2] + s_cols[cols, Rp/32], where Cp and Rp are cols and rows rounded up to 32: the
- * last block of a row or column is padded with zeros.  A NULL pair is skipped (a code pointer
- * without its scale pointer, or the reverse, is SL_EINVAL).  With v = x / 2^X for the block's
- * shared exponent X (scale byte X + 127):
+ * last block of a row or column is padded with zeros.  2^24 tiles of 128 x 128 or more are
+ * SL_ESHAPE.  A NULL pair is skipped (a code pointer without its scale pointer, or the reverse, is
+ * SL_EINVAL).  With v = x / 2^X for the block's shared exponent X (scale byte X + 127):
  *   SL_ROUND_NEAREST     X = clamp(floor(log2 amax) - 2, -127, 127); code = E2M1 of v, round half to
  *                        even, saturating at 6 (the OCP MX conversion)
  *   SL_ROUND_STOCHASTIC  X = the least exponent >= -127 with amax <= 6 * 2^X, so that nothing

@@ -10,6 +10,7 @@ namespace {
 
 constexpr int64_t kMaxExtent = int64_t(1) << 31;
 constexpr int64_t kMaxTiles = int64_t(1) << 31;        // workgroups of one launch
+constexpr int64_t kMaxCastTiles = int64_t(1) << 24;    // of 256 threads: a launch has fewer than 2^32
 constexpr int64_t kMaxFeatures = int64_t(1) << 23;     // rows of a tile stay within 32-bit offsets
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -150,7 +151,7 @@ extern "C" int sl_mxfp4_quantize(void* stream, const void* x, int64_t rows, int6
   if (!x) return SL_EINVAL;
   if (!aligned16(x) || (q_rows && !aligned16(q_rows)) || (q_cols && !aligned16(q_cols))) return SL_EALIGN;
   if (reinterpret_cast<uintptr_t>(seed_offset) & 7u) return SL_EALIGN;
-  if (ntiles(rows, cols, 128, 128) >= kMaxTiles) return SL_ESHAPE;
+  if (ntiles(rows, cols, 128, 128) >= kMaxCastTiles) return SL_ESHAPE;
   const F4QuantArgs a{x, rows, cols, q_rows, s_rows, q_cols, s_cols, rounding == SL_ROUND_STOCHASTIC, seed, seed_offset};
   return f4_quantize(static_cast<hipStream_t>(stream), a) == 0 ? SL_OK : SL_EHIP;
 }

@@ -211,3 +211,9 @@ def test_autograd_refuses_a_weight_without_main_grad():
     w = torch.nn.Parameter(torch.zeros(32, 32, dtype=torch.bfloat16))
     with pytest.raises(ValueError, match="main_grad"):
         sl.linear_mxfp4_with_grad_accumulation(torch.zeros(4, 32, dtype=torch.bfloat16), w)
+
+
+def test_cast_of_more_tiles_than_a_launch_takes_is_refused():
+    q = _lib.lib().sl_mxfp4_quantize
+    for rows, cols in (((1 << 31) - 1, 8), ((1 << 31) - 127, 128), (1 << 30, 136)):
+        assert q(None, A, rows, cols, A, A, A, A, 0, 0, None) == ESHAPE
