@@ -68,16 +68,23 @@ __device__ __forceinline__ uint32_t signs8(const uint32_t (&w)[4]) {
 // fp32 numbers 0, 2^-127, 2^-126 and 1.5, 2, 3, 4, 6 times 2^-126, which have one mantissa bit and, below
 // 2^-126, the fixed step of a subnormal as E2M1 has below 1: the bits from 22 up are the code.  So the draw is added
 // below that bit of 2^-126 v, which is cut off at 2^-149 (the kernel rounds toward zero), far below the draw's last bit.
-// draws: two of them, HI the upper one's, taken as it is by a 16-bit multiply-add.
+// draws: two of them, HI the upper one's, taken as it is by a 16-bit multiply-add.  e: -126 - X.
 template <bool HI>
-__device__ __forceinline__ uint32_t e2m1_stochastic(float x, int X, uint32_t draws) {
-  const uint32_t v = __float_as_uint(__builtin_ldexpf(__builtin_fabsf(x), -126 - X));
+__device__ __forceinline__ uint32_t e2m1_stochastic(float x, int e, uint32_t draws) {
+  const uint32_t v = __float_as_uint(__builtin_ldexpf(__builtin_fabsf(x), e));
   uint32_t s;
   if constexpr (HI) asm("v_mad_u32_u16 %0, %1, 64, %2 op_sel:[1,0,0,0]" : "=v"(s) : "v"(draws), "v"(v));
   else asm("v_mad_u32_u16 %0, %1, 64, %2" : "=v"(s) : "v"(draws), "v"(v));
   return s >> 22;
 }
-__device__ __forceinline__ void round_toward_zero() { __builtin_amdgcn_s_setreg(1 | 1 << 11, 3); }  // MODE bits 0..1: fp32 rounding
+// Sets the wave's fp32 rounding toward zero (MODE bits 0..1) and returns -126, on which every float operation
+// that needs it has to depend: the compiler moves float operations past a change of the mode, but not past
+// their operands.  before1, before2: wave-uniform values whose computation needs the mode that was.
+__device__ __forceinline__ int round_toward_zero(uint32_t before1, uint32_t before2) {
+  int e;
+  asm volatile("s_setreg_imm32_b32 hwreg(HW_REG_MODE, 0, 2), 3\n\ts_movk_i32 %0, 0xff82" : "=s"(e) : "s"(before1), "s"(before2));
+  return e;
+}
 
 // Shared exponent of a block whose largest magnitude has the bf16 bits amax (finite, not zero).  A
 // subnormal amax counts as 2^-127, which the clamp makes right.
@@ -89,17 +96,17 @@ __device__ __forceinline__ int mx4_exponent(uint32_t amax) {
 }
 
 // Encodes 8 elements, two to a word, of a block with largest magnitude amax: codes of elements
-// 0..7 in nibbles 0..7.  r: their draws (stochastic only).
+// 0..7 in nibbles 0..7.  r: their draws, unit: -126 from round_toward_zero (stochastic only).
 template <bool SR>
-__device__ __forceinline__ uint32_t mx4_codes(uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3, int X, uint4 r) {
+__device__ __forceinline__ uint32_t mx4_codes(uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3, int X, uint4 r, int unit) {
   const uint32_t w[4] = {w0, w1, w2, w3};
   uint32_t q = 0;
   if constexpr (SR) {
     const uint32_t d[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {                             // each code enters at the top
-      q = __builtin_amdgcn_alignbit(e2m1_stochastic<false>(bf16_lo(w[i]), X, d[i]), q, 4);
-      q = __builtin_amdgcn_alignbit(e2m1_stochastic<true>(bf16_hi(w[i]), X, d[i]), q, 4);
+      q = __builtin_amdgcn_alignbit(e2m1_stochastic<false>(bf16_lo(w[i]), unit - X, d[i]), q, 4);
+      q = __builtin_amdgcn_alignbit(e2m1_stochastic<true>(bf16_hi(w[i]), unit - X, d[i]), q, 4);
     }
     q |= signs8(w);
   } else {
@@ -157,7 +164,8 @@ __global__ void __launch_bounds__(256) mx4_quant_tile(F4QuantArgs a) {
   const uint32_t ntc = uint32_t((a.C + kQC - 1) / kQC), ntr = uint32_t((a.R + H * kQH - 1) / (H * kQH));
   const uint32_t b = uint32_t(xcd_remap(int(blockIdx.x), int(gridDim.x))), g = b / (kDown * ntc), p = b % (kDown * ntc);
   const uint32_t down = min(kDown, ntr - g * kDown);
-  const int64_t r0 = int64_t(g * kDown + p % down) * (H * kQH), c0 = int64_t(p / down) * kQC;
+  const uint32_t tr = g * kDown + p % down, tc = p / down;
+  const int64_t r0 = int64_t(tr) * (H * kQH), c0 = int64_t(tc) * kQC;
   const int t = threadIdx.x, ch = t & 15;
   const uint64_t key = a.seed + (SR && a.seed_offset ? *a.seed_offset : 0);
   const int64_t nbr = (a.C + 31) / 32, nbc = (a.R + 31) / 32;   // blocks of a row, of a column
@@ -169,7 +177,8 @@ __global__ void __launch_bounds__(256) mx4_quant_tile(F4QuantArgs a) {
 #pragma unroll
   for (int k = 0; k < 4 * H; ++k)                                   // C % 8 == 0: a chunk is inside or outside
     raw[k] = 16 * k < left && gc < a.C ? reinterpret_cast<const uint4*>(x)[at0 + k * (2 * a.C)] : make_uint4(0, 0, 0, 0);
-  if constexpr (SR) round_toward_zero();                        // behind the index division, which uses fp32 itself
+  int unit = 0;
+  if constexpr (SR) unit = round_toward_zero(tr, tc);           // the tile's place by a division, which uses fp32 itself
   uint32_t q[H][4], s[H];                                       // columnwise codes and scales, a block from each half
 #pragma unroll
   for (int h = 0; h < H; ++h) {
@@ -189,7 +198,7 @@ __global__ void __launch_bounds__(256) mx4_quant_tile(F4QuantArgs a) {
         const uint32_t amax = quad_max(mag_max(w));              // every lane takes part
         int X;
         const uint32_t sc = mx4_scale<SR>(amax, X);
-        uint32_t c = mx4_codes<SR>(w[0], w[1], w[2], w[3], X, d);
+        uint32_t c = mx4_codes<SR>(w[0], w[1], w[2], w[3], X, d, unit);
         if (amax == 0 || amax >= kNonFinite) c = 0;
         if (16 * n < left && gc < nbr * 32) {
           const int64_t at = qat0 + n * (16 * nbr);
@@ -225,7 +234,7 @@ __global__ void __launch_bounds__(256) mx4_quant_tile(F4QuantArgs a) {
       for (int e = 0; e < 4; ++e) {
         uint4 r = make_uint4(0, 0, 0, 0);
         if constexpr (SR) r = make_uint4(d[4 * e], d[4 * e + 1], d[4 * e + 2], d[4 * e + 3]);
-        q[h][e] = mx4_codes<SR>(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3], X, r);
+        q[h][e] = mx4_codes<SR>(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3], X, r, unit);
         if (amax == 0 || amax >= kNonFinite) q[h][e] = 0;
       }
       __syncthreads();
