@@ -56,8 +56,10 @@ const char* sl_status_str(int status);
  *                                     tiles, which only the forward has)
  *   SL_TUNE_{DGRAD,WGRAD}_CONFIG      bf16 tile configuration 0..24 of that product
  *   SL_TUNE_SPLITK                    split count 1..64 of the bf16 weight gradient
- *   SL_TUNE_F8_CONFIG                 block-scaled fp8 configuration 0..2 (0: 256x256, 1: 128x128,
- *                                     2: 256x128), for the weight gradient as well
+ *   SL_TUNE_F8_CONFIG                 block-scaled configuration 0..2, for the weight gradient as
+ *                                     well, of the products of two MXFP8 operands (0: 256x256, 1:
+ *                                     128x128, 2: 256x128) and of two MXFP4 operands (0: 256x256, 1:
+ *                                     128x128, 2: 128x128 staged four deep): one value, set for both
  * An unknown knob or a value out of range returns SL_EINVAL and changes nothing.  The knobs are
  * process-wide atomics: safe to set from any thread, but a call that overlaps a change may see
  * either value, so change them only while no call is being planned.

@@ -19,7 +19,9 @@
 //
 // Measured: [8192, 4096] over 11008 184 us, 4.0 PFLOP/s; [8192, 8192] over 2048 85 us, 3.2 PFLOP/s, of which the
 // results' 134 MB take 26; accumulating [11008, 4096] over 8192 237 us.  A loop of these MFMAs alone holds 6.4
-// PFLOP/s (1.5-1.6 GHz, the power limit), this one without its loads 4.2-4.5.
+// PFLOP/s (1.5-1.6 GHz, the power limit), this one without its loads 4.2-4.5.  In the first of these products the
+// matrix units are busy 51 % of the cycles, at about 1.9 GHz: neither the power limit nor the LDS's bytes (75 % of
+// that 51 %) hold it, but the waits of one wave a SIMD in its fixed order of reads, loads and products.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>

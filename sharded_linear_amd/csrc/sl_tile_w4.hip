@@ -10,7 +10,8 @@
 // which read a third less from LDS (58.6 -> 54.4 us for 200 tokens by [8192, 2048] unsplit; LDS is busy half
 // of the time, the matrix unit a quarter).  Reading a step's fragments while the step before is multiplied
 // (170 registers) gained nothing.  Activations, codes and scales go HBM -> LDS directly, three steps deep.
-// Small grids split the contraction: f32 planes, added in order by a second launch.
+// Small grids split the contraction: f32 planes, added in order by a second launch.  The gradient takes these tiles
+// for any number of tokens: one token through [8192, 2048] 12.1 us and 3.5 for the join.
 //   forward: a lane's share of 16 weight rows is one 16-byte chunk, a whole scale block, made bf16 in
 //     registers (exact); the j-th of the step's four v_mfma_f32_16x16x32_bf16 contracts elements
 //     8 j .. 8 j + 7 of every lane's block, and the activations are read from LDS in that order.

@@ -514,7 +514,8 @@ def sl_mxfp4w_fwd_workspace_bytes(T: int, n_in: int, n_out: int) -> int:
 
 
 def sl_linear_fwd_mxfp4w(X, Wq, Ws, Y=None, workspace=None):
-    """Y[T,out] = X[T,in] . deq(Wq, Ws)[out,in]^T with bf16 X and Y, from one token on."""
+    """Y[T,out] = X[T,in] . deq(Wq, Ws)[out,in]^T with bf16 X and Y, from one token on.  The workspace of many
+    tokens (1024, fewer by a wide weight) is a bf16 copy of the weight, 2 out in bytes for the call's time."""
     dev = _device(X)
     n_out, n_in = _want_mxfp4(Wq, Ws, ("Wq", "Ws"), dev)
     T = X.shape[0]
@@ -534,7 +535,8 @@ def sl_mxfp4w_dgrad_workspace_bytes(T: int, n_in: int, n_out: int) -> int:
 
 
 def sl_linear_dgrad_mxfp4w(dY, Wq, Ws, dX=None, workspace=None):
-    """dX[T,in] = dY[T,out] . deq(Wq, Ws)[out,in] with bf16 dY and dX (a frozen MXFP4 weight's input gradient)."""
+    """dX[T,in] = dY[T,out] . deq(Wq, Ws)[out,in] with bf16 dY and dX (a frozen MXFP4 weight's input gradient).
+    Workspaces are as sl_linear_fwd_mxfp4w's."""
     dev = _device(dY)
     n_out, n_in = _want_mxfp4(Wq, Ws, ("Wq", "Ws"), dev)
     T = dY.shape[0]
