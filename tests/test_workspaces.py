@@ -151,3 +151,35 @@ def test_a_call_keeps_no_memory():
         sl.sl_linear_fwd_mxfp4w(X, *w, Y)
         assert torch.cuda.memory_allocated() == before
     torch.cuda.synchronize()
+
+
+@pytest.mark.gpu
+def test_two_graphs_of_split_bf16_weight_gradients():
+    """Two captured graphs, replayed side by side on two streams: neither uses the other's planes, nor an eager call's."""
+    say("case two graphs of bf16 weight gradients")
+    T, n_in, n_out = 4096, 264, 520
+    assert sl.sl_wgrad_workspace_bytes(T, n_in, n_out)
+    cases = []
+    for k in range(2):
+        g = torch.Generator(device="cuda")
+        g.manual_seed(k)
+        X, dY = (torch.randn((T, n), device="cuda", generator=g).bfloat16() for n in (n_in, n_out))
+        grad = torch.zeros((n_out, n_in), device="cuda")
+        want = sl.sl_linear_wgrad_accum(X, dY, torch.zeros_like(grad))
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            grad.zero_()
+            sl.sl_linear_wgrad_accum(X, dY, grad)
+        cases.append((graph, X, dY, grad, want))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(3):
+        torch.cuda.synchronize()
+        for (graph, *_rest), s in zip(cases, streams):
+            with torch.cuda.stream(s):
+                graph.replay()
+        eager = sl.sl_linear_wgrad_accum(*cases[0][1:3], torch.zeros((n_out, n_in), device="cuda"))
+        torch.cuda.synchronize()
+        assert torch.equal(eager, cases[0][4])
+        for _graph, _x, _dy, grad, want in cases:
+            assert torch.equal(grad, want)
