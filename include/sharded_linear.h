@@ -345,6 +345,78 @@ int sl_linear_dgrad_mxfp4w(void* stream, const void* dY, const uint8_t* Wq, cons
                            void* dX, int64_t T, int64_t in, int64_t out, void* workspace,
                            size_t workspace_bytes);
 
+/* ---- Vocabulary-parallel embedding -----------------------------------------------------------
+ * The table shard W[V, H] (bf16, a param_data view) holds the ids vocab_start .. vocab_start + V - 1;
+ * an id outside them is another rank's (any value: it is never used as an index).
+ *   fwd:   Y[t]          = bf16(scale * W[ids[t] - vocab_start]), zeros for another rank's id, so that the
+ *                          ranks' results add up, as a row-parallel forward's do
+ *   wgrad: main_grad[v] += scale * sum of dY[t] over the t with ids[t] - vocab_start = v, fp32, in place;
+ *                          rows that no token names are not touched
+ * ids[T] are int32 or int64 (ids_bytes 4 or 8, aligned to that).  H % 8 == 0; V up to 2^24; the gradient
+ * takes up to 2^26 tokens, and T * H up to about 2^35 (SL_ESHAPE).  vocab_start >= 0 and scale finite
+ * (SL_EINVAL).  The gradient's sums are fp32 in an order that depends on the ids alone: the same call gives
+ * the same bits.  It takes a workspace of its query's bytes (16-byte aligned; initial contents do not
+ * matter; calls that may run concurrently need distinct ones) and makes up to three launches.
+ * --------------------------------------------------------------------------------------------- */
+int sl_embedding_fwd(void* stream, const void* ids, int32_t ids_bytes, const void* W, void* Y, int64_t T,
+                     int64_t V, int64_t H, int64_t vocab_start, float scale);
+size_t sl_embedding_wgrad_workspace_bytes(int64_t T, int64_t V, int64_t H);
+int sl_embedding_wgrad_accum(void* stream, const void* ids, int32_t ids_bytes, const void* dY, float* main_grad,
+                             int64_t T, int64_t V, int64_t H, int64_t vocab_start, float scale,
+                             void* workspace, size_t workspace_bytes);
+
+/* ---- Root-mean-square norm ---------------------------------------------------------------------
+ * Rows x[T, H] (bf16), an optional residual[T, H] (bf16) and the weight w[H] (bf16):
+ *   h = bf16(x + residual) (x itself without one)    rstd[t] = (mean(h[t]^2) + eps)^-1/2 (fp32)
+ *   y = h * rstd * w
+ * sl_rmsnorm_fwd writes y in bf16.  sl_rmsnorm_fwd_mxfp8 writes it in MXFP8 by the rule of
+ * sl_mxfp8_quantize, from the fp32 product (no bf16 rounding between): rowwise codes q_rows[T, H] +
+ * s_rows[T, H/32] (H % 32 == 0) and/or columnwise ones, stored transposed, q_cols[H, T] + s_cols[H, T/32]
+ * (T % 32 == 0); a NULL pair is skipped.  A block with an infinity or a NaN has scale 255 (NaN) and codes 0.
+ * Both write h (only with a residual; else h may be NULL) and rstd, which the gradient reads:
+ *   sl_rmsnorm_bwd: g = w * dY;  dX = rstd * (g - h * rstd^2 * mean(g * h)) + dresidual;
+ *                   w_grad[H] += sum over t of dY * h * rstd (fp32, in place, fixed order); w_grad NULL
+ *                   (with any workspace) leaves it out
+ * dX is the gradient of x and of the residual alike; dresidual (bf16, may be NULL) is the gradient that reaches
+ * h by other ways, and may be dX itself.  Sums and means are fp32.  H % 8 == 0 and H <= 16384 (SL_ESHAPE); eps >= 0 and finite
+ * (SL_EINVAL); w_grad and rstd 4-byte aligned.  The gradient takes a workspace of its query's bytes, as above.
+ * --------------------------------------------------------------------------------------------- */
+int sl_rmsnorm_fwd(void* stream, const void* x, const void* residual, const void* w, float eps, void* y, void* h,
+                   float* rstd, int64_t T, int64_t H);
+int sl_rmsnorm_fwd_mxfp8(void* stream, const void* x, const void* residual, const void* w, float eps,
+                         uint8_t* q_rows, uint8_t* s_rows, uint8_t* q_cols, uint8_t* s_cols, void* h,
+                         float* rstd, int64_t T, int64_t H);
+size_t sl_rmsnorm_bwd_workspace_bytes(int64_t T, int64_t H);
+int sl_rmsnorm_bwd(void* stream, const void* dY, const void* h, const void* w, const float* rstd,
+                   const void* dresidual, void* dX, float* w_grad, int64_t T, int64_t H, void* workspace,
+                   size_t workspace_bytes);
+
+/* ---- Orthogonalised updates ---------------------------------------------------------------------
+ * L matrices [rows, cols] of one shape, any extents (not bound to multiples of 8).  With U a matrix as
+ * [m, n], m <= n (a tall one is transposed on the way in and out):
+ *   X = U / |U|_F (zeros stay zeros);   `steps` times:  A = X.X^T,  X <- a X + (b A + c A.A).X
+ * coeffs is a host array of a, b, c for each step.  Products run in fp16 at one fixed scale with fp32 sums; the
+ * host checks that the coefficients keep singular values that start in [0, 1] below 3 and b A + c A.A
+ * below 15 (SL_EINVAL otherwise), which keeps every element in fp16's range.  A gradient with an infinity or a NaN gives
+ * NaN.
+ *
+ * sl_orthogonalize: O[L, rows, cols] (bf16) = X for U = G[L, rows, cols] (fp32 or bf16: g_bytes 4 or 2).
+ * sl_muon_step: one optimiser step of L weights.  W, G, M and master are host arrays of L device pointers, read
+ * during the call: bf16 weights, fp32 gradients (main_grad views), fp32 momenta, and fp32 master weights (master NULL:
+ * none).  No two matrices of W, M and master may overlap.
+ *   M <- momentum * M + G;   U = nesterov ? G + momentum * M : M
+ *   W <- (1 - lr * weight_decay) * W - lr * scale * X   (of the master where there is one, which is then rounded to W)
+ * lr, momentum, weight_decay and scale must be finite, steps 0 .. 64 (SL_EINVAL); L <= 65535 and a padded matrix under
+ * 2 GiB in fp16 (SL_ESHAPE).  All matrices are 16-byte aligned.  Both take a workspace of the query's bytes, as above.
+ * --------------------------------------------------------------------------------------------- */
+size_t sl_orthogonalize_workspace_bytes(int64_t L, int64_t rows, int64_t cols);
+int sl_orthogonalize(void* stream, const void* G, int32_t g_bytes, void* O, int64_t L, int64_t rows, int64_t cols,
+                     int32_t steps, const float* coeffs, void* workspace, size_t workspace_bytes);
+int sl_muon_step(void* stream, void* const* W, float* const* master, const float* const* G, float* const* M,
+                 int64_t L, int64_t rows, int64_t cols, float lr, float momentum, int32_t nesterov,
+                 float weight_decay, float scale, int32_t steps, const float* coeffs, void* workspace,
+                 size_t workspace_bytes);
+
 #ifdef __cplusplus
 }
 #endif

@@ -12,10 +12,14 @@ from .ops import (sl_grad_buffer_zero, sl_linear_dgrad, sl_linear_dgrad_mxfp8, s
                   sl_linear_wgrad_accum_noalloc, sl_mxfp4_quantize, sl_mxfp4_dequantize, sl_linear_fwd_mxfp4,
                   sl_linear_dgrad_mxfp4, sl_linear_wgrad_accum_mxfp4, sl_mxfp4_fwd_workspace_bytes, sl_mxfp4_dgrad_workspace_bytes, sl_mxfp4_wgrad_workspace_bytes,
                   sl_linear_fwd_mxfp4w, sl_linear_dgrad_mxfp4w, sl_mxfp4w_fwd_workspace_bytes,
-                  sl_mxfp4w_dgrad_workspace_bytes)
+                  sl_mxfp4w_dgrad_workspace_bytes, sl_embedding_fwd, sl_embedding_wgrad_accum,
+                  sl_embedding_wgrad_workspace_bytes, sl_rmsnorm_fwd, sl_rmsnorm_fwd_mxfp8, sl_rmsnorm_bwd,
+                  sl_rmsnorm_bwd_workspace_bytes, sl_orthogonalize, sl_orthogonalize_workspace_bytes, sl_muon_step)
 from .buffer import ParamAndGradBuffer, sl_bucket_divisor, sl_default_bucket_size, sl_layout_build
-from .autograd import (LinearMXFP4WithGradAccumulation, LinearWithGradAccumulation,
-                       linear_mxfp4_with_grad_accumulation, linear_with_grad_accumulation)
+from .autograd import (EmbeddingWithGradAccumulation, LinearMXFP4WithGradAccumulation, LinearWithGradAccumulation,
+                       NormLinearMXFP8WithGradAccumulation, RMSNormWithGradAccumulation, embedding_with_grad_accumulation,
+                       linear_mxfp4_with_grad_accumulation, linear_with_grad_accumulation,
+                       norm_linear_mxfp8_with_grad_accumulation, rmsnorm_with_grad_accumulation)
 
 __all__ = [
     "sl_grad_buffer_zero", "sl_linear_fwd", "sl_linear_dgrad", "sl_linear_wgrad_accum",
@@ -28,4 +32,8 @@ __all__ = [
     "sl_mxfp4_quantize", "sl_mxfp4_dequantize", "sl_linear_fwd_mxfp4", "sl_linear_dgrad_mxfp4",
     "sl_linear_wgrad_accum_mxfp4", "sl_mxfp4_fwd_workspace_bytes", "sl_mxfp4_dgrad_workspace_bytes", "sl_mxfp4_wgrad_workspace_bytes", "sl_linear_fwd_mxfp4w", "sl_linear_dgrad_mxfp4w",
     "sl_mxfp4w_fwd_workspace_bytes", "sl_mxfp4w_dgrad_workspace_bytes",
+    "sl_embedding_fwd", "sl_embedding_wgrad_accum", "sl_embedding_wgrad_workspace_bytes", "sl_rmsnorm_fwd", "sl_rmsnorm_fwd_mxfp8",
+    "sl_rmsnorm_bwd", "sl_rmsnorm_bwd_workspace_bytes", "sl_orthogonalize", "sl_orthogonalize_workspace_bytes", "sl_muon_step",
+    "EmbeddingWithGradAccumulation", "embedding_with_grad_accumulation", "RMSNormWithGradAccumulation",
+    "rmsnorm_with_grad_accumulation", "NormLinearMXFP8WithGradAccumulation", "norm_linear_mxfp8_with_grad_accumulation",
 ]

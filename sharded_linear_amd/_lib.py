@@ -15,7 +15,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libsharded_linear.so")
 
 c_i32, c_i64, c_vp, c_sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t
-c_u64 = ctypes.c_uint64
+c_u64, c_f32 = ctypes.c_uint64, ctypes.c_float
 P_I64 = ctypes.POINTER(ctypes.c_int64)
 P_I32 = ctypes.POINTER(ctypes.c_int32)
 
@@ -60,6 +60,17 @@ PROTOTYPES = {
     "sl_linear_fwd_mxfp4w": (ctypes.c_int, [c_vp, c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_vp, c_sz]),
     "sl_mxfp4w_dgrad_workspace_bytes": (c_sz, [c_i64, c_i64, c_i64]),
     "sl_linear_dgrad_mxfp4w": (ctypes.c_int, [c_vp, c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_vp, c_sz]),
+    "sl_embedding_fwd": (ctypes.c_int, [c_vp, c_vp, c_i32, c_vp, c_vp, c_i64, c_i64, c_i64, c_i64, c_f32]),
+    "sl_embedding_wgrad_workspace_bytes": (c_sz, [c_i64, c_i64, c_i64]),
+    "sl_embedding_wgrad_accum": (ctypes.c_int, [c_vp, c_vp, c_i32, c_vp, c_vp, c_i64, c_i64, c_i64, c_i64, c_f32, c_vp, c_sz]),
+    "sl_rmsnorm_fwd": (ctypes.c_int, [c_vp, c_vp, c_vp, c_vp, c_f32, c_vp, c_vp, c_vp, c_i64, c_i64]),
+    "sl_rmsnorm_fwd_mxfp8": (ctypes.c_int, [c_vp, c_vp, c_vp, c_vp, c_f32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_i64, c_i64]),
+    "sl_rmsnorm_bwd_workspace_bytes": (c_sz, [c_i64, c_i64]),
+    "sl_rmsnorm_bwd": (ctypes.c_int, [c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_vp, c_sz]),
+    "sl_orthogonalize_workspace_bytes": (c_sz, [c_i64, c_i64, c_i64]),
+    "sl_orthogonalize": (ctypes.c_int, [c_vp, c_vp, c_i32, c_vp, c_i64, c_i64, c_i64, c_i32, c_vp, c_vp, c_sz]),
+    "sl_muon_step": (ctypes.c_int, [c_vp, c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_f32, c_f32, c_i32, c_f32, c_f32, c_i32,
+                                    c_vp, c_vp, c_sz]),
 }
 
 _lib = None

@@ -12,8 +12,10 @@ import torch
 
 from torch.autograd.function import once_differentiable
 
-from .ops import (sl_linear_dgrad, sl_linear_dgrad_mxfp4, sl_linear_fwd, sl_linear_fwd_mxfp4, sl_linear_wgrad_accum,
-                  sl_linear_wgrad_accum_mxfp4, sl_mxfp4_quantize)
+from .ops import (sl_embedding_fwd, sl_embedding_wgrad_accum, sl_linear_dgrad, sl_linear_dgrad_mxfp4, sl_linear_dgrad_mxfp8,
+                  sl_linear_fwd, sl_linear_fwd_mxfp4, sl_linear_fwd_mxfp8, sl_linear_wgrad_accum, sl_linear_wgrad_accum_mxfp4,
+                  sl_linear_wgrad_accum_mxfp8, sl_mxfp4_quantize, sl_mxfp8_quantize, sl_rmsnorm_bwd, sl_rmsnorm_fwd,
+                  sl_rmsnorm_fwd_mxfp8)
 
 
 class LinearWithGradAccumulation(torch.autograd.Function):
@@ -106,3 +108,147 @@ def linear_mxfp4_with_grad_accumulation(input: torch.Tensor, weight: torch.Tenso
     own.  ``weight_mxfp4`` is sl_mxfp4_quantize(weight), made once and passed to every micro-batch that
     uses the same weight; without it the weight is cast in each call."""
     return LinearMXFP4WithGradAccumulation.apply(input, weight, seed, weight_mxfp4)
+
+
+def _need_main_grad(weight, needed):
+    if needed and not hasattr(weight, "main_grad"):
+        raise ValueError("gradient accumulation fusion needs weight.main_grad (a grad_data view)")
+
+
+class EmbeddingWithGradAccumulation(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, ids, weight, vocab_start, scale):
+        _need_main_grad(weight, ctx.needs_input_grad[1])
+        ids = ids.contiguous()
+        ctx.save_for_backward(ids, weight)
+        ctx.at = vocab_start, scale
+        return sl_embedding_fwd(ids, weight.detach(), vocab_start=vocab_start, scale=scale)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_output):
+        ids, weight = ctx.saved_tensors
+        sl_embedding_wgrad_accum(ids, grad_output.contiguous(), weight.main_grad, *ctx.at)
+        weight.grad_added_to_main_grad = True
+        return None, None, None, None
+
+
+def embedding_with_grad_accumulation(ids: torch.Tensor, weight: torch.Tensor, vocab_start: int = 0, scale: float = 1.0) -> torch.Tensor:
+    """Rows of the table shard ``weight`` [V, H] for ids of any shape, times ``scale``; zeros for ids of other ranks (outside
+    vocab_start .. vocab_start + V - 1), so that the ranks' results add up.  Backward adds into weight.main_grad."""
+    if not torch.is_grad_enabled():
+        weight = weight.detach()
+    return EmbeddingWithGradAccumulation.apply(ids, weight, vocab_start, scale)
+
+
+def _norm_rows(x, weight, residual):
+    """x and the residual as contiguous rows of the norm's width."""
+    if weight.dim() != 1 or x.shape[-1] != weight.shape[0]:
+        raise ValueError(f"input of {x.shape[-1]} features by a norm weight of shape {tuple(weight.shape)}")
+    if residual is not None and residual.shape != x.shape:
+        raise ValueError(f"residual has shape {tuple(residual.shape)}, the input {tuple(x.shape)}")
+    rows = lambda t: None if t is None else t.reshape(-1, t.shape[-1]).contiguous()  # noqa: E731
+    return rows(x), rows(residual)
+
+
+class RMSNormWithGradAccumulation(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, input, weight, residual, eps):
+        _need_main_grad(weight, ctx.needs_input_grad[1])
+        x2, r2 = _norm_rows(input, weight, residual)
+        y, h, rstd = sl_rmsnorm_fwd(x2, weight.detach(), eps, residual=r2)
+        ctx.save_for_backward(h, weight, rstd)
+        ctx.set_materialize_grads(False)
+        ctx.shape = input.shape
+        y = y.view(input.shape)
+        return y if residual is None else (y, h.view(input.shape))
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_y, grad_h=None):
+        h, weight, rstd = ctx.saved_tensors
+        return _norm_backward(ctx, grad_y, grad_h, h, weight, rstd) + (None,)
+
+
+def _norm_backward(ctx, grad_y, grad_h, h, weight, rstd):
+    """Gradients of input, weight (into main_grad) and residual."""
+    if grad_y is None:
+        return grad_h, None, grad_h if ctx.needs_input_grad[2] else None
+    rows = lambda t: None if t is None else t.reshape(-1, t.shape[-1]).contiguous()  # noqa: E731
+    need_w = ctx.needs_input_grad[1]
+    dx = sl_rmsnorm_bwd(rows(grad_y), h, weight.detach(), rstd, weight.main_grad if need_w else None,
+                        dresidual=rows(grad_h)).view(ctx.shape)
+    if need_w:
+        weight.grad_added_to_main_grad = True
+    return dx, None, dx if ctx.needs_input_grad[2] else None
+
+
+def rmsnorm_with_grad_accumulation(input: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None,
+                                   eps: float = 1e-5):
+    """The root-mean-square norm of ``input`` over its last axis, or of h = input + residual: returns y, or (y, h), h being
+    the residual stream that the next block adds to.  The weight's gradient goes to weight.main_grad."""
+    if not torch.is_grad_enabled():
+        weight = weight.detach()
+    return RMSNormWithGradAccumulation.apply(input, weight, residual, eps)
+
+
+class NormLinearMXFP8WithGradAccumulation(torch.autograd.Function):
+    """A norm and the all-MXFP8 linear step behind it.  The norm writes the step's input in MXFP8, along both axes at once, and
+    in no other form; backward keeps its columnwise copy, the weight's, and h."""
+
+    @classmethod
+    def apply(cls, input, norm_weight, residual, weight, eps, weight_mxfp8):
+        if not torch.is_grad_enabled():      # needs_input_grad tells of the tensors alone
+            input, norm_weight, weight = input.detach(), norm_weight.detach(), weight.detach()
+            residual = None if residual is None else residual.detach()
+        return super().apply(input, norm_weight, residual, weight, eps, weight_mxfp8)
+
+    @staticmethod
+    def forward(ctx, input, norm_weight, residual, weight, eps, weight_mxfp8):
+        need_x = any(ctx.needs_input_grad[:3])
+        need_w = ctx.needs_input_grad[3]
+        _need_main_grad(norm_weight, ctx.needs_input_grad[1])
+        _need_main_grad(weight, need_w)
+        if weight.dim() != 2 or input.shape[-1] != weight.shape[1]:
+            raise ValueError(f"input of {input.shape[-1]} features by a weight of shape {tuple(weight.shape)}")
+        x2, r2 = _norm_rows(input, norm_weight, residual)
+        n_out, n_in = weight.shape
+        T = x2.shape[0]
+        if (need_w and T % 128) or (need_x and n_out % 128) or n_in % 32:
+            raise ValueError(f"MXFP8 products of {T} tokens by a weight {(n_out, n_in)}: the contracted extents of the gradients "
+                             "are multiples of 128, the input's of 32")
+        if weight_mxfp8 is None:
+            weight_mxfp8 = sl_mxfp8_quantize(weight.detach(), cols=need_x)
+        wr, wrs, wc, wcs = weight_mxfp8
+        if need_x and wc is None:
+            raise ValueError("the input gradient needs the weight's columnwise MXFP8 copy")
+        xr, xrs, xc, xcs, h, rstd = sl_rmsnorm_fwd_mxfp8(x2, norm_weight.detach(), eps, residual=r2, cols=need_w)
+        y = sl_linear_fwd_mxfp8(xr, xrs, wr, wrs).view(*input.shape[:-1], n_out)
+        ctx.save_for_backward(h, norm_weight, rstd, weight, xc, xcs, wc, wcs)
+        ctx.set_materialize_grads(False)
+        ctx.shape = input.shape
+        return y if residual is None else (y, h.view(input.shape))
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_y, grad_h=None):
+        h, norm_weight, rstd, weight, xc, xcs, wc, wcs = ctx.saved_tensors
+        grad_n = None
+        if grad_y is not None:
+            need_x, need_w = any(ctx.needs_input_grad[:3]), ctx.needs_input_grad[3]
+            dy = grad_y.reshape(-1, grad_y.shape[-1]).contiguous()
+            dr, drs, dc, dcs = sl_mxfp8_quantize(dy, rows=need_x, cols=need_w)
+            if need_x:
+                grad_n = sl_linear_dgrad_mxfp8(dr, drs, wc, wcs)
+            if need_w:
+                sl_linear_wgrad_accum_mxfp8(dc, dcs, xc, xcs, weight.main_grad)
+                weight.grad_added_to_main_grad = True
+        return _norm_backward(ctx, grad_n, grad_h, h, norm_weight, rstd) + (None, None, None)
+
+
+def norm_linear_mxfp8_with_grad_accumulation(input: torch.Tensor, norm_weight: torch.Tensor, weight: torch.Tensor,
+                                             residual: torch.Tensor | None = None, eps: float = 1e-5, weight_mxfp8=None):
+    """Y = norm(input + residual) . weight^T with every product of the step on MXFP8 operands: returns Y, or (Y, h) with a
+    residual, h = input + residual.  Both weights' gradients go to their main_grad.  ``weight_mxfp8`` is
+    sl_mxfp8_quantize(weight), made once and passed to every micro-batch; without it the weight is quantised in each call."""
+    return NormLinearMXFP8WithGradAccumulation.apply(input, norm_weight, residual, weight, eps, weight_mxfp8)

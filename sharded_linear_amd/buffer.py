@@ -15,7 +15,7 @@ from dataclasses import dataclass
 import torch
 
 from ._lib import check, lib
-from .ops import sl_grad_buffer_zero
+from .ops import sl_grad_buffer_zero, sl_muon_step
 
 
 @dataclass
@@ -104,3 +104,15 @@ class ParamAndGradBuffer:
 
     def zero_grad_buffer(self) -> None:
         sl_grad_buffer_zero(self.grad_data)
+
+    def muon_step(self, names, momentum_data: torch.Tensor, lr: float, **options) -> None:
+        """sl_muon_step of the named matrices, from grad_data into param_data.  ``momentum_data`` is laid out as grad_data
+        (zeros at first); weights of one shape share a call."""
+        if momentum_data.shape != self.grad_data.shape:
+            raise ValueError(f"momentum_data has shape {tuple(momentum_data.shape)}, expected {tuple(self.grad_data.shape)}")
+        by_shape = {}
+        for name in names:
+            by_shape.setdefault(self.shapes[name], []).append(name)
+        for shape, group in by_shape.items():
+            momenta = [momentum_data[s:e].view(shape) for s, e, _ in (self.index[n] for n in group)]
+            sl_muon_step([self.param(n) for n in group], [self.main_grad(n) for n in group], momenta, lr, **options)

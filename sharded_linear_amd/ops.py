@@ -549,3 +549,205 @@ def sl_linear_dgrad_mxfp4w(dY, Wq, Ws, dX=None, workspace=None):
     _launch("sl_linear_dgrad_mxfp4w", dev, _addr(dY), _addr(Wq), _addr(Ws), _addr(dX), T, n_in, n_out, _addr(workspace),
             nbytes)
     return dX
+
+
+# ---- vocabulary-parallel embedding --------------------------------------------------------------
+
+def _want_ids(ids, dev):
+    """Checks token ids of any shape; returns the bytes of one."""
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"ids must be torch.int32 or torch.int64, got {ids.dtype}")
+    _want(ids, "ids", ids.dtype, ids.shape, dev)
+    return ids.element_size()
+
+
+def _want_matrix(t, name):
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix")
+    return t.shape
+
+
+def sl_embedding_fwd(ids, W, Y=None, vocab_start=0, scale=1.0):
+    """Y[*ids.shape, H] = bf16(scale * W[ids - vocab_start]) of the table shard W[V, H] (bf16); zeros where an id
+    is not in vocab_start .. vocab_start + V - 1 (another rank's)."""
+    dev = _device(ids)
+    size = _want_ids(ids, dev)
+    V, H = _want_matrix(W, "W")
+    _want(W, "W", BF16, (V, H), dev)
+    if Y is None:
+        Y = torch.empty((*ids.shape, H), dtype=BF16, device=dev)
+    else:
+        _want(Y, "Y", BF16, (*ids.shape, H), dev)
+    _launch("sl_embedding_fwd", dev, _addr(ids), size, _addr(W), _addr(Y), ids.numel(), V, H, vocab_start, scale)
+    return Y
+
+
+def sl_embedding_wgrad_workspace_bytes(T: int, V: int, H: int) -> int:
+    return int(lib().sl_embedding_wgrad_workspace_bytes(T, V, H))
+
+
+def sl_embedding_wgrad_accum(ids, dY, main_grad, vocab_start=0, scale=1.0, workspace=None):
+    """main_grad[V, H] += scale * the sums of dY[*ids.shape, H] (bf16) over equal ids, fp32, in place."""
+    dev = _device(ids)
+    size = _want_ids(ids, dev)
+    V, H = _want_matrix(main_grad, "main_grad")
+    _want(main_grad, "main_grad", F32, (V, H), dev)
+    _want(dY, "dY", BF16, (*ids.shape, H), dev)
+    T = ids.numel()
+    workspace, nbytes = _scratch(dev, sl_embedding_wgrad_workspace_bytes(T, V, H), workspace)
+    _launch("sl_embedding_wgrad_accum", dev, _addr(ids), size, _addr(dY), _addr(main_grad), T, V, H, vocab_start, scale,
+            _addr(workspace), nbytes)
+    return main_grad
+
+
+# ---- root-mean-square norm ----------------------------------------------------------------------
+
+def _norm_inputs(x, w, residual, h):
+    """Checks a norm's inputs; returns (device, T, H, h, rstd), h being x itself without a residual."""
+    dev = _device(x)
+    T, H = _want_matrix(x, "x")
+    _want(x, "x", BF16, (T, H), dev)
+    _want(w, "w", BF16, (H,), dev)
+    if residual is None:
+        if h is not None:
+            raise ValueError("h is the sum with a residual, and none is given")
+        h = x
+    else:
+        _want(residual, "residual", BF16, (T, H), dev)
+        if h is None:
+            h = torch.empty((T, H), dtype=BF16, device=dev)
+        else:
+            _want(h, "h", BF16, (T, H), dev)
+    return dev, T, H, h, torch.empty(T, dtype=F32, device=dev)
+
+
+def sl_rmsnorm_fwd(x, w, eps, residual=None, y=None, h=None):
+    """Returns (y, h, rstd) of x[T, H]: h = bf16(x + residual) (x itself without one), rstd = (mean(h^2) + eps)^-1/2
+    (fp32 [T]), y = bf16(h * rstd * w)."""
+    dev, T, H, h, rstd = _norm_inputs(x, w, residual, h)
+    if y is None:
+        y = torch.empty((T, H), dtype=BF16, device=dev)
+    else:
+        _want(y, "y", BF16, (T, H), dev)
+    _launch("sl_rmsnorm_fwd", dev, _addr(x), _addr(residual), _addr(w), eps, _addr(y), None if residual is None else _addr(h),
+            _addr(rstd), T, H)
+    return y, h, rstd
+
+
+def sl_rmsnorm_fwd_mxfp8(x, w, eps, residual=None, rows=True, cols=True, out=None, h=None):
+    """sl_rmsnorm_fwd with y in MXFP8, rounded once from fp32: returns (q_rows, s_rows, q_cols, s_cols, h, rstd); a copy not
+    asked for is None.  The copies are laid out as sl_mxfp8_quantize's: rowwise [T, H] + [T, H/32] (H % 32 == 0), columnwise,
+    stored transposed, [H, T] + [H, T/32] (T % 32 == 0).  ``out`` may supply the four tensors."""
+    dev, T, H, h, rstd = _norm_inputs(x, w, residual, h)
+    if out is None:
+        new = lambda *shape: torch.empty(shape, dtype=U8, device=dev)  # noqa: E731
+        out = ((new(T, H), new(T, H // 32)) if rows else (None, None)) + ((new(H, T), new(H, T // 32)) if cols else (None, None))
+    qr, sr, qc, sc = out
+    if qr is not None:
+        _want(qr, "q_rows", U8, (T, H), dev)
+        _want(sr, "s_rows", U8, (T, H // 32), dev)
+    if qc is not None:
+        _want(qc, "q_cols", U8, (H, T), dev)
+        _want(sc, "s_cols", U8, (H, T // 32), dev)
+    _launch("sl_rmsnorm_fwd_mxfp8", dev, _addr(x), _addr(residual), _addr(w), eps, _addr(qr), _addr(sr), _addr(qc), _addr(sc),
+            None if residual is None else _addr(h), _addr(rstd), T, H)
+    return qr, sr, qc, sc, h, rstd
+
+
+def sl_rmsnorm_bwd_workspace_bytes(T: int, H: int) -> int:
+    return int(lib().sl_rmsnorm_bwd_workspace_bytes(T, H))
+
+
+def sl_rmsnorm_bwd(dY, h, w, rstd, w_grad, dresidual=None, dX=None, workspace=None):
+    """dX[T, H] (bf16) of sl_rmsnorm_fwd, the gradient of x and of the residual alike, from the h and rstd it returned;
+    dresidual is the gradient that reaches h by other ways.  w_grad[H] += the weight's gradient (fp32, in place);
+    None leaves it out."""
+    dev = _device(dY)
+    T, H = _want_matrix(dY, "dY")
+    _want(dY, "dY", BF16, (T, H), dev)
+    _want(h, "h", BF16, (T, H), dev)
+    _want(w, "w", BF16, (H,), dev)
+    _want(rstd, "rstd", F32, (T,), dev)
+    if w_grad is not None:
+        _want(w_grad, "w_grad", F32, (H,), dev)
+    if dresidual is not None:
+        _want(dresidual, "dresidual", BF16, (T, H), dev)
+    if dX is None:
+        dX = torch.empty((T, H), dtype=BF16, device=dev)
+    else:
+        _want(dX, "dX", BF16, (T, H), dev)
+    workspace, nbytes = _scratch(dev, 0 if w_grad is None else sl_rmsnorm_bwd_workspace_bytes(T, H), workspace)
+    _launch("sl_rmsnorm_bwd", dev, _addr(dY), _addr(h), _addr(w), _addr(rstd), _addr(dresidual), _addr(dX), _addr(w_grad), T, H,
+            _addr(workspace), nbytes)
+    return dX
+
+
+# ---- orthogonalised updates ---------------------------------------------------------------------
+
+NEWTON_SCHULZ = (3.4445, -4.7750, 2.0315)      # moves singular values of 0.01 .. 1 to 0.7 .. 1.2 in 5 steps
+
+
+def _coefficients(steps, coefficients):
+    """(steps, a C array of a, b, c for each); one triple serves every step."""
+    if steps < 0:
+        raise ValueError(f"steps is {steps}")
+    flat = [float(v) for c in coefficients for v in (c if isinstance(c, (tuple, list)) else (c,))]
+    if len(flat) == 3:
+        flat = flat * steps
+    if len(flat) != 3 * steps:
+        raise ValueError(f"coefficients are one triple, or one for each of the {steps} steps")
+    return steps, (ctypes.c_float * max(1, len(flat)))(*flat)
+
+
+def sl_orthogonalize_workspace_bytes(L: int, rows: int, cols: int) -> int:
+    return int(lib().sl_orthogonalize_workspace_bytes(L, rows, cols))
+
+
+def sl_orthogonalize(G, out=None, steps=5, coefficients=NEWTON_SCHULZ, workspace=None):
+    """bf16 Newton-Schulz iterate of G[rows, cols] or of each of G[L, rows, cols] (fp32 or bf16): X = G / |G|_F, and
+    ``steps`` times X <- a X + (b A + c A A) X with A = X X^T."""
+    dev = _device(G)
+    if G.dim() not in (2, 3) or G.dtype not in (F32, BF16):
+        raise ValueError(f"G must be one or a batch of fp32 or bf16 matrices, got {G.dtype} {tuple(G.shape)}")
+    _want(G, "G", G.dtype, G.shape, dev)
+    rows, cols = G.shape[-2:]
+    L = G.shape[0] if G.dim() == 3 else 1
+    if out is None:
+        out = torch.empty(G.shape, dtype=BF16, device=dev)
+    else:
+        _want(out, "out", BF16, G.shape, dev)
+    steps, k = _coefficients(steps, coefficients)
+    workspace, nbytes = _scratch(dev, sl_orthogonalize_workspace_bytes(L, rows, cols), workspace)
+    _launch("sl_orthogonalize", dev, _addr(G), G.element_size(), _addr(out), L, rows, cols, steps, k, _addr(workspace), nbytes)
+    return out
+
+
+def sl_muon_step(weights, main_grads, momenta, lr, momentum=0.95, nesterov=True, weight_decay=0.0, scale=None, masters=None,
+                 steps=5, coefficients=NEWTON_SCHULZ, workspace=None):
+    """One step of bf16 weights of one shape, in place, from their fp32 main_grads: M <- momentum M + G, U = G + momentum M
+    (``nesterov``) or M, W <- (1 - lr weight_decay) W - lr scale orthogonalize(U).  Arguments are matrices or lists of them; a
+    list's products run together, so weights of one shape belong in one call.  ``masters`` are fp32 weights that take the step in W's
+    place; W is then their rounding.  ``scale`` None is sqrt(max(1, rows / cols))."""
+    lists = [[t] if isinstance(t, torch.Tensor) else list(t) for t in (weights, main_grads, momenta)]
+    lists.append(None if masters is None else [masters] if isinstance(masters, torch.Tensor) else list(masters))
+    W = lists[0]
+    if any(x is not None and len(x) != len(W) for x in lists):
+        raise ValueError("weights, main_grads, momenta and masters differ in number")
+    if not W:
+        return
+    dev = _device(W[0])
+    rows, cols = _want_matrix(W[0], "a weight")
+    for x, name, dtype in zip(lists, ("a weight", "a main_grad", "a momentum", "a master"), (BF16, F32, F32, F32)):
+        for t in x or ():
+            _want(t, name, dtype, (rows, cols), dev)
+    written = [t.data_ptr() for x in (lists[0], lists[2], lists[3]) for t in x or ()]
+    if rows and cols and len(set(written)) < len(written) or {t.data_ptr() for t in lists[1]} & set(written):
+        raise ValueError("a weight, momentum or master is given twice")
+    if scale is None:
+        scale = max(1.0, rows / cols) ** 0.5 if cols else 1.0
+    steps, k = _coefficients(steps, coefficients)
+    table = lambda x: None if x is None else (ctypes.c_void_p * len(x))(*(t.data_ptr() for t in x))  # noqa: E731
+    w, g, m, p = (table(x) for x in lists)
+    workspace, nbytes = _scratch(dev, sl_orthogonalize_workspace_bytes(len(W), rows, cols), workspace)
+    _launch("sl_muon_step", dev, w, p, g, m, len(W), rows, cols, lr, momentum, int(nesterov), weight_decay, scale, steps, k,
+            _addr(workspace), nbytes)

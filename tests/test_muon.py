@@ -1,0 +1,347 @@
+"""Orthogonalised updates: refusals on the CPU, iterates and optimiser steps on the GPU against 64 bits."""
+import ctypes
+
+import pytest
+import torch
+
+import sharded_linear_amd as sl
+from sharded_linear_amd import _lib
+from tests.gpu_util import say
+
+OK, EINVAL, EALIGN, ESHAPE, EWORKSPACE = 0, -1, -2, -3, -4
+A = 1 << 20          # an aligned fake device address, never dereferenced
+BF16, F32 = torch.bfloat16, torch.float32
+COEFFS = (3.4445, -4.7750, 2.0315)
+# The 2-norm of an iterate's error over that of the iterate.  An element is rounded to fp16 within half a step, 2^-11, so the
+# roundings of one matrix are 2^-11 / sqrt(3) = 2.8e-4 of its norm.  With singular values near 1, X moves by at most
+# |b + 2 c| = 0.7 .. 4.8 times what A moves by, by up to 2.8 times the relative change of b A + c A^2, and a change of X grows by
+# up to a = 3.4 a step while its singular value is small and by less than 1 later: three last steps of 2.8e-4 (1 + 4.8 + 2.8), added
+# as squares, are 4.2e-3 at most.
+OFF = 4.2e-3
+BF16_OFF = 2.0 ** -8 / 3 ** 0.5      # the rounding of the result, as a 2-norm
+
+
+def _arr(*v):
+    return (ctypes.c_float * len(v))(*v)
+
+
+def test_orthogonalize_validation():
+    L = _lib.lib()
+    f, ws = L.sl_orthogonalize, L.sl_orthogonalize_workspace_bytes
+    need = ws(2, 100, 60)
+    k = _arr(*COEFFS * 5)
+    assert need > 0 and ws(0, 5, 5) == 0 and ws(1, 0, 5) == 0 and ws(-1, 5, 5) == 0 and ws(1, 1 << 31, 5) == 0
+    assert ws(1, (1 << 31) - 1, (1 << 31) - 1) == 0 and ws(1 << 30, 8, 8) == 0
+    assert f(None, A, 4, A, 2, 100, 60, 5, k, A, need - 1) == EWORKSPACE
+    assert f(None, A, 4, A, 2, 100, 60, 5, k, None, 0) == EWORKSPACE
+    assert f(None, A, 4, A, 2, 100, 60, 5, k, A + 8, need) == EWORKSPACE
+    assert f(None, A, 3, A, 2, 100, 60, 5, k, A, need) == EINVAL
+    assert f(None, A, 4, A, 2, 100, 60, -1, k, A, need) == EINVAL
+    assert f(None, A, 4, A, 2, 100, 60, 65, k, A, need) == EINVAL
+    assert f(None, A, 4, A, 2, 100, 60, 5, None, A, need) == EINVAL
+    assert f(None, A, 4, A, -1, 100, 60, 5, k, A, need) == EINVAL
+    assert f(None, None, 4, A, 2, 100, 60, 5, k, A, need) == EINVAL
+    assert f(None, A, 4, None, 2, 100, 60, 5, k, A, need) == EINVAL
+    assert f(None, A + 4, 4, A, 2, 100, 60, 5, k, A, need) == EALIGN
+    assert f(None, A, 4, A + 4, 2, 100, 60, 5, k, A, need) == EALIGN
+    assert f(None, A, 4, A, 1, 1 << 20, 1 << 20, 5, k, A, 1 << 62) == ESHAPE
+    assert f(None, A, 4, A, 70000, 8, 8, 5, k, A, 1 << 62) == ESHAPE
+    assert f(None, None, 4, None, 0, 100, 60, 5, k, None, 0) == OK
+    assert f(None, None, 4, None, 2, 0, 60, 5, k, None, 0) == OK
+
+
+@pytest.mark.parametrize("k,ok", [((3.4445, -4.7750, 2.0315), True), ((1.5, -0.5, 0.0), True), ((1.875, -1.25, 0.375), True), ((1.0, 0.0, 0.0), True),
+                                  ((8.28749, -23.5959, 17.3004), True), ((4.0, 0.0, 0.0), False), ((2.0, 1.5, 0.0), False), ((3.4445, -4.7750, 12.0), False),
+                                  ((9.0, -20.0, 12.5), True), ((float("nan"), 0.0, 0.0), False), ((1.0, 30.0, -30.0), False)])
+def test_coefficients_that_leave_the_range_are_refused(k, ok):
+    """One step of each from singular values in [0, 1]: below 3, and the inner polynomial below 15."""
+    f = _lib.lib().sl_orthogonalize
+    s = torch.linspace(0, 1, 100001, dtype=torch.float64)
+    if ok:
+        assert (k[0] * s + k[1] * s ** 3 + k[2] * s ** 5).abs().max() <= 3 and (k[1] * s ** 2 + k[2] * s ** 4).abs().max() <= 15
+    assert f(None, None, 4, None, 0, 8, 8, 1, _arr(*k), None, 0) == (OK if ok else EINVAL)
+
+
+def test_coefficients_are_followed_over_the_steps():
+    f = _lib.lib().sl_orthogonalize
+    double = (2.0, 0.0, 0.0)
+    assert f(None, None, 4, None, 0, 8, 8, 1, _arr(*double), None, 0) == OK
+    assert f(None, None, 4, None, 0, 8, 8, 2, _arr(*double * 2), None, 0) == EINVAL        # singular values of 4
+    assert f(None, None, 4, None, 0, 8, 8, 2, _arr(*double, 0.5, 0.0, 0.0), None, 0) == OK
+
+
+def test_muon_validation():
+    L = _lib.lib()
+    f = L.sl_muon_step
+    need = L.sl_orthogonalize_workspace_bytes(2, 100, 60)
+    P = lambda *v: (ctypes.c_void_p * len(v))(*v)  # noqa: E731
+    k = _arr(*COEFFS * 5)
+    good = P(A, A)
+    tail = (0.1, 0.9, 1, 0.0, 1.0, 5, k, A)
+    assert f(None, good, None, good, good, 2, 100, 60, *tail, need - 1) == EWORKSPACE
+    assert f(None, None, None, good, good, 2, 100, 60, *tail, need) == EINVAL
+    assert f(None, good, None, None, good, 2, 100, 60, *tail, need) == EINVAL
+    assert f(None, good, None, good, None, 2, 100, 60, *tail, need) == EINVAL
+    assert f(None, P(A, None), None, good, good, 2, 100, 60, *tail, need) == EINVAL
+    assert f(None, good, P(A, None), good, good, 2, 100, 60, *tail, need) == EINVAL
+    assert f(None, P(A, A + 8), None, good, good, 2, 100, 60, *tail, need) == EALIGN
+    assert f(None, good, P(A, A + 8), good, good, 2, 100, 60, *tail, need) == EALIGN
+    for j in (0, 1, 3, 4):
+        t = list(tail)
+        t[j] = float("inf")
+        assert f(None, good, None, good, good, 2, 100, 60, *t, need) == EINVAL, j
+    assert f(None, None, None, None, None, 0, 100, 60, *tail, 0) == OK
+
+
+def test_binding_refusals(monkeypatch):
+    from sharded_linear_amd import ops
+    with pytest.raises(ValueError, match="GPU tensors"):
+        sl.sl_orthogonalize(torch.zeros(4, 4))
+    monkeypatch.setattr(ops, "_device", lambda t: t.device)
+    G = torch.zeros(4, 6)
+    for bad in (G.half(), G[0], G[None, None]):
+        with pytest.raises(ValueError, match="G must be"):
+            sl.sl_orthogonalize(bad)
+    with pytest.raises(ValueError, match="contiguous"):
+        sl.sl_orthogonalize(G.t())
+    with pytest.raises(ValueError, match="coefficients"):
+        sl.sl_orthogonalize(G, steps=2, coefficients=[COEFFS] * 3)
+    with pytest.raises(ValueError, match="steps"):
+        sl.sl_orthogonalize(G, steps=-1)
+    w, m = torch.zeros(4, 6, dtype=BF16), torch.zeros(4, 6)
+    with pytest.raises(ValueError, match="number"):
+        sl.sl_muon_step([w, w.clone()], [G], [m], 0.1)
+    with pytest.raises(TypeError, match="main_grad"):
+        sl.sl_muon_step(w, w, m, 0.1)
+    with pytest.raises(ValueError, match="weight has shape"):
+        sl.sl_muon_step([w, w[:3]], [G, G], [m, m.clone()], 0.1)
+    with pytest.raises(ValueError, match="twice"):
+        sl.sl_muon_step([w, w], [G, G], [m, m.clone()], 0.1)
+    with pytest.raises(ValueError, match="twice"):
+        sl.sl_muon_step([w], [G], [G], 0.1)
+    assert sl.sl_muon_step([], [], [], 0.1) is None
+
+
+# ---- on the GPU -----------------------------------------------------------------------------------
+
+def _gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def _randn(g, *shape):
+    return torch.randn(shape, generator=g, device="cuda")
+
+
+def _iterate(u, steps=5, coefficients=COEFFS):
+    """Newton-Schulz in float64 of one matrix."""
+    u = u.double()
+    n = u.norm()
+    x = u / n if n > 0 else u
+    tall = x.shape[0] > x.shape[1]
+    x = x.t().contiguous() if tall else x
+    ks = [coefficients] * steps if len(coefficients) == 3 and not isinstance(coefficients[0], (tuple, list)) else coefficients
+    for a, b, c in ks:
+        A = x @ x.t().contiguous()
+        x = a * x + (b * A + c * (A @ A)) @ x
+    return x.t() if tall else x
+
+
+def _off(got, ref):
+    return ((got.double() - ref).norm() / ref.norm()).item()
+
+
+def _bound(shape=(16, 16)):
+    """Of fewer than 16 rows or columns nothing averages out: every rounding counts with its whole half step, and they add up:
+    three steps of 2^-11 (1 + 4.8 + 2.8), and the result's 2^-8."""
+    return (OFF ** 2 + BF16_OFF ** 2) ** 0.5 if min(shape[-2:]) >= 16 else 3 * 2.0 ** -11 * 8.6 + 2.0 ** -8
+
+
+# below one tile, at and across the tiles' edges, odd rows, wide, tall, one row, one column
+SHAPES = [(1, 1), (1, 300), (300, 1), (3, 5), (16, 16), (63, 65), (64, 128), (127, 129), (128, 128), (257, 100), (130, 1000), (1000, 131), (384, 384), (512, 256),
+          (250, 2000), (640, 1160), (1024, 1024)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("rows,cols", SHAPES)
+def test_orthogonalize(rows, cols, dtype):
+    say(f"case orthogonalize [{rows}, {cols}] {dtype}")
+    G = (_randn(_gen(rows + cols), rows, cols) * 1e-4).to(dtype)
+    O = sl.sl_orthogonalize(G)
+    assert O.dtype is BF16 and O.shape == G.shape
+    assert _off(O, _iterate(G)) <= _bound(G.shape)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("L,rows,cols", [(2, 5, 7), (3, 65, 130), (7, 200, 100), (33, 24, 40), (70, 10, 9), (5, 513, 515)])
+def test_batches(L, rows, cols):
+    say(f"case orthogonalize {L} x [{rows}, {cols}]")
+    G = _randn(_gen(L), L, rows, cols) * torch.logspace(-8, 8, L, device="cuda")[:, None, None]     # each has its own norm
+    O = sl.sl_orthogonalize(G)
+    for l in range(L):
+        assert _off(O[l], _iterate(G[l])) <= _bound(G.shape), l
+    one = sl.sl_orthogonalize(G[L - 1].clone())
+    assert _off(one, O[L - 1].double()) <= 2 * _bound(G.shape)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,cols", [(2048, 2048), (4104, 300), (300, 4104), (1536, 2048), (2304, 2816)])
+def test_large_tiles(rows, cols):
+    say(f"case orthogonalize [{rows}, {cols}]")
+    G = _randn(_gen(rows), 3, rows, cols)
+    O = sl.sl_orthogonalize(G)
+    for l in range(3):
+        assert _off(O[l], _iterate(G[l])) <= _bound()
+    assert torch.equal(sl.sl_orthogonalize(G), O)
+
+
+@pytest.mark.gpu
+def test_singular_values_over_decades():
+    """Where singular values fall over four decades and over two steps of rank, the small ones are reached as the formula
+    has it: a rounding of X would be multiplied by up to 3.4^5 there, but the first three steps carry what it left."""
+    say("case orthogonalize falling singular values")
+    g = _gen(4)
+    m, n = 256, 640
+    U = torch.linalg.qr(_randn(g, m, m).double())[0]
+    V = torch.linalg.qr(_randn(g, n, m).double())[0]
+    for s in (torch.logspace(0, -4, m, device="cuda").double(), torch.where(torch.arange(m, device="cuda") < m // 4, 1.0, 1e-3).double()):
+        G = ((U * s) @ V.t()).float()
+        for x in (G, G.t().contiguous()):
+            assert _off(sl.sl_orthogonalize(x), _iterate(x)) <= _bound()
+
+
+@pytest.mark.gpu
+def test_steps_and_coefficients():
+    say("case orthogonalize steps and coefficients")
+    G = _randn(_gen(5), 200, 333)
+    for steps in (0, 1, 2, 3, 4, 8):
+        assert _off(sl.sl_orthogonalize(G, steps=steps), _iterate(G, steps)) <= _bound(), steps
+    ks = [(3.4445, -4.7750, 2.0315)] * 3 + [(1.875, -1.25, 0.375)] * 2
+    assert _off(sl.sl_orthogonalize(G, coefficients=ks), _iterate(G, 5, ks)) <= _bound()
+    ks = [(1.5, -0.5, 0.0)] * 14                                               # the cubic iteration, to convergence
+    O = sl.sl_orthogonalize(G, steps=14, coefficients=(1.5, -0.5, 0.0))
+    assert _off(O, _iterate(G, 14, ks)) <= _bound()
+    assert (O.double() @ O.double().t() - torch.eye(200, device="cuda", dtype=torch.float64)).norm() / 200 ** 0.5 <= 3 * _bound()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("power", [-100, -60, 60, 110])
+def test_any_magnitude(power):
+    """The norm is a sum in 64 bits: the scale of a gradient, a power of two, changes no bit of the result."""
+    say(f"case orthogonalize 2^{power}")
+    G = _randn(_gen(6), 70, 50)
+    assert torch.equal(sl.sl_orthogonalize(G * 2.0 ** power), sl.sl_orthogonalize(G))
+
+
+@pytest.mark.gpu
+def test_zeros_and_other_than_numbers():
+    say("case orthogonalize zeros, infinities and NaN")
+    G = _randn(_gen(7), 4, 100, 150)
+    want = sl.sl_orthogonalize(G)
+    G[1], G[2, 5, 7], G[3, 99, 149] = 0, float("nan"), float("inf")
+    O = sl.sl_orthogonalize(G)
+    assert torch.equal(O[0], want[0]) and not O[1].any()
+    assert torch.isnan(O[2]).all() and torch.isnan(O[3]).any()
+
+
+def _muon(W, G, M, lr, mu, nesterov, wd, scale):
+    """The step in float64: new momentum and new weight."""
+    M = mu * M.double() + G.double()
+    U = G.double() + mu * M if nesterov else M
+    return M, (1 - lr * wd) * W.double() - lr * scale * _iterate(U)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("nesterov", [True, False])
+@pytest.mark.parametrize("rows,cols,count", [(100, 60, 1), (61, 130, 3), (512, 256, 2), (24, 40, 40)])
+def test_muon_step(rows, cols, count, nesterov):
+    say(f"case muon {count} x [{rows}, {cols}] nesterov={nesterov}")
+    g = _gen(rows)
+    W = [(_randn(g, rows, cols) * 0.02).to(BF16) for _ in range(count)]
+    masters = [w.float() + 1e-5 * _randn(g, rows, cols) for w in W]
+    G = [_randn(g, rows, cols) * 1e-3 for _ in range(count)]
+    M = [_randn(g, rows, cols) * 1e-2 for _ in range(count)]
+    lr, mu, wd = 0.02, 0.9, 0.1
+    scale = max(1.0, rows / cols) ** 0.5
+    want = [_muon(w, x, m, lr, mu, nesterov, wd, scale) for w, x, m in zip(W, G, M)]
+    kept = [_muon(w, x, m, lr, mu, nesterov, wd, 0.3) for w, x, m in zip(masters, G, M)]
+    W2, M2, kept_g = [w.clone() for w in W], [m.clone() for m in M], [x.clone() for x in G]
+    mass = [(mu * m.abs() + x.abs()).double() for m, x in zip(M, G)]
+    assert sl.sl_muon_step(W, G, M, lr, momentum=mu, nesterov=nesterov, weight_decay=wd) is None
+    for l in range(count):
+        assert ((M[l].double() - want[l][0]).abs() <= 2 * 2.0 ** -24 * mass[l]).all()
+        step = (lr * scale * _iterate(G[l].double() + mu * want[l][0] if nesterov else want[l][0])).norm()
+        # half a bf16 step of every weight, and the iterate's error times lr scale
+        assert (W[l].double() - want[l][1]).norm() <= 2.0 ** -8 * want[l][1].norm() + OFF * step
+        assert torch.equal(G[l], kept_g[l])
+    # fp32 masters take the step; the bf16 weights are their rounding
+    sl.sl_muon_step(W2, G, M2, lr, momentum=mu, nesterov=nesterov, weight_decay=wd, scale=0.3, masters=masters)
+    for l in range(count):
+        assert torch.equal(M2[l], M[l]) and torch.equal(W2[l], masters[l].to(BF16))
+        step = (lr * 0.3 * _iterate(G[l].double() + mu * want[l][0] if nesterov else want[l][0])).norm()
+        assert (masters[l].double() - kept[l][1]).norm() <= 4 * 2.0 ** -24 * kept[l][1].norm() + OFF * step
+
+
+@pytest.mark.gpu
+def test_muon_on_the_buffer():
+    """Weights of three shapes in one buffer, stepped from grad_data into param_data; what is not named stays."""
+    say("case muon on the buffer")
+    g = _gen(9)
+    shapes = {"a": (136, 72), "b": (72, 136), "c": (136, 72), "norm": (136,), "d": (64, 64)}
+    buf = sl.ParamAndGradBuffer(shapes, "cuda", bucket_size=None)
+    buf.param_data.copy_((_randn(g, buf.numel) * 0.02).to(BF16))
+    buf.grad_data.copy_(_randn(g, buf.numel) * 1e-3)
+    momentum = torch.zeros_like(buf.grad_data)
+    old, names = buf.param_data.clone(), ["a", "b", "c", "d"]
+    want = {n: _muon(buf.param(n), buf.main_grad(n), torch.zeros(shapes[n], device="cuda"), 0.05, 0.95, True, 0.01,
+                     max(1.0, shapes[n][0] / shapes[n][1]) ** 0.5) for n in names}
+    buf.muon_step(names, momentum, 0.05, weight_decay=0.01)
+    inside = torch.zeros(buf.numel, dtype=torch.bool, device="cuda")
+    for n in names:
+        s, e, _ = buf.index[n]
+        inside[s:e] = True
+        assert torch.equal(momentum[s:e], buf.grad_data[s:e])
+        step = (want[n][1] - old[s:e].view(shapes[n]).double()).norm()
+        assert (buf.param(n).double() - want[n][1]).norm() <= 2.0 ** -8 * want[n][1].norm() + OFF * step
+    assert torch.equal(buf.param_data[~inside], old[~inside]) and not momentum[~inside].any()
+    with pytest.raises(ValueError, match="momentum_data"):
+        buf.muon_step(names, momentum[:-1], 0.05)
+
+
+@pytest.mark.gpu
+def test_empty_extents():
+    say("case orthogonalize nothing")
+    assert sl.sl_orthogonalize(torch.zeros((0, 5, 6), device="cuda")).shape == (0, 5, 6)
+    assert sl.sl_orthogonalize(torch.zeros((2, 0, 6), device="cuda")).shape == (2, 0, 6)
+
+
+@pytest.mark.gpu
+def test_captured_and_replayed():
+    say("case muon graphs")
+    g = _gen(10)
+    G = _randn(g, 2, 300, 200)
+    W, M = (_randn(g, 300, 200) * 0.02).to(BF16), torch.zeros((300, 200), device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        sl.sl_orthogonalize(G)
+        sl.sl_muon_step(W.clone(), G[0].clone(), M.clone(), 0.1)
+    torch.cuda.current_stream().wait_stream(s)
+    grad = G[0].clone()
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    with torch.cuda.graph(graphs[0]):
+        O = sl.sl_orthogonalize(G)
+    with torch.cuda.graph(graphs[1]):
+        sl.sl_muon_step(W, grad, M, 0.1)
+    for r in range(3):
+        G.copy_(_randn(g, 2, 300, 200))
+        grad.copy_(G[1])
+        W2, M2 = W.clone(), M.clone()
+        graphs[r % 2].replay()
+        graphs[1 - r % 2].replay()
+        sl.sl_muon_step(W2, grad, M2, 0.1)
+        want = sl.sl_orthogonalize(G)
+        torch.cuda.synchronize()
+        assert torch.equal(O, want) and torch.equal(W, W2) and torch.equal(M, M2)
