@@ -2,26 +2,28 @@
 #pragma once
 #include <hip/hip_runtime.h>
 
+#include <cstddef>
 #include <cstdint>
 
-// C[M][N] = alpha * A . B + beta * (D + Dlo / 2^11) for each of `batches` matrices, sums in fp32, results rounded to
-// fp16 once; with clo, what the rounding left, times 2^11, goes there (fp16).  A is [M][K]; B is [N][K] (half_gemm_nt) or
-// [K][N] (half_gemm_nn).  M, N and K are multiples of 128; matrices are dense and follow each other without gaps.
+// C[M][N] = alpha * A . B + beta * D + diag * I for each of `batches` matrices, summed in fp32 and rounded to fp16 once;
+// with clo, what that rounding left, times 2^11, goes there (fp16).  A is [M][K] and B [N][K] (half_gemm_sym) or [K][N]
+// (half_gemm_nn).  M, N and K are multiples of 128; matrices are dense and follow each other without gaps.
 struct HalfArgs {
   const void *a, *b;           // the first matrix of each
-  const void *d, *dlo;         // like C; may be null, dlo alone too
-  void *c, *clo;               // c is no operand and not d; clo null, or another matrix or dlo itself
+  const void* d;               // like C, or null
+  void *c, *clo;               // C is no operand and not D; clo null, or like C, D itself if need be
   int M, N, K;
   int64_t batches;
-  float alpha, beta;
-  // set by the launchers, and by the kernels to the matrix of the workgroup
-  int64_t lda, ldb;
-  uint32_t a_bytes, b_bytes;
-  int tiles_m, tiles_n;
+  float alpha, beta, diag;
+  float* ws;                   // half_gemm_workspace_bytes() for split sums
+  // set by the launchers
+  int tiles_m, tiles_n, full, rest, splits, kt_per_split;
 };
 constexpr int kHalfPad = 128;
 
-// A and B K-major.  Where the result is known to be symmetric (`sym`, M == N), tiles on and below the diagonal are
-// computed and those below written a second time, transposed.
-int half_gemm_nt(hipStream_t st, HalfArgs g, bool sym);
+// A . B^T of a product known to be symmetric (M == N): tiles on and below the diagonal are computed and those below it
+// written a second time, transposed.
+int half_gemm_sym(hipStream_t st, HalfArgs g);
 int half_gemm_nn(hipStream_t st, HalfArgs g);
+// Workspace of either with these extents (nn: M, N, K; sym: M == N).
+size_t half_gemm_workspace_bytes(int M, int N, int K, int64_t batches, bool sym);

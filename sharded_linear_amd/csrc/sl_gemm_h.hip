@@ -1,6 +1,16 @@
-// fp16 products of the orthogonalised update (gfx950): the fixed-order main loop of the bf16 kernels (sl_gemm4.h) on
-// v_mfma_f32_16x16x32_f16, with batches of matrices, symmetric results, and an epilogue that adds a multiple of a third
-// matrix in fp32 before the one rounding.
+// fp16 products of the orthogonalised update (gfx950) on v_mfma_f32_16x16x32_f16: batches of matrices, symmetric
+// results, and an epilogue that adds a multiple of a third matrix and of the unit matrix in fp32 before the one rounding.
+//
+// A workgroup walks a list of items (a tile, or a part of a tile's sum) and the stages of one item follow those of the
+// item before without a gap: operands go HBM -> LDS directly, 64 k to a stage, two stages deep, in the fixed issue order
+// of the bf16 kernels (sl_gemm4.h holds the operand layouts).  The loads of stage s + 2 go out behind the barrier that ends the
+// reads of stage s, whichever item it belongs to, so an item starts with its first two stages in LDS or under way, and
+// only its results' stores stand between its products and the next item's.  Results leave straight from the
+// accumulators: the 16-lane groups of a wave trade pieces, so that a lane has 8 columns of a row.
+//
+// Tiles are dealt out in whole rounds of the chip; where the last round would leave workgroups idle, its tiles' sums are
+// split into fp32 planes (kept in the accumulators' own order, whole lines a store) which a second kernel adds in order
+// and finishes through the same epilogue.
 #include <hip/hip_runtime.h>
 
 #include <atomic>
@@ -11,160 +21,429 @@
 
 namespace sl2 {
 
-// Lower triangle of a grid of tiles, row by row: tile t is row i, column j <= i.
-__device__ __forceinline__ void triangle(int t, int& i, int& j) {
-  i = int((sqrtf(8.f * float(t) + 1.f) - 1.f) * 0.5f);
-  while ((i + 1) * (i + 2) / 2 <= t) ++i;
-  while (i * (i + 1) / 2 > t) --i;
-  j = t - i * (i + 1) / 2;
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// ---- items ---------------------------------------------------------------------------------------
+
+struct HalfItem { int batch, m0, n0, kt0, kt1, plane; };      // plane < 0: the whole sum; all wave-uniform
+
+// Row and column of tile `t` of a lower triangle of n x n tiles in groups of 4 rows, column by column, so that tiles near each other in the
+// order share rows and columns: group q holds (4 q + 1) columns of all its rows, then the corner at the diagonal.
+__device__ __forceinline__ int2 triangle(int t, int n) {
+  int q = int((sqrtf(4.f + 32.f * float(t)) - 2.f) * (1.f / 16.f));
+  while ((8 * (q + 1) + 2) * (q + 1) <= t) ++q;
+  while ((8 * q + 2) * q > t) --q;
+  const int rows = min(n - 4 * q, 4), whole = (4 * q + 1) * rows, u = t - (8 * q + 2) * q;
+  if (u < whole) return make_int2(4 * q + u % rows, u / rows);
+  // the corner's columns of rows - 1, rows - 2, .. tiles
+  const int v = u - whole, d = v < rows - 1 ? 1 : v < 2 * rows - 3 ? 2 : 3;
+  const int j = 4 * q + d;
+  return make_int2(j + v - (d == 1 ? 0 : d == 2 ? rows - 1 : 2 * rows - 3), j);
 }
 
-template <int WM, int WN>
-__device__ __forceinline__ void store_rows(char* ep, _Float16* C, int64_t ldc, int M, int N, int mw, int nw, int lane) {
-  using E = Epi<WN, WM, false>;
-  const int rr = lane / E::kCPR, cr = lane % E::kCPR, n = nw + cr * 8;
-#pragma unroll
-  for (int t = 0; t < WM / E::kRPI; ++t) {
-    const int r = t * E::kRPI + rr, m = mw + r;
-    const uint4 v = *reinterpret_cast<const uint4*>(ep + E::off(r, cr));
-    if (m < M && n < N) *reinterpret_cast<uint4*>(C + int64_t(m) * ldc + n) = v;
-  }
-}
-
-// The same wave tile, transposed: a group of 16 lanes reads 4 x 16 blocks through transposing reads (source lane 4j + q:
-// row j, columns 4q .. 4q + 3; result lane s: column s, 4 rows), twice for 8 rows of its column, and the four groups take
-// 32 rows, so that a row of the result gets 64 bytes a store.
-template <int WM, int WN>
-__device__ __forceinline__ void store_transposed(char* ep, _Float16* C, int64_t ldc, int M, int N, int mw, int nw, int lane) {
-  using E = Epi<WN, WM, false>;
-  const int g = lane >> 4, s = lane & 15, j = s >> 2, q = s & 3;
-#pragma unroll
-  for (int cb = 0; cb < WN / 16; ++cb) {
-    const int col = 16 * cb + 4 * q;
-#pragma unroll
-    for (int mb = 0; mb < WM / 32; ++mb) {
-      const int row = 32 * mb + 8 * g;
-      const char* p0 = ep + E::off(row + j, col / 8) + 2 * (col % 8);
-      const char* p1 = ep + E::off(row + 4 + j, col / 8) + 2 * (col % 8);
-      const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4*)p0);
-      const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4*)p1);
-      const uint2 a = __builtin_bit_cast(uint2, lo), b = __builtin_bit_cast(uint2, hi);
-      const int n = nw + 16 * cb + s, m = mw + row;
-      if (n < N && m < M) *reinterpret_cast<uint4*>(C + int64_t(n) * ldc + m) = make_uint4(a.x, a.y, b.x, b.y);
-    }
-  }
-}
-
-template <class P, bool SYM, int OCC>
-__global__ void __launch_bounds__(P::WAVES * 64, OCC) half_gemm(HalfArgs g) {
-  constexpr int WM = P::WM, WN = P::WN, TM = P::TM, TN = P::TN;
-  extern __shared__ __attribute__((aligned(1024))) char smem[];
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int per = SYM ? g.tiles_m * (g.tiles_m + 1) / 2 : g.tiles_m * g.tiles_n;
-  const int t = xcd_remap(blockIdx.x, gridDim.x), batch = t / per, tile = t % per;
+template <class P, bool SYM>
+__device__ __forceinline__ HalfItem half_item(const HalfArgs& g, int x) {
+  const int per = SYM ? g.tiles_m * (g.tiles_m + 1) / 2 : g.tiles_m * g.tiles_n, stages = g.K / P::BK;
+  const bool part = x >= g.full;               // the parts of a tile are neighbours in the order
+  const int plane = part ? x - g.full : -1, tile = part ? g.full + plane / g.splits : x;
+  const int kt0 = part ? plane % g.splits * g.kt_per_split : 0, kt1 = part ? min(stages, kt0 + g.kt_per_split) : stages;
+  const int batch = tile / per, t = tile % per;
   int tm, tn;
   if constexpr (SYM) {
-    triangle(tile, tm, tn);
+    const int2 at = triangle(t, g.tiles_m);
+    tm = at.x;
+    tn = at.y;
   } else {
     constexpr int GR = 4;
-    const int first = tile / (GR * g.tiles_n) * GR, rows = min(g.tiles_m - first, GR), in = tile % (GR * g.tiles_n);
+    const int first = t / (GR * g.tiles_n) * GR, rows = min(g.tiles_m - first, GR), in = t % (GR * g.tiles_n);
     tm = first + in % rows;
     tn = in / rows;
   }
-  const int m0 = tm * P::BM, n0 = tn * P::BN;
-  g.a = static_cast<const _Float16*>(g.a) + int64_t(batch) * g.M * g.K;
-  g.b = static_cast<const _Float16*>(g.b) + int64_t(batch) * g.N * g.K;
+  return HalfItem{batch, __builtin_amdgcn_readfirstlane(tm * P::BM), __builtin_amdgcn_readfirstlane(tn * P::BN), kt0, kt1, plane};
+}
+
+// ---- epilogue ------------------------------------------------------------------------------------
+// A wave finishes 32 rows by 64 columns at a time: lane l holds row 16 i + l % 16 and columns 16 j + 4 (l / 16) + 0..3 of
+// blocks [2][4].  M and N are multiples of 128, so such a piece lies wholly inside the matrix or outside.
+
+// Blocks j and j + 1 as fp16 words: afterwards lane group g holds columns 8 (g / 2) .. + 7 of block j + g % 2 (its own
+// inverse).
+__device__ __forceinline__ u32x4 trade(u32x4 v) {
+  const auto a = __builtin_amdgcn_permlane16_swap(v[0], v[2], false, false), b = __builtin_amdgcn_permlane16_swap(v[1], v[3], false, false);
+  return u32x4{a[0], b[0], a[1], b[1]};
+}
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t half_rows(const void* p, int64_t first, int64_t bytes, bool in) {
+  return __builtin_amdgcn_make_buffer_rsrc(static_cast<char*>(const_cast<void*>(p)) + first, 0, in ? int(bytes) : 0, kRsrcWord3);
+}
+
+constexpr int kStageBytes = 32 * 64 * 2;       // a wave's piece in LDS, for its transposed copy
+
+// `lds`: kStageBytes of the wave's own, used where `mirror` asks for the transposed copy too.
+__device__ __forceinline__ void half_finish(const HalfArgs& g, f32x4v (&acc)[2][4], int batch, int m, int n, bool mirror, uint32_t lds, int lane) {
+  const bool in = m < g.M && n < g.N;
+  const int64_t first = (int64_t(batch) * g.M + m) * g.N * 2, bytes = int64_t(32) * g.N * 2;
+  const int rl = lane & 15, gl = lane >> 4;
+  const uint32_t off = uint32_t(rl) * uint32_t(g.N) * 2 + uint32_t(n + 16 * (gl & 1) + 8 * (gl >> 1)) * 2;
+  const uint32_t down = uint32_t(g.N) * 32;    // 16 rows
+  auto wide = [](uint32_t a, uint32_t b) { return __builtin_convertvector(__builtin_bit_cast(f16x4, make_uint2(a, b)), f32x4v); };
+  auto words = [](f32x4v v) { return __builtin_bit_cast(uint2, __builtin_convertvector(v, f16x4)); };
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] *= g.alpha;
+  if (g.d) {
+    const auto rd = half_rows(g.d, first, bytes, in);
+    u32x4 d[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int p = 0; p < 2; ++p) d[i][p] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rd, off + 64 * p + i * down, 0, 0));
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const u32x4 w = trade(d[i][p]);
+        acc[i][2 * p] += wide(w[0], w[1]) * g.beta;
+        acc[i][2 * p + 1] += wide(w[2], w[3]) * g.beta;
+      }
+  }
+  if (g.diag != 0.f && m < n + 64 && n < m + 32) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (m + 16 * i + rl == n + 16 * j + 4 * gl + e) acc[i][j][e] += g.diag;
+  }
+  const auto rc = half_rows(g.c, first, bytes, in);
+  u32x4 hi[2][2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const uint2 a = words(acc[i][2 * p]), b = words(acc[i][2 * p + 1]);
+      hi[i][p] = trade(u32x4{a.x, a.y, b.x, b.y});
+      __builtin_amdgcn_raw_buffer_store_b128(hi[i][p], rc, off + 64 * p + i * down, 0, 0);
+    }
+  if (g.clo) {
+    const auto rl_ = half_rows(g.clo, first, bytes, in);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        uint2 w[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const f32x4v v = acc[i][2 * p + h];
+          w[h] = words((v - __builtin_convertvector(__builtin_convertvector(v, f16x4), f32x4v)) * 0x1p11f);
+        }
+        __builtin_amdgcn_raw_buffer_store_b128(trade(u32x4{w[0].x, w[0].y, w[1].x, w[1].y}), rl_, off + 64 * p + i * down, 0, 0);
+      }
+  }
+  if (!mirror) return;
+  // Rows of 8 chunks in LDS, chunks XOR-swizzled by row; a group of 16 lanes then reads 4 x 16 blocks through transposing
+  // reads (source lane 4j + q: row j, columns 4q .. 4q + 3; result lane s: column s, 4 rows), twice for 8 rows of its
+  // column, and the four groups take the 32 rows, so that a row of the copy gets 64 bytes a store.
+  typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
+  typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
+  auto at = [&](int r, int c) { return lds + uint32_t(r * 128 + ((c ^ (r & 7)) << 4)); };
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int p = 0; p < 2; ++p) *(lds_u32x4*)(uintptr_t)at(16 * i + rl, 4 * p + 2 * (gl & 1) + (gl >> 1)) = hi[i][p];
+  asm volatile("" ::: "memory");
+  const auto rt = half_rows(g.c, (int64_t(batch) * g.M + n) * g.N * 2, int64_t(64) * g.N * 2, in);
+  const int jr = rl >> 2, q = rl & 3;
+#pragma unroll
+  for (int cb = 0; cb < 4; ++cb) {
+    const int col = 16 * cb + 4 * q, row = 8 * gl + jr;
+    const i16x4 lo4 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(uintptr_t)(at(row, col / 8) + 2 * (col % 8)));
+    const i16x4 hi4 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(uintptr_t)(at(row + 4, col / 8) + 2 * (col % 8)));
+    const uint2 a = __builtin_bit_cast(uint2, lo4), b = __builtin_bit_cast(uint2, hi4);
+    __builtin_amdgcn_raw_buffer_store_b128(u32x4{a.x, a.y, b.x, b.y}, rt, uint32_t(16 * cb + rl) * uint32_t(g.N) * 2 + uint32_t(m + 8 * gl) * 2, 0, 0);
+  }
+  asm volatile("" ::: "memory");
+}
+
+// ---- the kernel ----------------------------------------------------------------------------------
+
+template <class P, bool SYM, int OCC>
+__global__ void __launch_bounds__(P::WAVES * 64, OCC) half_gemm(HalfArgs g) {
+  constexpr int BK = P::BK, WAVES = P::WAVES, WM = P::WM, WN = P::WN, TM = P::TM, TN = P::TN, KS = P::KS;
+  constexpr int LA = P::LA, LB = P::LB, LPS = LA + LB, kStage = P::kStage, NR = TM + TN;
+  constexpr bool B_KM = P::B_KM;
+  using OA = typename P::OA;
+  using OB = typename P::OB;
+  static_assert(P::S == 2 && BK == 2 * KS && TN == 4 && WN == 64 && TM % 2 == 0, "two steps a stage, pieces of 32 x 64");
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / P::WGN, wn = wave % P::WGN;
+  const uint32_t lds0 = lds_addr(smem);
+
+  // Each XCD takes a contiguous range of the whole tiles and one of the parts, its workgroups side by side in them.
+  const int xcd = blockIdx.x % kXCD, slot0 = blockIdx.x / kXCD, stride = (int(gridDim.x) - xcd + kXCD - 1) / kXCD;
+  auto range = [&](int n, int& lo, int& hi) {
+    const int per = n / kXCD, rem = n % kXCD;
+    lo = xcd * per + min(xcd, rem);
+    hi = lo + per + (xcd < rem);
+  };
+  int f0, f1, p0, p1;
+  range(g.full, f0, f1);
+  range(g.rest * g.splits, p0, p1);
+  const int nf = f1 - f0 > slot0 ? (f1 - f0 - slot0 + stride - 1) / stride : 0;
+  const int np = p1 - p0 > slot0 ? (p1 - p0 - slot0 + stride - 1) / stride : 0;
+  const int count = nf + np;
+  if (count == 0) return;
+  auto nth = [&](int q) { return half_item<P, SYM>(g, q < nf ? f0 + slot0 + q * stride : g.full + p0 + slot0 + (q - nf) * stride); };
+
+  // Lane offsets of the loads and fragment reads, the same for every tile: descriptors begin at the tile.  A wave's loads
+  // of an operand differ by whole multiples of 16 rows, over which the swizzles repeat, so one lane offset and a scalar
+  // serve them all; a K-major fragment's second step is the other half of each 128-byte row.
+  uint32_t va[1], vb[1], ofb[B_KM ? 1 : TN];
+  const int64_t ldb = B_KM ? g.K : g.N;
+  OA::template prep<WAVES>(va, lane, wave, 0, P::BM, g.K);
+  OB::template prep<WAVES>(vb, lane, wave, 0, P::BN, ldb);
+  const uint32_t ofa = kmaj_frag_off16<OA>(wm * WM, 0, lane);
+  if constexpr (B_KM) ofb[0] = OA::kBytes + kmaj_frag_off16<OB>(wn * WN, 0, lane);
+  else
+#pragma unroll
+    for (int j = 0; j < TN; ++j) ofb[j] = OA::kBytes + mnmaj_frag_off16<OB>(wn * WN + 16 * j, lane);
+  constexpr int kRowsA = WAVES * 64 / OA::kCPR, kRowsB = WAVES * 64 / OB::kCPR;        // rows of one load of all waves
+  static_assert(kRowsA % 16 == 0 && kRowsB % 16 == 0, "the swizzles' period");
+  const uint32_t a_rows = uint32_t(kRowsA) * uint32_t(g.K) * 2, b_rows = uint32_t(kRowsB) * uint32_t(ldb) * 2;
+  const uint32_t ka_step = BK * 2, kb_step = B_KM ? BK * 2 : uint32_t(BK) * uint32_t(g.N) * 2;
+
+  // The item being loaded: operands as descriptors from the tile's first element to the matrix's end.  A tile's second
+  // half of rows may lie past the end as a whole (extents are multiples of 128): its descriptor then has no bytes, and the
+  // loads write zeros.  Columns past a K x N operand's edge read what follows in the workspace, and no result of theirs is
+  // stored.
+  i32x4 ra, rb;
+  int a_high, b_high;                          // bytes of the second halves' descriptors
+  uint32_t ka, kb;
+  int lq = 0, left;
+  auto open = [&](const HalfItem it) {
+    ra = rsrc_uniform(static_cast<const _Float16*>(g.a) + (int64_t(it.batch) * g.M + it.m0) * g.K, uint32_t(int64_t(g.M - it.m0) * g.K * 2));
+    a_high = it.m0 + P::BM / 2 < g.M ? ra[2] : 0;
+    if constexpr (B_KM)
+      rb = rsrc_uniform(static_cast<const _Float16*>(g.b) + (int64_t(it.batch) * g.N + it.n0) * g.K, uint32_t(int64_t(g.N - it.n0) * g.K * 2));
+    else
+      rb = rsrc_uniform(static_cast<const _Float16*>(g.b) + int64_t(it.batch) * g.K * g.N + it.n0, uint32_t((int64_t(g.K) * g.N - it.n0) * 2));
+    b_high = !B_KM || it.n0 + P::BN / 2 < g.N ? rb[2] : 0;
+    ka = uint32_t(it.kt0) * ka_step;
+    kb = uint32_t(it.kt0) * kb_step;
+    left = it.kt1 - it.kt0;
+  };
+  auto advance = [&]() {                       // to the next stage of the list; past its end, descriptors of no bytes
+    ka += ka_step;
+    kb += kb_step;
+    if (--left == 0) {
+      if (++lq < count) open(nth(lq));
+      else ra[2] = rb[2] = a_high = b_high = 0;
+    }
+  };
+  auto load_one = [&](auto ic_l, uint32_t base) {
+    constexpr int l = decltype(ic_l)::value;
+    i32x4 r = l < LA ? ra : rb;
+    if constexpr (l >= LA / 2 && l < LA) r[2] = a_high;
+    if constexpr (l >= LA + LB / 2) r[2] = b_high;
+    if constexpr (l < LA) lds_dma16s(r, base + (l * WAVES + wave) * 1024, va[0], ka + l * a_rows);
+    else lds_dma16s(r, base + OA::kBytes + ((l - LA) * WAVES + wave) * 1024, vb[0], kb + (l - LA) * b_rows);
+  };
 
   f32x4v acc[TM][TN];
-  gemm4_core<P>(g, smem, lane, wave, m0, n0, 0, (g.K + P::BK - 1) / P::BK, acc);
-  asm_wait_vm<0>();
-  __syncthreads();          // every wave is past its last operand read: the ring becomes epilogue space
-
-  // Lane l holds row 16 i + l % 16 and columns 16 j + 4 (l / 16) + 0..3 of its wave tile.  Each wave stages its own
-  // part of LDS, and reads D where its accumulators lie.
-  const int64_t base = int64_t(batch) * g.M * g.N, ldc = g.N;
-  const int mw = m0 + wave / P::WGN * WM, nw = n0 + wave % P::WGN * WN;
-  const int rl = lane & 15, gl = lane >> 4;
-  char* ep = smem + wave * Epi<WN, WM, false>::kBytes;
-  const _Float16* D = static_cast<const _Float16*>(g.d);
-  const _Float16* Dlo = static_cast<const _Float16*>(g.dlo);
-#pragma unroll
-  for (int i = 0; i < TM; ++i)
-#pragma unroll
-    for (int j = 0; j < TN; ++j) {
-      acc[i][j] *= g.alpha;
-      const int m = mw + 16 * i + rl, n = nw + 16 * j + 4 * gl;
-      if (D && m < g.M && n < g.N) {
-        const int64_t at = base + int64_t(m) * ldc + n;
-        f32x4v d = __builtin_convertvector(*reinterpret_cast<const f16x4*>(D + at), f32x4v);
-        if (Dlo) d += __builtin_convertvector(*reinterpret_cast<const f16x4*>(Dlo + at), f32x4v) * 0x1p-11f;
-        acc[i][j] += d * g.beta;
-      }
-    }
-  auto stage = [&](auto part) {
+  bf16x8 fa[2][TM], fb[2][TN];
+  auto clear = [&]() {
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
-      for (int j = 0; j < TN; ++j)
-        *reinterpret_cast<f16x4*>(ep + Epi<WN, WM, false>::off(i * 16 + rl, 2 * j + (gl >> 1)) + 8 * (gl & 1)) = part(acc[i][j]);
-    asm volatile("" ::: "memory");       // the wave's lanes read each other's pieces, in order behind these writes
+      for (int j = 0; j < TN; ++j) acc[i][j] = f32x4v{0.f, 0.f, 0.f, 0.f};
   };
-  auto high = [](f32x4v v) { return __builtin_convertvector(v, f16x4); };
-  stage(high);
-  _Float16* C = static_cast<_Float16*>(g.c) + base;
-  store_rows<WM, WN>(ep, C, ldc, g.M, g.N, mw, nw, lane);
-  if constexpr (SYM) {
-    if (tm != tn) store_transposed<WM, WN>(ep, C, ldc, g.M, g.N, mw, nw, lane);
-  } else {
-    if (g.clo) {
-      asm volatile("" ::: "memory");
-      stage([&](f32x4v v) { return __builtin_convertvector((v - __builtin_convertvector(high(v), f32x4v)) * 0x1p11f, f16x4); });
-      store_rows<WM, WN>(ep, static_cast<_Float16*>(g.clo) + base, ldc, g.M, g.N, mw, nw, lane);
+  auto read_one = [&](auto ic_m, auto ic_to, auto ic_ks, uint32_t base) {
+    constexpr int m = decltype(ic_m)::value, to = decltype(ic_to)::value, ks = decltype(ic_ks)::value;
+    if constexpr (m < TM) fa[to][m] = lds_rd128<m * 16 * OA::kRowBytes>((base + ofa) ^ (64 * ks));
+    else if constexpr (B_KM) fb[to][m - TM] = lds_rd128<(m - TM) * 16 * OB::kRowBytes>((base + ofb[0]) ^ (64 * ks));
+    else fb[to][m - TM] = lds_rd_tr<ks * KS * OB::kRowBytes, (ks * KS + 4) * OB::kRowBytes>(base + ofb[m - TM]);
+  };
+  // One step: the products on buffer CUR, with the next step's fragment reads over the first three quarters of them and,
+  // in a stage's second step, the loads spread over all.
+  auto step = [&](auto ic_cur, uint32_t rbase, uint32_t lbase) {
+    constexpr int cur = decltype(ic_cur)::value, NL = cur ? LPS : 0, NQ = TM * TN, RQ = NQ * 3 / 4;
+    static_for<NQ>([&](auto qc) {
+      constexpr int q = decltype(qc)::value, i = q / TN, j = (i & 1) ? TN - 1 - q % TN : q % TN;
+      acc[i][j] = mfma16<true>(fb[cur][j], fa[cur][i], acc[i][j]);
+      constexpr int rlo = q < RQ ? q * NR / RQ : NR, rhi = q < RQ ? (q + 1) * NR / RQ : NR;
+      static_for<rhi - rlo>([&](auto mc) { read_one(ic<rlo + decltype(mc)::value>{}, ic<cur ^ 1>{}, ic<cur ^ 1>{}, rbase); });
+      constexpr int llo = (2 * q * NL + NQ) / (2 * NQ), lhi = (2 * (q + 1) * NL + NQ) / (2 * NQ);
+      static_for<lhi - llo>([&](auto mc) { load_one(ic<llo + decltype(mc)::value>{}, lbase); });
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  };
+
+  HalfItem it = nth(0);
+  open(it);
+  static_for<LPS>([&](auto lc) { load_one(lc, lds0); });
+  advance();
+  static_for<LPS>([&](auto lc) { load_one(lc, lds0 + kStage); });
+  advance();
+  asm_wait_vm<LPS>();
+  bare_barrier();
+  static_for<NR>([&](auto mc) { read_one(mc, ic<0>{}, ic<0>{}, lds0); });
+  __builtin_amdgcn_sched_barrier(0);
+  clear();
+
+  uint32_t cur = lds0, nxt = lds0 + kStage;
+  bool stores = false;                         // the results of an item went out since the last wait
+  for (int q = 0;;) {
+    for (int k = it.kt0; k < it.kt1; ++k) {
+      step(ic<0>{}, cur, 0);
+      // The next stage has landed: memory operations return in order, and each item's results are at least 2 TM stores of
+      // every wave, all younger than that stage's loads.
+      if (stores) asm_wait_vm<2 * TM>();
+      else asm_wait_vm<0>();
+      stores = false;
+      lds_barrier();
+      step(ic<1>{}, nxt, cur);
+      advance();
+      const uint32_t t = cur;
+      cur = nxt;
+      nxt = t;
     }
+    const int m = it.m0 + wm * WM, n = it.n0 + wn * WN;
+    if (it.plane < 0) {
+#pragma unroll
+      for (int i = 0; i < TM / 2; ++i) {
+        f32x4v piece[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) piece[h][j] = acc[2 * i + h][j];
+        half_finish(g, piece, it.batch, m + 32 * i, n, SYM && it.m0 != it.n0, lds0 + 2 * kStage + wave * kStageBytes, lane);
+      }
+    } else {
+      f32x4v* to = reinterpret_cast<f32x4v*>(g.ws) + (int64_t(it.plane) * WAVES + wave) * (TM * TN * 64) + lane;
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) to[(i * TN + j) * 64] = acc[i][j];
+    }
+    asm volatile("" ::: "memory");
+    if (++q == count) break;
+    stores = true;
+    clear();
+    it = nth(q);
   }
+  asm_wait_vm<0>();
 }
 
-template <class P, bool SYM, int OCC>
-int launch_half(hipStream_t st, HalfArgs g) {
-  auto kfn = half_gemm<P, SYM, OCC>;
-  static std::atomic<uint64_t> attr{0};
-  if (smem_attr_once(reinterpret_cast<const void*>(kfn), P::kLds, attr)) return -5;
-  g.tiles_m = (g.M + P::BM - 1) / P::BM;
-  g.tiles_n = (g.N + P::BN - 1) / P::BN;
-  const int64_t tiles = SYM ? int64_t(g.tiles_m) * (g.tiles_m + 1) / 2 : int64_t(g.tiles_m) * g.tiles_n;
-  hipLaunchKernelGGL(kfn, dim3(unsigned(tiles * g.batches)), dim3(P::WAVES * 64), P::kLds, st, g);
-  return hipGetLastError() == hipSuccess ? 0 : -5;
+// Adds the planes of the tiles from g.full on, in order, and finishes them: a wave to 32 rows by 64 columns.
+template <class P, bool SYM>
+__global__ void __launch_bounds__(64) half_join(HalfArgs g) {
+  __shared__ __attribute__((aligned(16))) char stage[kStageBytes];
+  constexpr int PIECES = P::TM / 2;
+  const int lane = threadIdx.x, piece = blockIdx.x % PIECES, wave = blockIdx.x / PIECES % P::WAVES, tile = blockIdx.x / (PIECES * P::WAVES);
+  f32x4v acc[2][4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4v{0.f, 0.f, 0.f, 0.f};
+  for (int s = 0; s < g.splits; ++s) {
+    const f32x4v* from = reinterpret_cast<const f32x4v*>(g.ws) + (int64_t(tile * g.splits + s) * P::WAVES + wave) * (P::TM * P::TN * 64) + lane;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] += from[((2 * piece + i) * P::TN + j) * 64];
+  }
+  const HalfItem it = half_item<P, SYM>(g, g.full + tile * g.splits);
+  half_finish(g, acc, it.batch, it.m0 + wave / P::WGN * P::WM + 32 * piece, it.n0 + wave % P::WGN * P::WN, SYM && it.m0 != it.n0, lds_addr(stage), lane);
 }
 
-// 256x256 tiles of 8 waves, one workgroup a CU, and 128x128 tiles of 4 waves, two a CU; both two stages of 64 k.
+// ---- host ----------------------------------------------------------------------------------------
+
+// 256x256 tiles of 8 waves, one workgroup a CU, and 128x128 tiles of 4 waves, two a CU.
 template <bool B_KM> using Big = G4<true, B_KM, false, 2, 2, 4, 64, 256, 16, 256, true>;
 template <bool B_KM> using Small = G4<true, B_KM, false, 2, 2, 2, 64, 128, 16, 128, true>;
 
-// Whether 256x256 tiles fill the chip: their rounds over 256 CUs cost less than those of 128x128 tiles over 512 places,
-// whose workgroups reach about 0.7 of their rate.
-bool big_tiles(const HalfArgs& g, bool sym) {
-  auto tiles = [&](int64_t e) {
-    const int64_t m = (g.M + e - 1) / e, n = (g.N + e - 1) / e;
-    return g.batches * (sym ? m * (m + 1) / 2 : m * n);
-  };
-  const double big = double((tiles(256) + 255) / 256), small = double((tiles(128) + 511) / 512) * 0.5 / 0.7;
-  return big <= small;
+struct HalfPlan {
+  bool big;
+  int64_t tiles, full, rest;
+  int splits, kt_per_split;
+  double us;
+};
+
+// Estimated time of a product in tiles of `edge`: whole rounds over the `places` of the chip, and a last one of `rest`
+// tiles whose sums may be split into up to `places` parts.
+HalfPlan half_plan_of(int M, int N, int K, int64_t batches, bool sym, bool big) {
+  const int edge = big ? 256 : 128, places = big ? 256 : 512;
+  const double stage = big ? 1.4 : 1.0, fixed = big ? 6.0 : 4.0;         // us of a 64 k stage, and of an item beside its stages
+  const int64_t m = (M + edge - 1) / edge, n = (N + edge - 1) / edge;
+  HalfPlan p{};
+  p.big = big;
+  p.tiles = batches * (sym ? m * (m + 1) / 2 : m * n);
+  p.rest = p.tiles % places;
+  p.full = p.tiles - p.rest;
+  const int stages = K / 64;
+  p.splits = 1;
+  p.kt_per_split = stages;
+  double last = p.rest ? fixed + stages * stage : 0;
+  for (int s = 2; p.rest && s <= places / p.rest && s <= stages / 4; ++s) {
+    const int per = (stages + s - 1) / s, parts = (stages + per - 1) / per;
+    const double t = fixed + per * stage + 5.0 + double(p.rest * parts) * edge * edge * 8 / 4.0e6;   // planes out and back at 4 TB/s
+    if (t < last) {
+      last = t;
+      p.splits = parts;
+      p.kt_per_split = per;
+    }
+  }
+  if (p.splits == 1) {
+    p.full = p.tiles;
+    p.rest = 0;
+  }
+  p.us = double(p.tiles / places) * (fixed + stages * stage) + last;
+  return p;
+}
+
+HalfPlan half_plan(int M, int N, int K, int64_t batches, bool sym) {
+  const HalfPlan a = half_plan_of(M, N, K, batches, sym, true), b = half_plan_of(M, N, K, batches, sym, false);
+  return a.us <= b.us ? a : b;
+}
+
+template <class P, bool SYM, int OCC>
+int launch_half(hipStream_t st, HalfArgs g, const HalfPlan& p) {
+  auto kfn = half_gemm<P, SYM, OCC>;
+  constexpr int kLds = 2 * P::kStage + (SYM ? P::WAVES * kStageBytes : 0);
+  static_assert(OCC * kLds <= 160 * 1024, "LDS");
+  static std::atomic<uint64_t> attr{0};
+  if (smem_attr_once(reinterpret_cast<const void*>(kfn), kLds, attr)) return -5;
+  g.tiles_m = (g.M + P::BM - 1) / P::BM;
+  g.tiles_n = (g.N + P::BN - 1) / P::BN;
+  g.full = int(p.full);
+  g.rest = int(p.rest);
+  g.splits = p.splits;
+  g.kt_per_split = p.kt_per_split;
+  const int64_t items = p.full + p.rest * p.splits, places = OCC * 256;
+  hipLaunchKernelGGL(kfn, dim3(unsigned(items < places ? items : places)), dim3(P::WAVES * 64), kLds, st, g);
+  if (hipGetLastError() != hipSuccess) return -5;
+  if (!p.rest) return 0;
+  hipLaunchKernelGGL((half_join<P, SYM>), dim3(unsigned(p.rest * P::WAVES * P::TM / 2)), dim3(64), 0, st, g);
+  return hipGetLastError() == hipSuccess ? 0 : -5;
 }
 
 template <bool B_KM, bool SYM>
-int run_half(hipStream_t st, HalfArgs g) {
-  g.lda = g.K;
-  g.ldb = B_KM ? g.K : g.N;
-  g.a_bytes = uint32_t(int64_t(g.M) * g.K * 2);
-  g.b_bytes = uint32_t(int64_t(g.N) * g.K * 2);
-  return big_tiles(g, SYM) ? launch_half<Big<B_KM>, SYM, 1>(st, g) : launch_half<Small<B_KM>, SYM, 2>(st, g);
+int run_half(hipStream_t st, const HalfArgs& g) {
+  const HalfPlan p = half_plan(g.M, g.N, g.K, g.batches, SYM);
+  return p.big ? launch_half<Big<B_KM>, SYM, 1>(st, g, p) : launch_half<Small<B_KM>, SYM, 2>(st, g, p);
 }
 
 }  // namespace sl2
 
-int half_gemm_nt(hipStream_t st, HalfArgs g, bool sym) {
-  return sym ? sl2::run_half<true, true>(st, g) : sl2::run_half<true, false>(st, g);
-}
+int half_gemm_sym(hipStream_t st, HalfArgs g) { return sl2::run_half<true, true>(st, g); }
 
 int half_gemm_nn(hipStream_t st, HalfArgs g) { return sl2::run_half<false, false>(st, g); }
+
+size_t half_gemm_workspace_bytes(int M, int N, int K, int64_t batches, bool sym) {
+  const sl2::HalfPlan p = sl2::half_plan(M, N, K, batches, sym);
+  return size_t(p.rest) * size_t(p.splits) * (p.big ? 256 * 256 * 4 : 128 * 128 * 4);
+}

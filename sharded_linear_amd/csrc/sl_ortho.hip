@@ -1,15 +1,17 @@
 // The orthogonalised update (gfx950): Newton-Schulz iterations on a gradient, and the optimiser step around them.
 //
-//   X = U / |U|_F, as [m, n] with m <= n;   each step:  A = X X^T,  X <- a X + (b A + c A^2) X
+//   X = U / |U|_F, as [m, n] with m <= n;   each step:  A = X X^T,  P = a I + b A + c A^2,  X <- P X
 //   step of a weight:  M <- mu M + G,  U = G + mu M (Nesterov) or M,  W <- (1 - lr wd) W - lr s X
 //
 // The polynomial a + b z^3 + c z^5 moves every singular value towards 1; all of the work is products of [m, m] and
 // [m, n] matrices.  They run in fp16: singular values stay below 3 (checked on the host for the coefficients given), so
-// every element of X, A and b A + c A^2 lies within fp16's range at one fixed scale, 2^12, where fp16 keeps 11 bits and
+// every element of X, A and P lies within fp16's range at one fixed scale, 2^12, where fp16 keeps 11 bits and
 // bf16 would keep 8.  Measured against 64 bits on [512, 2048] of normal values the result is 1.5e-3 off in fp16 and
 // 1.2e-2 in bf16 (relative, in the 2-norm).  A rounding of X in a direction whose singular value is small is multiplied
-// by up to a each step, so the first kLoSteps steps add what the rounding of X left (kept in fp16 beside it) to a X: with
-// singular values falling over four decades the error is 1.5e-3 with it and 9e-3 without.
+// by up to a each step, so the first kLoSteps steps add a times what the rounding of X left (kept in fp16 beside it) to
+// P X: with singular values falling over four decades the error is 1.5e-3 with it and 9e-3 without.  (P has a on its
+// diagonal rather than the epilogue adding a X: P's rounding scales X and so leaves small singular values their place,
+// P is nearer to 1 than P - a I in the last steps, and X is not read a second time.)
 //
 // Around the products: one pass for the momentum and the norm (sums of squares in 64 bits: any finite gradient has a
 // norm), one that scales, transposes a tall matrix and pads to multiples of 128 with zeros, and one that writes the
@@ -219,7 +221,7 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 struct OrthoPlan {
   int64_t mp, np;
   bool tall;
-  int64_t x_bytes, a_bytes, part_bytes, bytes;           // one [L, mp, np] and one [L, mp, mp] fp16 array
+  int64_t x_bytes, a_bytes, part_bytes, bytes;           // one [L, mp, np] and one [L, mp, mp] fp16 array; the norms' sums
 };
 
 int ortho_plan(int64_t L, int64_t rows, int64_t cols, OrthoPlan& p) {
@@ -236,16 +238,22 @@ int ortho_plan(int64_t L, int64_t rows, int64_t cols, OrthoPlan& p) {
   p.a_bytes = L * p.mp * p.mp * 2;
   p.part_bytes = L * kNormBlocks * 8;
   p.bytes = 3 * p.x_bytes + 2 * p.a_bytes + p.part_bytes;
+  if (p.mp == 0 || p.np == 0) return SL_OK;
+  size_t planes = 0;                                     // of the products' split sums
+  for (size_t b : {half_gemm_workspace_bytes(int(p.mp), int(p.mp), int(p.np), L, true), half_gemm_workspace_bytes(int(p.mp), int(p.mp), int(p.mp), L, true),
+                   half_gemm_workspace_bytes(int(p.mp), int(p.np), int(p.mp), L, false)})
+    planes = b > planes ? b : planes;
+  p.bytes += int64_t(planes);
   return SL_OK;
 }
 
-// The largest |a s + b s^3 + c s^5| over 0 <= s <= top, and the largest |b z + c z^2| over 0 <= z <= top^2.
+// The largest |a s + b s^3 + c s^5| over 0 <= s <= top, and the largest |a + b z + c z^2| over 0 <= z <= top^2.
 void step_bounds(const float* k, double top, double& x, double& inner) {
   const double a = k[0], b = k[1], c = k[2];
   auto p = [&](double s) { return std::fabs(s * (a + s * s * (b + c * s * s))); };
-  auto q = [&](double z) { return std::fabs(z * (b + c * z)); };
+  auto q = [&](double z) { return std::fabs(a + z * (b + c * z)); };
   x = p(top);
-  inner = q(top * top);
+  inner = std::fmax(q(0), q(top * top));
   if (c != 0) {
     const double z = -b / (2 * c), d = 9 * b * b - 20 * a * c;
     if (z > 0 && z < top * top) inner = std::fmax(inner, q(z));
@@ -259,7 +267,7 @@ void step_bounds(const float* k, double top, double& x, double& inner) {
   }
 }
 
-// Whether X, A and b A + c A^2 stay in range at kScale: |X| <= 3 (12288), |A| <= 9 (36864), the third <= 15 (61440).
+// Whether X, A and a I + b A + c A^2 stay in range at kScale: |X| <= 3 (12288), |A| <= 9 (36864), the third <= 15 (61440).
 int check_steps(int32_t steps, const float* coeffs) {
   if (steps < 0 || steps > kMaxSteps || (steps && !coeffs)) return SL_EINVAL;
   double top = 1;
@@ -281,8 +289,8 @@ int iterate(hipStream_t st, const Mats& mats, PassArgs a, const OrthoPlan& p, in
   x[1] = reinterpret_cast<_Float16*>(at); at += p.x_bytes;
   _Float16* lo = reinterpret_cast<_Float16*>(at); at += p.x_bytes;
   _Float16* A = reinterpret_cast<_Float16*>(at); at += p.a_bytes;
-  _Float16* B = reinterpret_cast<_Float16*>(at); at += p.a_bytes;
-  a.part = reinterpret_cast<double*>(at) + first * kNormBlocks;
+  _Float16* P = reinterpret_cast<_Float16*>(at); at += p.a_bytes;
+  a.part = reinterpret_cast<double*>(at) + first * kNormBlocks; at += p.part_bytes;
   a.x = x[0] + first * p.mp * p.np;
   a.lo = lo + first * p.mp * p.np;
   const int64_t groups = (a.rows * a.cols + 3) / 4;
@@ -296,22 +304,23 @@ int iterate(hipStream_t st, const Mats& mats, PassArgs a, const OrthoPlan& p, in
   if (first + left < L) return SL_OK;                    // the products take all matrices at once
   for (int k = 0; k < steps; ++k) {
     const float ca = coeffs[3 * k], cb = coeffs[3 * k + 1], cc = coeffs[3 * k + 2];
+    const int kept = steps < kLoSteps ? steps : kLoSteps;
     HalfArgs g{};
     g.batches = L;
+    g.ws = reinterpret_cast<float*>(at);
     g.a = g.b = x[k & 1]; g.c = A;
     g.M = g.N = int(p.mp); g.K = int(p.np);
     g.alpha = 1.f / kScale;
-    if (half_gemm_nt(st, g, true)) return SL_EHIP;
-    g.a = g.b = g.d = A; g.c = B;
+    if (half_gemm_sym(st, g)) return SL_EHIP;
+    g.a = g.b = g.d = A; g.c = P;
     g.K = int(p.mp);
-    g.alpha = cc / kScale; g.beta = cb;
-    if (half_gemm_nt(st, g, true)) return SL_EHIP;
-    const int kept = steps < kLoSteps ? steps : kLoSteps;
-    g.a = B; g.b = g.d = x[k & 1]; g.c = x[~k & 1];
+    g.alpha = cc / kScale; g.beta = cb; g.diag = ca * kScale;
+    if (half_gemm_sym(st, g)) return SL_EHIP;
+    g.a = P; g.b = x[k & 1]; g.c = x[~k & 1];
     g.N = int(p.np);
-    g.dlo = k < kept ? lo : nullptr;
+    g.d = k < kept ? lo : nullptr;
     g.clo = k + 1 < kept ? lo : nullptr;
-    g.alpha = 1.f / kScale; g.beta = ca;
+    g.alpha = 1.f / kScale; g.beta = ca * 0x1p-11f; g.diag = 0.f;
     if (half_gemm_nn(st, g)) return SL_EHIP;
   }
   return SL_OK;

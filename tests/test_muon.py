@@ -54,11 +54,11 @@ def test_orthogonalize_validation():
                                   ((8.28749, -23.5959, 17.3004), True), ((4.0, 0.0, 0.0), False), ((2.0, 1.5, 0.0), False), ((3.4445, -4.7750, 12.0), False),
                                   ((9.0, -20.0, 12.5), True), ((float("nan"), 0.0, 0.0), False), ((1.0, 30.0, -30.0), False)])
 def test_coefficients_that_leave_the_range_are_refused(k, ok):
-    """One step of each from singular values in [0, 1]: below 3, and the inner polynomial below 15."""
+    """One step of each from singular values in [0, 1]: below 3, and a + b z + c z^2 below 15."""
     f = _lib.lib().sl_orthogonalize
     s = torch.linspace(0, 1, 100001, dtype=torch.float64)
     if ok:
-        assert (k[0] * s + k[1] * s ** 3 + k[2] * s ** 5).abs().max() <= 3 and (k[1] * s ** 2 + k[2] * s ** 4).abs().max() <= 15
+        assert (k[0] * s + k[1] * s ** 3 + k[2] * s ** 5).abs().max() <= 3 and (k[0] + k[1] * s ** 2 + k[2] * s ** 4).abs().max() <= 15
     assert f(None, None, 4, None, 0, 8, 8, 1, _arr(*k), None, 0) == (OK if ok else EINVAL)
 
 
