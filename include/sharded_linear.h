@@ -353,10 +353,11 @@ int sl_linear_dgrad_mxfp4w(void* stream, const void* dY, const uint8_t* Wq, cons
  *   wgrad: main_grad[v] += scale * sum of dY[t] over the t with ids[t] - vocab_start = v, fp32, in place;
  *                          rows that no token names are not touched
  * ids[T] are int32 or int64 (ids_bytes 4 or 8, aligned to that).  H % 8 == 0; V up to 2^24; the gradient
- * takes up to 2^26 tokens, and T * H up to about 2^35 (SL_ESHAPE).  vocab_start >= 0 and scale finite
+ * takes up to 2^26 tokens, and T * H up to about 2^39 (SL_ESHAPE).  vocab_start >= 0 and scale finite
  * (SL_EINVAL).  The gradient's sums are fp32 in an order that depends on the ids alone: the same call gives
- * the same bits.  It takes a workspace of its query's bytes (16-byte aligned; initial contents do not
- * matter; calls that may run concurrently need distinct ones) and makes up to three launches.
+ * the same bits.  It takes a workspace of its query's bytes (0 for few tokens, workspace may then be NULL; 16-byte
+ * aligned; initial contents do not matter; calls that may run concurrently need distinct ones) and makes up to three
+ * launches.
  * --------------------------------------------------------------------------------------------- */
 int sl_embedding_fwd(void* stream, const void* ids, int32_t ids_bytes, const void* W, void* Y, int64_t T,
                      int64_t V, int64_t H, int64_t vocab_start, float scale);

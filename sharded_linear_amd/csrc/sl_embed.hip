@@ -16,8 +16,9 @@
 //  * Sums.  The sorted list is cut into chunks of kChunk places.  A workgroup adds up its chunk's rows
 //    in fp32 registers and writes each finished run of equal ids to main_grad; a run that crosses a
 //    chunk's border goes to one of the chunk's two planes of partial sums.
-//  * Join.  The workgroup of the chunk in which a crossing run begins adds its planes, 16 waves a
-//    contiguous part each, in order.
+//  * Join.  The chunks in which a crossing run begins are listed as the sums find them (the list's order is not fixed, and
+//    no result depends on it); a workgroup adds the planes of such a run, 16 waves a contiguous part each, in order.
+// Up to kFewTokens tokens one kernel does it all: a workgroup for each place whose id no earlier place has.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -76,29 +77,34 @@ __global__ void __launch_bounds__(256) embed_lookup(const I* __restrict__ ids, c
 constexpr int kSortWaves = 16;
 constexpr int kSortBins = 1000;           // most ids of one bucket: kSortWaves counters each in 64 KiB of LDS
 constexpr int kChunk = 16;                // sorted places to a workgroup of the sums
+constexpr int kFewTokens = 1024;          // tokens up to which one kernel does it all
 
 struct EmbedPlan {
   int bits;               // log2 of the number of buckets
   int64_t chunks;         // chunks of the longest sorted list
-  int64_t key_off, part_off, bytes;
+  int64_t cross_off, key_off, part_off, bytes;
 };
 
 // Buckets: 256, one workgroup a CU, or as many as leave kSortBins ids to each.
 EmbedPlan embed_plan(int64_t T, int64_t V, int64_t H) {
   EmbedPlan p{};
+  if (T <= kFewTokens) return p;
   p.bits = 8;
   while ((V + (int64_t(1) << p.bits) - 1) >> p.bits > kSortBins) ++p.bits;
   p.chunks = (T + kChunk - 1) / kChunk;
   const int64_t list = (T * 4 + 255) / 256 * 256;
-  p.key_off = 256 + list;                 // 256 bytes of header: the length of the sorted list
-  p.part_off = p.key_off + list;
+  p.key_off = 256 + list;                 // 256 bytes of header: the lengths of the sorted list and of the list of crossing runs
+  p.cross_off = p.key_off + list;
+  p.part_off = p.cross_off + (p.chunks * 4 + 255) / 256 * 256;
   p.bytes = p.part_off + p.chunks * 2 * H * 4;
   return p;
 }
 
+constexpr int kHeld = 16;                 // ids of a lane in flight, and held from the first walk to the second
+
 template <typename I>
 __global__ void __launch_bounds__(kSortWaves * 64) embed_sort(const I* __restrict__ ids, int64_t T, int64_t V, int64_t start,
-                                                              int bits, int* __restrict__ n_out, int* __restrict__ order,
+                                                              int bits, int* __restrict__ head, int* __restrict__ order,
                                                               int* __restrict__ key) {
   extern __shared__ int count[];          // [bins][kSortWaves]
   __shared__ int wave_before[kSortWaves], wave_sum[kSortWaves];
@@ -111,12 +117,28 @@ __global__ void __launch_bounds__(kSortWaves * 64) embed_sort(const I* __restric
   const int64_t per = ((T + kSortWaves * 64 - 1) / (kSortWaves * 64)) * 64;
   const int64_t t0 = wave * per, t1 = t0 + per < T ? t0 + per : T;
   int before = 0;                         // the rank's ids of smaller buckets in this lane's places
-  for (int64_t t = t0 + lane; t < t1; t += 64) {
-    const int64_t row = local_row(ids, t, start, V);
-    if (row < 0) continue;
-    const int64_t b = row & mask;
-    before += b < bucket;
-    if (b == bucket) atomicAdd(&count[int(row >> bits) * kSortWaves + wave], 1);
+  int held[kHeld];                        // this lane's rows of the last kHeld groups walked
+  auto load = [&](int64_t tb) {
+    I id[kHeld];
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u) {
+      const int64_t t = tb + 64 * u + lane;
+      id[u] = t < t1 ? ids[t] : I(-1);
+    }
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u) {
+      const int64_t x = int64_t(id[u]);
+      held[u] = x >= start && x - start < V ? int(x - start) : -1;
+    }
+  };
+  for (int64_t tb = t0; tb < t1; tb += 64 * kHeld) {
+    load(tb);
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u) {
+      const int b = held[u] & int(mask);
+      before += held[u] >= 0 && b < int(bucket);
+      if (held[u] >= 0 && b == int(bucket)) atomicAdd(&count[(held[u] >> bits) * kSortWaves + wave], 1);
+    }
   }
   for (int d = 1; d < 64; d <<= 1) before += __shfl_xor(before, d);
   if (lane == 0) wave_before[wave] = before;
@@ -142,7 +164,8 @@ __global__ void __launch_bounds__(kSortWaves * 64) embed_sort(const I* __restric
   if (threadIdx.x == 0 && bucket == mask) {
     int all = mine;
     for (int w = 0; w < kSortWaves; ++w) all += wave_before[w];
-    *n_out = all;
+    head[0] = all;
+    head[1] = 0;                          // runs that cross chunks, counted by the sums
   }
   int at = base + incl - sum;
   for (int i = i0; i < i1; ++i) {
@@ -153,27 +176,29 @@ __global__ void __launch_bounds__(kSortWaves * 64) embed_sort(const I* __restric
   __syncthreads();
   if (mine == 0) return;
   // places: lanes with the same id take consecutive ones; only this wave moves its counters
-  for (int64_t tb = t0; tb < t1; tb += 64) {
-    const int64_t t = tb + lane;
-    const int64_t row = t < t1 ? local_row(ids, t, start, V) : -1;
-    bool open = row >= 0 && (row & mask) == bucket;
-    const int bin = int(row >> bits);
-    uint64_t left = __ballot(open);
-    while (left) {
-      const int first = __builtin_ctzll(left);
-      const int b = __builtin_amdgcn_readlane(bin, first);
-      const bool same = open && bin == b;
-      const uint64_t peers = __ballot(same);
-      int* const counter = &count[b * kSortWaves + wave];
-      const int at0 = __hip_atomic_load(counter, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
-      if (same) {
-        const int place = at0 + __popcll(peers & ((uint64_t(1) << lane) - 1));
-        order[place] = int(t);
-        key[place] = int(row);
-        open = false;
+  for (int64_t tb = t0; tb < t1; tb += 64 * kHeld) {
+    if (per > 64 * kHeld) load(tb);
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u) {
+      bool open = held[u] >= 0 && (held[u] & int(mask)) == int(bucket);
+      const int bin = held[u] >> bits;
+      uint64_t left = __ballot(open);
+      while (left) {
+        const int first = __builtin_ctzll(left);
+        const int b = __builtin_amdgcn_readlane(bin, first);
+        const bool same = open && bin == b;
+        const uint64_t peers = __ballot(same);
+        int* const counter = &count[b * kSortWaves + wave];
+        const int at0 = __hip_atomic_load(counter, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+        if (same) {
+          const int place = at0 + __popcll(peers & ((uint64_t(1) << lane) - 1));
+          order[place] = int(tb + 64 * u + lane);
+          key[place] = held[u];
+          open = false;
+        }
+        if (lane == first) __hip_atomic_store(counter, at0 + __popcll(peers), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+        left &= ~peers;
       }
-      if (lane == first) __hip_atomic_store(counter, at0 + __popcll(peers), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
-      left &= ~peers;
     }
   }
 }
@@ -194,14 +219,17 @@ __device__ __forceinline__ void put_row(float* g, f32x8 v) {
 }
 
 // A workgroup takes one chunk of the sorted list and blockDim.x * 8 columns; a thread owns 8 columns.
-__global__ void __launch_bounds__(256) embed_sums(const uint4* __restrict__ dY, float* __restrict__ grad, const int* __restrict__ n_in,
-                                                  const int* __restrict__ order, const int* __restrict__ key,
+__global__ void __launch_bounds__(256) embed_sums(const uint4* __restrict__ dY, float* __restrict__ grad, int* __restrict__ head,
+                                                  int* __restrict__ cross, const int* __restrict__ order, const int* __restrict__ key,
                                                   float* __restrict__ part, int64_t H, int slices, float scale) {
   const int64_t chunk = blockIdx.x / slices;
-  const int n = *n_in;
+  const int n = head[0];
   const int64_t p0 = chunk * kChunk;
   if (p0 >= n) return;
   const int len = n - p0 < kChunk ? int(n - p0) : kChunk;
+  if (threadIdx.x == 0 && blockIdx.x % slices == 0 && p0 + len < n && key[p0 + len] == key[p0 + len - 1] &&
+      !(p0 > 0 && key[p0 - 1] == key[p0 + len]))
+    cross[atomicAdd(&head[1], 1)] = int(chunk);          // a run begins in this chunk and goes on
   const int64_t col = (int64_t(blockIdx.x % slices) * blockDim.x + threadIdx.x) * 8;
   if (col >= H) return;
   const int64_t row_chunks = H / 8;
@@ -228,60 +256,117 @@ __global__ void __launch_bounds__(256) embed_sums(const uint4* __restrict__ dY, 
 }
 
 constexpr int kJoinWaves = 16;
+constexpr int64_t kJoinBlocks = 512;
 
-// The runs that cross chunks: planes 2c + 1 (begins in chunk c) and 2k (goes on in chunk k > c).
-__global__ void __launch_bounds__(kJoinWaves * 64) embed_join(float* __restrict__ grad, const int* __restrict__ n_in,
+// The runs that cross chunks: planes 2c + 1 (begins in chunk c) and 2k (goes on in chunk k > c).  Workgroups walk the
+// list of (run, 512 columns).
+__global__ void __launch_bounds__(kJoinWaves * 64) embed_join(float* __restrict__ grad, const int* __restrict__ head, const int* __restrict__ cross,
                                                               const int* __restrict__ key, const float* __restrict__ part,
                                                               int64_t H, int slices, float scale) {
   __shared__ f32x8 sums[kJoinWaves][64];
   __shared__ int last;
-  const int64_t c = blockIdx.x / slices;
-  const int64_t n = *n_in, next = (c + 1) * kChunk;
-  if (next >= n) return;
-  const int k = key[next];
-  if (key[next - 1] != k) return;                       // nothing crosses the end of this chunk
-  if (c > 0 && key[c * kChunk] == k && key[c * kChunk - 1] == k) return;      // it began before this chunk
-  // chunks c + 1 .. last hold the rest: the first chunk that does not begin with k ends the search
-  const int64_t chunks = (n + kChunk - 1) / kChunk;
-  int64_t from = c + 2;
-  for (;; from += kJoinWaves * 64) {
-    if (threadIdx.x == 0) last = 0x7fffffff;
-    __syncthreads();
-    const int64_t x = from + threadIdx.x;
-    if (x >= chunks || key[x * kChunk] != k) atomicMin(&last, int(threadIdx.x));
-    __syncthreads();
-    const int found = last;
-    __syncthreads();
-    if (found != 0x7fffffff) {
-      from += found - 1;
-      break;
-    }
-  }
-  const int64_t more = from - c;                        // planes c + 1 .. from
+  const int64_t n = head[0], chunks = (n + kChunk - 1) / kChunk, items = int64_t(head[1]) * slices;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t col = (int64_t(blockIdx.x % slices) * 64 + lane) * 8;
-  const int64_t per = (more + kJoinWaves - 1) / kJoinWaves;
-  const int64_t a0 = c + 1 + wave * per, a1 = a0 + per < from + 1 ? a0 + per : from + 1;
-  f32x8 acc = {0, 0, 0, 0, 0, 0, 0, 0};
-  if (col < H) {
+  for (int64_t x = blockIdx.x; x < items; x += gridDim.x) {
+    const int64_t c = cross[x / slices];
+    const int k = key[(c + 1) * kChunk];
+    // chunks c + 1 .. last hold the rest: the first chunk that does not begin with k ends the search
+    int64_t from = c + 2;
+    for (;; from += kJoinWaves * 64) {
+      if (threadIdx.x == 0) last = 0x7fffffff;
+      __syncthreads();
+      const int64_t y = from + threadIdx.x;
+      if (y >= chunks || key[y * kChunk] != k) atomicMin(&last, int(threadIdx.x));
+      __syncthreads();
+      const int found = last;
+      __syncthreads();
+      if (found != 0x7fffffff) {
+        from += found - 1;
+        break;
+      }
+    }
+    const int64_t col = (x % slices * 64 + lane) * 8;
+    const int64_t per = (from - c + kJoinWaves - 1) / kJoinWaves;
+    const int64_t a0 = c + 1 + wave * per, a1 = a0 + per < from + 1 ? a0 + per : from + 1;
+    auto plane = [&](int64_t i) {
+      const float4* p = reinterpret_cast<const float4*>(part + i * H + col);
+      const float4 a = p[0], b = p[1];
+      return f32x8{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    };
+    f32x8 acc = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (col < H) {
 #pragma unroll 4
-    for (int64_t x = a0; x < a1; ++x) {
-      const float4* p = reinterpret_cast<const float4*>(part + 2 * x * H + col);
-      const float4 a = p[0], b = p[1];
-      acc += f32x8{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+      for (int64_t y = a0; y < a1; ++y) acc += plane(2 * y);
+      if (wave == 0) acc = plane(2 * c + 1) + acc;
     }
-    if (wave == 0) {
-      const float4* p = reinterpret_cast<const float4*>(part + (2 * c + 1) * H + col);
-      const float4 a = p[0], b = p[1];
-      acc = f32x8{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w} + acc;
+    sums[wave][lane] = acc;
+    __syncthreads();
+    if (wave == 0 && col < H) {
+      for (int w = 1; w < kJoinWaves; ++w) acc += sums[w][lane];
+      add_row(grad + int64_t(k) * H + col, acc * scale);
     }
+    __syncthreads();
   }
-  sums[wave][lane] = acc;
+}
+
+// ---- gradient of few tokens ----------------------------------------------------------------------
+// One launch.  The workgroup of place t leaves where an earlier place has its id; else it lists the places of that id in
+// order and adds up their rows, its groups of `width` threads (8 columns each) every G-th row, eight in flight.
+constexpr int kFewThreads = 512;
+
+template <typename I>
+__global__ void __launch_bounds__(kFewThreads) embed_few(const I* __restrict__ ids, const uint4* __restrict__ dY, float* __restrict__ grad, int T,
+                                                         int64_t V, int64_t H, int64_t start, int width, int slices, float scale) {
+  constexpr int kEach = kFewTokens / kFewThreads;
+  __shared__ int places[kFewTokens], counts[kEach][kFewThreads / 64];
+  __shared__ f32x8 sums[kFewThreads];
+  const int t = blockIdx.x / slices, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t row = local_row(ids, t, start, V);
+  if (row < 0) return;
+  const I mine = ids[t];
+  bool same[kEach], earlier = false;
+#pragma unroll
+  for (int u = 0; u < kEach; ++u) {
+    const int p = u * kFewThreads + threadIdx.x;
+    same[u] = p < T && ids[p] == mine;
+    earlier |= same[u] && p < t;
+  }
+  if (__syncthreads_or(earlier)) return;
+  uint64_t ballot[kEach];
+#pragma unroll
+  for (int u = 0; u < kEach; ++u) {
+    ballot[u] = __ballot(same[u]);
+    if (lane == 0) counts[u][wave] = __popcll(ballot[u]);
+  }
   __syncthreads();
-  if (wave == 0 && col < H) {
-    for (int w = 1; w < kJoinWaves; ++w) acc += sums[w][lane];
-    add_row(grad + int64_t(k) * H + col, acc * scale);
+  int n = 0;
+#pragma unroll
+  for (int u = 0; u < kEach; ++u)
+#pragma unroll
+    for (int w = 0; w < kFewThreads / 64; ++w) {
+      if (w == wave && same[u]) places[n + __popcll(ballot[u] & ((uint64_t(1) << lane) - 1))] = u * kFewThreads + threadIdx.x;
+      n += counts[u][w];
+    }
+  __syncthreads();
+  const int groups = kFewThreads / width, group = threadIdx.x / width, at = threadIdx.x % width;
+  const int64_t col = (int64_t(blockIdx.x % slices) * width + at) * 8;
+  f32x8 acc = {0, 0, 0, 0, 0, 0, 0, 0};
+  if (group < groups && col < H)
+    for (int i = group; i < n; i += 8 * groups) {
+      uint4 v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        v[u] = i + u * groups < n ? dY[int64_t(places[i + u * groups]) * (H / 8) + col / 8] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) acc += widen(v[u]);
+    }
+  if (n > 1) {
+    sums[threadIdx.x] = acc;
+    __syncthreads();
+    if (group == 0)
+      for (int g = 1; g < groups && g < n; ++g) acc += sums[g * width + at];
   }
+  if (group == 0 && col < H) add_row(grad + row * H + col, acc * scale);
 }
 
 constexpr int64_t kMaxExtent = int64_t(1) << 31;
@@ -342,31 +427,42 @@ extern "C" int sl_embedding_wgrad_accum(void* stream, const void* ids, int32_t i
   if (!dY || !main_grad) return SL_EINVAL;
   if (!aligned16(dY) || !aligned16(main_grad)) return SL_EALIGN;
   if (T > kMaxSorted) return SL_ESHAPE;
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  const int threads = H >= 2048 ? 256 : int((H / 8 + 63) / 64 * 64);
+  const int64_t slices = (H + threads * 8 - 1) / (threads * 8);
+  const uint4* dy = static_cast<const uint4*>(dY);
+  if (T <= kFewTokens) {
+    if (T * slices * kFewThreads >= kMaxThreads) return SL_ESHAPE;
+    const dim3 grid(unsigned(T * slices)), block(kFewThreads);
+    if (ids_bytes == 4)
+      hipLaunchKernelGGL(embed_few<int32_t>, grid, block, 0, st, static_cast<const int32_t*>(ids), dy, main_grad, int(T), V, H, vocab_start, threads, int(slices), scale);
+    else
+      hipLaunchKernelGGL(embed_few<int64_t>, grid, block, 0, st, static_cast<const int64_t*>(ids), dy, main_grad, int(T), V, H, vocab_start, threads, int(slices), scale);
+    return hipGetLastError() == hipSuccess ? SL_OK : SL_EHIP;
+  }
   const EmbedPlan p = embed_plan(T, V, H);
   if (!workspace || !aligned16(workspace) || workspace_bytes < size_t(p.bytes)) return SL_EWORKSPACE;
-  const int threads = H >= 2048 ? 256 : int((H / 8 + 63) / 64 * 64);
-  const int64_t slices = (H + threads * 8 - 1) / (threads * 8), join_slices = (H + 511) / 512;
-  // a launch has fewer than 2^32 threads
-  if (p.chunks * join_slices * (kJoinWaves * 64) >= kMaxThreads || p.chunks * slices * threads >= kMaxThreads) return SL_ESHAPE;
-  const hipStream_t st = static_cast<hipStream_t>(stream);
+  const int64_t join_slices = (H + 511) / 512;
+  if (p.chunks * slices * threads >= kMaxThreads) return SL_ESHAPE;
   char* ws = static_cast<char*>(workspace);
-  int* n = reinterpret_cast<int*>(ws);
+  int* head = reinterpret_cast<int*>(ws);
   int* order = reinterpret_cast<int*>(ws + 256);
   int* key = reinterpret_cast<int*>(ws + p.key_off);
+  int* cross = reinterpret_cast<int*>(ws + p.cross_off);
   float* part = reinterpret_cast<float*>(ws + p.part_off);
   const int bins = int((V + (int64_t(1) << p.bits) - 1) >> p.bits);
   const dim3 buckets(1u << p.bits), sort_threads(kSortWaves * 64);
-  const size_t lds = size_t(bins) * kSortWaves * 4;      // at most 64 KiB
+  const size_t lds = size_t(bins) * kSortWaves * 4;      // at most 64000 bytes
   if (ids_bytes == 4)
-    hipLaunchKernelGGL(embed_sort<int32_t>, buckets, sort_threads, lds, st, static_cast<const int32_t*>(ids), T, V, vocab_start, p.bits, n, order, key);
+    hipLaunchKernelGGL(embed_sort<int32_t>, buckets, sort_threads, lds, st, static_cast<const int32_t*>(ids), T, V, vocab_start, p.bits, head, order, key);
   else
-    hipLaunchKernelGGL(embed_sort<int64_t>, buckets, sort_threads, lds, st, static_cast<const int64_t*>(ids), T, V, vocab_start, p.bits, n, order, key);
+    hipLaunchKernelGGL(embed_sort<int64_t>, buckets, sort_threads, lds, st, static_cast<const int64_t*>(ids), T, V, vocab_start, p.bits, head, order, key);
   if (hipGetLastError() != hipSuccess) return SL_EHIP;
-  hipLaunchKernelGGL(embed_sums, dim3(unsigned(p.chunks * slices)), dim3(threads), 0, st, static_cast<const uint4*>(dY), main_grad, n, order,
-                     key, part, H, int(slices), scale);
+  hipLaunchKernelGGL(embed_sums, dim3(unsigned(p.chunks * slices)), dim3(threads), 0, st, dy, main_grad, head, cross, order, key, part, H,
+                     int(slices), scale);
   if (hipGetLastError() != hipSuccess) return SL_EHIP;
-  if (p.chunks > 1)
-    hipLaunchKernelGGL(embed_join, dim3(unsigned((p.chunks - 1) * join_slices)), dim3(kJoinWaves * 64), 0, st, main_grad, n, key, part, H,
-                       int(join_slices), scale);
+  const int64_t most = (p.chunks - 1) * join_slices;     // crossing runs, at most
+  hipLaunchKernelGGL(embed_join, dim3(unsigned(most < kJoinBlocks ? most : kJoinBlocks)), dim3(kJoinWaves * 64), 0, st, main_grad, head, cross, key,
+                     part, H, int(join_slices), scale);
   return hipGetLastError() == hipSuccess ? SL_OK : SL_EHIP;
 }

@@ -9,8 +9,8 @@
 // of the rounded h, which is what the next layer adds to and what the gradient reads again.
 //
 // Every kernel here is bound by HBM, so each row passes through registers once: TPR threads hold a
-// row, NC chunks of 8 elements a thread.  Means are fp32 sums: of a lane's elements in order, of the
-// lanes by DPP and half-wave swaps, of the waves in order.
+// row, NC chunks of 8 elements a thread.  Means are fp32 sums: of each of a lane's 8 columns in order, then of those, of the
+// lanes by DPP and half-wave swaps, and of the waves in order.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -46,6 +46,8 @@ __device__ __forceinline__ float wave_sum(float x) {
   return __builtin_bit_cast(float, uint32_t(r[0])) + __builtin_bit_cast(float, uint32_t(r[1]));
 }
 
+__device__ __forceinline__ float fold(f32x8 v) { return ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7])); }
+
 // Sum over the TPR threads of a row (a wave, or a whole workgroup).  `turn` alternates between calls, so that one
 // barrier a call is enough.
 template <int TPR>
@@ -61,6 +63,13 @@ __device__ __forceinline__ float row_sum(float x, float* red, int turn) {
     for (int w = 1; w < W; ++w) x += r[w];
   }
   return x;
+}
+
+// x^-1/2 to about half a unit in the last place: one correction with the residual 1 - x r^2 in exact products.
+__device__ __forceinline__ float inverse_root(float x) {
+  const float r = 1.0f / sqrtf(x), t = x * r, off = fmaf(-t, r, 1.0f) - fmaf(x, r, -t) * r;
+  const float c = fmaf(0.5f * r, off, r);
+  return c - c == 0.f ? c : r;                 // zeros, infinities and NaN as they come
 }
 
 // E8M0 byte of a block whose largest magnitude has the fp32 bits `amax`: floor(log2 amax) - 8, biased; 255 (NaN) for
@@ -96,7 +105,7 @@ struct FwdArgs {
   float* rstd;
   int64_t T;
   int chunks;          // H / 8
-  float inv_h, eps;
+  float h_float, eps;
 };
 
 template <int TPR, int NC, bool RES, int OUT>
@@ -125,21 +134,20 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_fwd(FwdArgs g) {
         if (lane + j * TPR < g.chunks) g.h[t * g.chunks + lane + j * TPR] = v[j];
       }
     }
-    float sum = 0.f;
+    f32x8 squares = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
       const f32x8 a = widen(v[j]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sum = fmaf(a[e], a[e], sum);
+      for (int e = 0; e < 8; ++e) squares[e] = fmaf(a[e], a[e], squares[e]);
     }
-    sum = row_sum<TPR>(sum, red, turn);
-    const float rstd = 1.0f / sqrtf(sum * g.inv_h + g.eps);
+    const float rstd = inverse_root(row_sum<TPR>(fold(squares), red, turn) / g.h_float + g.eps);
     if (lane == 0) g.rstd[t] = rstd;
     if constexpr (OUT != kNothing) {
 #pragma unroll
       for (int j = 0; j < NC; ++j) {
         const int c = lane + j * TPR;
-        const f32x8 y = widen(v[j]) * rstd * widen(w[j]);
+        const f32x8 y = widen(v[j]) * widen(w[j]) * rstd;        // the first product is exact
         if constexpr (OUT == kBF16) {
           if (c < g.chunks) g.y[t * g.chunks + c] = narrow(y);
         } else {
@@ -203,7 +211,7 @@ __global__ void __launch_bounds__(256) norm_cols(const uint16_t* __restrict__ h,
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float x = __uint_as_float(uint32_t(uint16_t(v[e])) << 16);
-        y[4 * r4 + e] = x * inv[rb * 32 + 4 * r4 + e] * wc;
+        y[4 * r4 + e] = x * wc * inv[rb * 32 + 4 * r4 + e];
         amax = max(amax, magnitude(y[4 * r4 + e]));
       }
     }
@@ -244,7 +252,7 @@ struct BwdArgs {
   float* part;         // [gridDim.x][H], or null: the weight is frozen
   int64_t T;
   int chunks;
-  float inv_h;
+  float h_float;
 };
 
 // A workgroup walks rows with the weight gradient of its threads' columns in registers and leaves one plane of
@@ -274,14 +282,14 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_bwd(BwdArgs g) {
       h[j] = in ? g.h[o + j * TPR] : make_uint4(0, 0, 0, 0);
       if constexpr (RES) dr[j] = in ? g.dres[o + j * TPR] : make_uint4(0, 0, 0, 0);
     }
-    float dot = 0.f;
+    f32x8 dots = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
       const f32x8 a = widen(dy[j]) * widen(w[j]), b = widen(h[j]) * rstd;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) dot = fmaf(a[e], b[e], dot);
+      for (int e = 0; e < 8; ++e) dots[e] = fmaf(a[e], b[e], dots[e]);
     }
-    const float mean = row_sum<TPR>(dot, red, turn) * g.inv_h;
+    const float mean = row_sum<TPR>(fold(dots), red, turn) / g.h_float;
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
       const f32x8 d = widen(dy[j]), n = widen(h[j]) * rstd;
@@ -409,7 +417,7 @@ extern "C" int sl_rmsnorm_fwd(void* stream, const void* x, const void* residual,
   if (!aligned16(x) || !aligned16(residual) || !aligned16(w) || !aligned16(y) || (residual && !aligned16(h)) || reinterpret_cast<uintptr_t>(rstd) & 3u)
     return SL_EALIGN;
   FwdArgs g{static_cast<const uint4*>(x), static_cast<const uint4*>(residual), static_cast<const uint4*>(w), static_cast<uint4*>(y),
-            static_cast<uint4*>(h), nullptr, nullptr, rstd, T, int(H / 8), 1.0f / float(H), eps};
+            static_cast<uint4*>(h), nullptr, nullptr, rstd, T, int(H / 8), float(H), eps};
   return run_fwd(static_cast<hipStream_t>(stream), g, kBF16);
 }
 
@@ -428,7 +436,7 @@ extern "C" int sl_rmsnorm_fwd_mxfp8(void* stream, const void* x, const void* res
   if (q_cols && tiles >= (int64_t(1) << 24)) return SL_ESHAPE;            // of 256 threads: a launch has fewer than 2^32
   const hipStream_t st = static_cast<hipStream_t>(stream);
   FwdArgs g{static_cast<const uint4*>(x), static_cast<const uint4*>(residual), static_cast<const uint4*>(w), nullptr, static_cast<uint4*>(h),
-            reinterpret_cast<uint2*>(q_rows), s_rows, rstd, T, int(H / 8), 1.0f / float(H), eps};
+            reinterpret_cast<uint2*>(q_rows), s_rows, rstd, T, int(H / 8), float(H), eps};
   const int f = run_fwd(st, g, q_rows ? kRows : kNothing);
   if (f || !q_cols) return f;
   hipLaunchKernelGGL(norm_cols, dim3(unsigned(tiles)), dim3(256), 0, st, static_cast<const uint16_t*>(residual ? h : x),
@@ -454,7 +462,7 @@ extern "C" int sl_rmsnorm_bwd(void* stream, const void* dY, const void* h, const
   const BwdPlan p = bwd_plan(T, int(H / 8));
   const hipStream_t st = static_cast<hipStream_t>(stream);
   BwdArgs g{static_cast<const uint4*>(dY), static_cast<const uint4*>(h), static_cast<const uint4*>(w), static_cast<const uint4*>(dresidual), rstd,
-            static_cast<uint4*>(dX), w_grad ? static_cast<float*>(workspace) : nullptr, T, int(H / 8), 1.0f / float(H)};
+            static_cast<uint4*>(dX), w_grad ? static_cast<float*>(workspace) : nullptr, T, int(H / 8), float(H)};
   const dim3 grid(unsigned(p.planes)), threads(p.tpr < 256 ? 256 : p.tpr);
   with_row(p.tpr, g.chunks, [&](auto t, auto n) {
     constexpr int TPR = decltype(t)::value, NC = decltype(n)::value;

@@ -34,12 +34,12 @@ def test_lookup_validation():
 def test_gradient_validation():
     L = _lib.lib()
     f, ws = L.sl_embedding_wgrad_accum, L.sl_embedding_wgrad_workspace_bytes
-    need = ws(100, 50, 64)
-    assert need > 0 and ws(0, 50, 64) == 0 and ws(100, 0, 64) == 0 and ws(100, 50, 12) == 0 and ws(-1, 50, 64) == 0
-    ok = (100, 50, 64, 0, 1.0)
-    assert f(None, A, 4, A, A, 100, 50, 60, 0, 1.0, A, need) == ESHAPE
+    need = ws(2000, 50, 64)
+    assert need > 0 and ws(0, 50, 64) == 0 and ws(2000, 0, 64) == 0 and ws(2000, 50, 12) == 0 and ws(-1, 50, 64) == 0 and ws(1000, 50, 64) == 0
+    ok = (2000, 50, 64, 0, 1.0)
+    assert f(None, A, 4, A, A, 2000, 50, 60, 0, 1.0, A, need) == ESHAPE
     assert f(None, A, 4, A, A, (1 << 26) + 1, 50, 64, 0, 1.0, A, 1 << 60) == ESHAPE
-    assert f(None, A, 4, A, A, 1 << 26, 50, 1024, 0, 1.0, A, 1 << 60) == ESHAPE     # more threads than a launch has
+    assert f(None, A, 4, A, A, 1 << 26, 50, 8192, 0, 1.0, A, 1 << 60) == ESHAPE     # more threads than a launch has
     assert f(None, A, 3, A, A, *ok, A, need) == EINVAL
     assert f(None, A, 4, None, A, *ok, A, need) == EINVAL
     assert f(None, A, 4, A, None, *ok, A, need) == EINVAL
@@ -50,7 +50,7 @@ def test_gradient_validation():
     assert f(None, A, 4, A, A, *ok, A, need - 1) == EWORKSPACE
     assert f(None, A, 4, A, A, *ok, A + 4, need) == EWORKSPACE
     assert f(None, None, 4, None, None, 0, 50, 64, 0, 1.0, None, 0) == OK
-    assert f(None, A, 4, None, None, 100, 0, 64, 0, 1.0, None, 0) == OK             # no rows in this shard
+    assert f(None, A, 4, None, None, 2000, 0, 64, 0, 1.0, None, 0) == OK             # no rows in this shard
 
 
 def test_binding_refusals(monkeypatch):
