@@ -17,7 +17,7 @@
 //    in fp32 registers and writes each finished run of equal ids to main_grad; a run that crosses a
 //    chunk's border goes to one of the chunk's two planes of partial sums.
 //  * Join.  The chunks in which a crossing run begins are listed as the sums find them (the list's order is not fixed, and
-//    no result depends on it); a workgroup adds the planes of such a run, 16 waves a contiguous part each, in order.
+//    no result depends on it); a workgroup adds the planes of such a run, 8 waves a contiguous part each, in order.
 // Up to kFewTokens tokens one kernel does it all: a workgroup for each place whose id no earlier place has.
 #include <hip/hip_runtime.h>
 
@@ -54,18 +54,16 @@ __global__ void __launch_bounds__(256) embed_lookup(const I* __restrict__ ids, c
                                                     int64_t T, int64_t V, int chunks, int64_t start, float scale) {
   for (int64_t t = int64_t(blockIdx.x) * (256 / LPR) + threadIdx.x / LPR; t < T; t += int64_t(gridDim.x) * (256 / LPR)) {
     const int64_t row = local_row(ids, t, start, V);
-    const uint4* src = W + row * chunks;
+    const uint4* src = W + (row < 0 ? 0 : row) * chunks;       // loads stand behind no condition: each would be waited for
     uint4* dst = Y + t * chunks;
     for (int c0 = threadIdx.x % LPR; c0 < chunks; c0 += 4 * LPR) {
       uint4 v[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int c = c0 + u * LPR;
-        v[u] = row >= 0 && c < chunks ? src[c] : make_uint4(0, 0, 0, 0);
-      }
+      for (int u = 0; u < 4; ++u) v[u] = src[min(c0 + u * LPR, chunks - 1)];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int c = c0 + u * LPR;
+        if (row < 0) v[u] = make_uint4(0, 0, 0, 0);
         if (c < chunks) dst[c] = scale == 1.0f || row < 0 ? v[u] : narrow(widen(v[u]) * scale);
       }
     }
@@ -75,8 +73,8 @@ __global__ void __launch_bounds__(256) embed_lookup(const I* __restrict__ ids, c
 // ---- gradient: sort ------------------------------------------------------------------------------
 
 constexpr int kSortWaves = 16;
-constexpr int kSortBins = 1000;           // most ids of one bucket: kSortWaves counters each in 64 KiB of LDS
-constexpr int kChunk = 16;                // sorted places to a workgroup of the sums
+constexpr int kSortBins = 1000;           // most ids of one bucket, kSortWaves counters each in LDS
+constexpr int kChunk = 8;                // sorted places to a workgroup of the sums
 constexpr int kFewTokens = 1024;          // tokens up to which one kernel does it all
 
 struct EmbedPlan {
@@ -100,7 +98,7 @@ EmbedPlan embed_plan(int64_t T, int64_t V, int64_t H) {
   return p;
 }
 
-constexpr int kHeld = 16;                 // ids of a lane in flight, and held from the first walk to the second
+constexpr int kHeld = 8;                  // ids of a lane in flight, and held from the first walk to the second
 
 template <typename I>
 __global__ void __launch_bounds__(kSortWaves * 64) embed_sort(const I* __restrict__ ids, int64_t T, int64_t V, int64_t start,
@@ -116,19 +114,34 @@ __global__ void __launch_bounds__(kSortWaves * 64) embed_sort(const I* __restric
   // wave w walks places [t0, t1), 64 at a time
   const int64_t per = ((T + kSortWaves * 64 - 1) / (kSortWaves * 64)) * 64;
   const int64_t t0 = wave * per, t1 = t0 + per < T ? t0 + per : T;
+  const uint32_t rows32 = start < (int64_t(1) << 31) ? uint32_t(V) : 0;      // rows that an id of 32 bits reaches
   int before = 0;                         // the rank's ids of smaller buckets in this lane's places
   int held[kHeld];                        // this lane's rows of the last kHeld groups walked
   auto load = [&](int64_t tb) {
     I id[kHeld];
+    const I* from = ids + tb + lane;
+    if (t1 - tb >= 64 * kHeld) {
 #pragma unroll
-    for (int u = 0; u < kHeld; ++u) {
-      const int64_t t = tb + 64 * u + lane;
-      id[u] = t < t1 ? ids[t] : I(-1);
+      for (int u = 0; u < kHeld; ++u) id[u] = from[64 * u];
+    } else {                              // behind a condition of its own each load would be waited for by itself
+      const int last = int(t1 - tb) - 1;
+#pragma unroll
+      for (int u = 0; u < kHeld; ++u) {
+        const int i = 64 * u + lane;
+        id[u] = ids[tb + min(i, last)];
+        if (i > last) id[u] = -1;
+      }
     }
+    // V is at most 2^24: below it, the difference has no wrap that a nonnegative id could bring about
 #pragma unroll
     for (int u = 0; u < kHeld; ++u) {
-      const int64_t x = int64_t(id[u]);
-      held[u] = x >= start && x - start < V ? int(x - start) : -1;
+      if constexpr (sizeof(I) == 4) {
+        const uint32_t r = uint32_t(id[u]) - uint32_t(start);
+        held[u] = id[u] >= 0 && r < rows32 ? int(r) : -1;
+      } else {
+        const uint64_t r = uint64_t(id[u]) - uint64_t(start);
+        held[u] = id[u] >= 0 && r < uint64_t(V) ? int(r) : -1;
+      }
     }
   };
   for (int64_t tb = t0; tb < t1; tb += 64 * kHeld) {
@@ -235,28 +248,44 @@ __global__ void __launch_bounds__(256) embed_sums(const uint4* __restrict__ dY, 
   const int64_t row_chunks = H / 8;
   uint4 v[kChunk];
 #pragma unroll
-  for (int i = 0; i < kChunk; ++i)
-    if (i < len) v[i] = dY[int64_t(order[p0 + i]) * row_chunks + col / 8];
+  for (int i = 0; i < kChunk; ++i) v[i] = dY[int64_t(order[p0 + min(i, len - 1)]) * row_chunks + col / 8];
   bool open = p0 > 0 && key[p0 - 1] == key[p0];       // the current run began in an earlier chunk
-  f32x8 acc = {0, 0, 0, 0, 0, 0, 0, 0};
+  // the rows that this chunk finishes are read ahead, so that no store waits for a load
+  float4 old[kChunk][2];
+  bool ends[kChunk], whole[kChunk];
+  int k[kChunk];
 #pragma unroll
   for (int i = 0; i < kChunk; ++i) {
-    if (i < len) {
-      acc += widen(v[i]);
-      const int k = key[p0 + i];
-      const bool ends = p0 + i + 1 >= n || key[p0 + i + 1] != k;
-      if (ends && !open) add_row(grad + int64_t(k) * H + col, acc * scale);
-      else if (ends || i + 1 == len) put_row(part + (chunk * 2 + (open ? 0 : 1)) * H + col, acc);
-      if (ends) {
-        acc = f32x8{0, 0, 0, 0, 0, 0, 0, 0};
-        open = false;
-      }
+    k[i] = key[p0 + min(i, len - 1)];
+    ends[i] = i < len && (p0 + i + 1 >= n || key[p0 + i + 1] != k[i]);
+    whole[i] = ends[i] && !open;
+    if (ends[i]) open = false;
+    const float4* p = reinterpret_cast<const float4*>(grad + int64_t(k[i]) * H + col);
+    old[i][0] = p[0];
+    old[i][1] = p[1];
+  }
+  f32x8 acc = {0, 0, 0, 0, 0, 0, 0, 0};
+  bool first = p0 > 0 && key[p0 - 1] == key[p0];
+#pragma unroll
+  for (int i = 0; i < kChunk; ++i) {
+    if (i >= len) break;
+    acc += widen(v[i]);
+    if (whole[i]) {
+      acc *= scale;
+      const float4 a = old[i][0], b = old[i][1];
+      put_row(grad + int64_t(k[i]) * H + col, f32x8{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w} + acc);
+    } else if (ends[i] || i + 1 == len) {
+      put_row(part + (chunk * 2 + (first ? 0 : 1)) * H + col, acc);
+    }
+    if (ends[i]) {
+      acc = f32x8{0, 0, 0, 0, 0, 0, 0, 0};
+      first = false;
     }
   }
 }
 
-constexpr int kJoinWaves = 16;
-constexpr int64_t kJoinBlocks = 512;
+constexpr int kJoinWaves = 8;
+constexpr int64_t kJoinBlocks = 1024;
 
 // The runs that cross chunks: planes 2c + 1 (begins in chunk c) and 2k (goes on in chunk k > c).  Workgroups walk the
 // list of (run, 512 columns).
@@ -355,10 +384,10 @@ __global__ void __launch_bounds__(kFewThreads) embed_few(const I* __restrict__ i
     for (int i = group; i < n; i += 8 * groups) {
       uint4 v[8];
 #pragma unroll
-      for (int u = 0; u < 8; ++u)
-        v[u] = i + u * groups < n ? dY[int64_t(places[i + u * groups]) * (H / 8) + col / 8] : make_uint4(0, 0, 0, 0);
+      for (int u = 0; u < 8; ++u) v[u] = dY[int64_t(places[min(i + u * groups, n - 1)]) * (H / 8) + col / 8];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) acc += widen(v[u]);
+      for (int u = 0; u < 8; ++u)
+        if (i + u * groups < n) acc += widen(v[u]);
     }
   if (n > 1) {
     sums[threadIdx.x] = acc;
@@ -389,7 +418,7 @@ void launch_lookup(hipStream_t st, const void* ids, int32_t ids_bytes, const voi
   int64_t blocks = (T + 256 / LPR - 1) / (256 / LPR);
   if (blocks > (1 << 20)) blocks = 1 << 20;
   const dim3 grid{unsigned(blocks)};
-  const uint4* w = static_cast<const uint4*>(W);
+  const uint4* w = static_cast<const uint4*>(V > 0 ? W : Y);      // read, and not used, for a shard without rows
   uint4* y = static_cast<uint4*>(Y);
   if (ids_bytes == 4)
     hipLaunchKernelGGL((embed_lookup<LPR, int32_t>), grid, dim3(256), 0, st, static_cast<const int32_t*>(ids), w, y, T, V, chunks, start, scale);
@@ -452,7 +481,7 @@ extern "C" int sl_embedding_wgrad_accum(void* stream, const void* ids, int32_t i
   float* part = reinterpret_cast<float*>(ws + p.part_off);
   const int bins = int((V + (int64_t(1) << p.bits) - 1) >> p.bits);
   const dim3 buckets(1u << p.bits), sort_threads(kSortWaves * 64);
-  const size_t lds = size_t(bins) * kSortWaves * 4;      // at most 64000 bytes
+  const size_t lds = size_t(bins) * kSortWaves * 4;
   if (ids_bytes == 4)
     hipLaunchKernelGGL(embed_sort<int32_t>, buckets, sort_threads, lds, st, static_cast<const int32_t*>(ids), T, V, vocab_start, p.bits, head, order, key);
   else

@@ -133,8 +133,9 @@ def _exact_case(ids, V, H, start, seed, scale=1.0):
     g = _gen(seed)
     dY = torch.randint(-8, 9, (ids.numel(), H), generator=g, device="cuda").to(BF16)
     grad = torch.randint(-8, 9, (V, H), generator=g, device="cuda").float()
-    at = ids.long().view(-1) - start
-    mine = (at >= 0) & (at < V)
+    at = ids.long().view(-1)
+    mine = (at >= start) & (at - max(start - 1, 0) <= V) if start else (at >= 0) & (at < V)
+    at = at - start
     ref = grad.double().index_add_(0, at[mine], dY.double()[mine] * scale)
     got = sl.sl_embedding_wgrad_accum(ids, dY.view(*ids.shape, H), grad, vocab_start=start, scale=scale)
     assert got is grad
@@ -166,6 +167,19 @@ def test_gradient_of_large_tables(V):
     ids = _ids(_gen(3), 700, 0, V, torch.int64)
     ids[:3] = torch.tensor([0, V - 1, V - 1], device="cuda")
     _exact_case(ids, V, 8, 0, V)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [40, 3000])
+def test_gradient_of_far_ids(T):
+    """Ids and shards at the ends of 32 and 64 bits: differences that wrap name no row."""
+    say(f"case embedding gradient of far ids T={T}")
+    for dtype, start, ends in ((torch.int32, 2 ** 31 - 20, (-2 ** 31, -1, 0, 2 ** 31 - 21, 2 ** 31 - 1)),
+                               (torch.int32, 2 ** 31 + 5, (-2 ** 31, 2 ** 31 - 1)), (torch.int32, 2 ** 32 + 3, (0, 3, 4)),
+                               (torch.int64, 2 ** 62, (-2 ** 63, -2 ** 62, 2 ** 62 - 1, 2 ** 62 + 50, 2 ** 63 - 1)),
+                               (torch.int64, 2 ** 63 - 20, (-2 ** 63, -1, 2 ** 63 - 1))):
+        ids = torch.tensor([ends[k % len(ends)] for k in range(T)], dtype=dtype, device="cuda")
+        _exact_case(ids, 30, 16, start, T)
 
 
 @pytest.mark.gpu
