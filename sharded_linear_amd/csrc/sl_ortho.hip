@@ -24,6 +24,7 @@
 #include "sharded_linear.h"
 #include "sl_device.h"
 #include "sl_gemm_h.h"
+#include "sl_narrow_h.h"
 
 namespace {
 
@@ -220,9 +221,12 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 struct OrthoPlan {
   int64_t mp, np;
-  bool tall;
+  bool tall, narrow;
   int64_t x_bytes, a_bytes, part_bytes, bytes;           // one [L, mp, np] and one [L, mp, mp] fp16 array; the norms' sums
 };
+
+// Whether the steps go to the kernels of sl_narrow_h.hip.
+bool few_rows(int64_t mp, int64_t np, int64_t L) { return mp <= kNarrowRows; }
 
 int ortho_plan(int64_t L, int64_t rows, int64_t cols, OrthoPlan& p) {
   if (L < 0 || rows < 0 || cols < 0) return SL_EINVAL;
@@ -238,22 +242,28 @@ int ortho_plan(int64_t L, int64_t rows, int64_t cols, OrthoPlan& p) {
   p.a_bytes = L * p.mp * p.mp * 2;
   p.part_bytes = L * kNormBlocks * 8;
   p.bytes = 3 * p.x_bytes + 2 * p.a_bytes + p.part_bytes;
-  if (p.mp == 0 || p.np == 0) return SL_OK;
-  size_t planes = 0;                                     // of the products' split sums
-  for (size_t b : {half_gemm_workspace_bytes(int(p.mp), int(p.mp), int(p.np), L, true), half_gemm_workspace_bytes(int(p.mp), int(p.mp), int(p.mp), L, true),
+  if (L == 0 || p.mp == 0 || p.np == 0) return SL_OK;
+  p.narrow = few_rows(p.mp, p.np, L);
+  size_t planes = 0;                                     // of the products' split sums, or of the Gram matrices' shares
+  if (p.narrow) planes = size_t(L) * size_t(narrow_groups(int(p.mp), int(p.np), L)) * size_t(p.mp * p.mp) * 4;
+  else for (size_t b : {half_gemm_workspace_bytes(int(p.mp), int(p.mp), int(p.np), L, true), half_gemm_workspace_bytes(int(p.mp), int(p.mp), int(p.mp), L, true),
                    half_gemm_workspace_bytes(int(p.mp), int(p.np), int(p.mp), L, false)})
     planes = b > planes ? b : planes;
   p.bytes += int64_t(planes);
   return SL_OK;
 }
 
-// The largest |a s + b s^3 + c s^5| over 0 <= s <= top, and the largest |a + b z + c z^2| over 0 <= z <= top^2.
-void step_bounds(const float* k, double top, double& x, double& inner) {
+// The largest |a s + b s^3 + c s^5| and |b s + c s^3| over 0 <= s <= top, and the largest |a + b z + c z^2| over
+// 0 <= z <= top^2.
+void step_bounds(const float* k, double top, double& x, double& inner, double& rest) {
   const double a = k[0], b = k[1], c = k[2];
   auto p = [&](double s) { return std::fabs(s * (a + s * s * (b + c * s * s))); };
   auto q = [&](double z) { return std::fabs(a + z * (b + c * z)); };
   x = p(top);
   inner = std::fmax(q(0), q(top * top));
+  auto r = [&](double s) { return std::fabs(s * (b + c * s * s)); };
+  rest = r(top);
+  if (c != 0 && -b / (3 * c) > 0 && -b / (3 * c) < top * top) rest = std::fmax(rest, r(std::sqrt(-b / (3 * c))));
   if (c != 0) {
     const double z = -b / (2 * c), d = 9 * b * b - 20 * a * c;
     if (z > 0 && z < top * top) inner = std::fmax(inner, q(z));
@@ -267,14 +277,15 @@ void step_bounds(const float* k, double top, double& x, double& inner) {
   }
 }
 
-// Whether X, A and a I + b A + c A^2 stay in range at kScale: |X| <= 3 (12288), |A| <= 9 (36864), the third <= 15 (61440).
+// Whether X, A and a I + b A + c A^2 stay in range at kScale: |X| <= 3 (12288), |A| <= 9 (36864), the third <= 15 (61440);
+// and b X + c A X at a quarter of it: <= 60.
 int check_steps(int32_t steps, const float* coeffs) {
   if (steps < 0 || steps > kMaxSteps || (steps && !coeffs)) return SL_EINVAL;
   double top = 1;
   for (int i = 0; i < steps; ++i) {
-    double x, inner;
-    step_bounds(coeffs + 3 * i, top, x, inner);
-    if (!(x <= 3) || !(inner <= 15)) return SL_EINVAL;
+    double x, inner, rest;
+    step_bounds(coeffs + 3 * i, top, x, inner, rest);
+    if (!(x <= 3) || !(inner <= 15) || !(rest <= 60)) return SL_EINVAL;
     top = x * 1.01;                                      // roundings
   }
   return SL_OK;
@@ -302,6 +313,27 @@ int iterate(hipStream_t st, const Mats& mats, PassArgs a, const OrthoPlan& p, in
   if (hipGetLastError() != hipSuccess) return SL_EHIP;
   *result = x[steps & 1];
   if (first + left < L) return SL_OK;                    // the products take all matrices at once
+  if (p.narrow) {
+    NarrowArgs g{};
+    g.A = A; g.lo = lo;
+    g.M = int(p.mp); g.N = int(p.np); g.batches = L;
+    g.groups = narrow_groups(g.M, g.N, L);
+    g.scale = kScale;
+    float* const planes = reinterpret_cast<float*>(at);
+    for (int k = 0; k < steps; ++k) {
+      const int kept = steps < kLoSteps ? steps : kLoSteps;
+      g.x = x[k & 1]; g.y = x[~k & 1];
+      g.planes = planes;
+      if (k == 0 && narrow_gram(st, g)) return SL_EHIP;
+      if (narrow_join(st, planes, A, g.M, g.groups, L, kScale)) return SL_EHIP;
+      g.planes = k + 1 < steps ? planes : nullptr;
+      g.lo = k < kept ? lo : nullptr;
+      g.ylo = k + 1 < kept ? lo : nullptr;
+      g.a = coeffs[3 * k]; g.b = coeffs[3 * k + 1]; g.c = coeffs[3 * k + 2];
+      if (narrow_step(st, g)) return SL_EHIP;
+    }
+    return SL_OK;
+  }
   for (int k = 0; k < steps; ++k) {
     const float ca = coeffs[3 * k], cb = coeffs[3 * k + 1], cc = coeffs[3 * k + 2];
     const int kept = steps < kLoSteps ? steps : kLoSteps;
