@@ -13,13 +13,14 @@ struct NarrowArgs {
   void* y;                     // the step's result, like x
   const void* lo;              // what the rounding of x left, times scale 2^11, or null
   void* ylo;                   // the same of y, or null; may be lo
-  float* planes;               // [batches][groups][M][M] partial Gram matrices of the result, or null
+  float* planes;               // [batches][groups] partial Gram matrices of the result, or null
   int M, N, groups;
   int64_t batches;
   float a, b, c, scale;
 };
 
-// Workgroups (and so planes) of one matrix.
+// Workgroups (and so planes) of one matrix, and the bytes of one plane.
+size_t narrow_plane_bytes(int M);
 int narrow_groups(int M, int N, int64_t batches);
 // planes = the Gram matrices of x in parts.
 int narrow_gram(hipStream_t st, const NarrowArgs& g);

@@ -6,7 +6,10 @@
 // so that a workgroup computes 32 columns of y from the same columns of x and the whole of A, with nothing to wait for in
 // between; the columns of y are then in LDS, and their share of the next Gram matrix, y y^T, is one more product there,
 // kept in accumulators over all columns that the workgroup takes.  The second launch adds the workgroups' shares in order.
-// A's rows stay in registers for both products with it: wave w holds rows w M / 8 ..
+// A's rows stay in registers for both products with it: of 256 rows wave w holds the blocks of 16 rows w and 15 - w, which
+// together have 17 blocks on and below the diagonal whatever w, and only those of the Gram matrix are computed and kept
+// (all 32 of a wave took 128 registers and twice the stores: a step of [256, 512] 13.2 us against 10.8).  Of 128 rows wave w
+// holds block w, and all of the Gram matrix is computed.
 //
 // Each of b x + c A x, y and A is rounded to fp16 once, the first at a quarter of the others' scale (its elements may be larger).
 #include <hip/hip_runtime.h>
@@ -24,7 +27,12 @@ constexpr int kCols = 32, kRow = kCols + 8;    // a slice's columns, and its row
 
 template <int M>
 struct Narrow {
-  static constexpr int RW = M / 8, TI = RW / 16, KS = M / 32, TJ = M / 16;
+  static constexpr int TI = M / 128, KS = M / 32, TJ = M / 16;
+  static constexpr int kBlocks = TI == 1 ? TJ : TJ + 1;        // blocks of the Gram matrix that a wave keeps
+  // Block t of wave w: row block and column block.
+  __device__ __host__ static constexpr int row(int w, int i) { return i == 0 ? w : TJ - 1 - w; }
+  __device__ __host__ static constexpr int half(int w, int t) { return TI == 1 || t <= w ? 0 : 1; }
+  __device__ __host__ static constexpr int col(int w, int t) { return TI == 1 || t <= w ? t : t - w - 1; }
   static constexpr int kChunks = M * kCols / 8 / 512;          // 16-byte chunks of a slice for each thread
 };
 
@@ -49,7 +57,10 @@ __global__ void __launch_bounds__(512) narrow_kernel(NarrowArgs g) {
   __shared__ __attribute__((aligned(16))) _Float16 zs[STEP ? M * kRow : 8];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int batch = blockIdx.x / g.groups, group = blockIdx.x % g.groups;
-  const int rl = lane & 15, gl = lane >> 4, row0 = wave * P::RW;
+  const int rl = lane & 15, gl = lane >> 4;
+  int rows[TI];                                // this lane's row in each of its wave's blocks
+#pragma unroll
+  for (int i = 0; i < TI; ++i) rows[i] = 16 * P::row(wave, i) + rl;
   const _Float16* x = static_cast<const _Float16*>(g.x) + int64_t(batch) * M * g.N;
   const int slices = g.N / kCols, per = (slices + g.groups - 1) / g.groups;
   const int s0 = group * per, s1 = min(s0 + per, slices);
@@ -70,14 +81,12 @@ __global__ void __launch_bounds__(512) narrow_kernel(NarrowArgs g) {
 #pragma unroll
     for (int i = 0; i < TI; ++i)
 #pragma unroll
-      for (int k = 0; k < KS; ++k) a[i][k] = *reinterpret_cast<const f16x8*>(A + (row0 + 16 * i + rl) * M + 32 * k + 8 * gl);
+      for (int k = 0; k < KS; ++k) a[i][k] = *reinterpret_cast<const f16x8*>(A + rows[i] * M + 32 * k + 8 * gl);
   }
-  f32x4v gram[GRAM ? TI : 1][GRAM ? TJ : 1];
+  f32x4v gram[GRAM ? P::kBlocks : 1];
   if constexpr (GRAM)
 #pragma unroll
-    for (int i = 0; i < TI; ++i)
-#pragma unroll
-      for (int j = 0; j < TJ; ++j) gram[i][j] = f32x4v{0.f, 0.f, 0.f, 0.f};
+    for (int t = 0; t < P::kBlocks; ++t) gram[t] = f32x4v{0.f, 0.f, 0.f, 0.f};
 
   for (int s = s0; s < s1; ++s) {
 #pragma unroll
@@ -88,7 +97,7 @@ __global__ void __launch_bounds__(512) narrow_kernel(NarrowArgs g) {
     __syncthreads();
     if (s + 1 < s1) fetch(s + 1);
     if constexpr (STEP) {
-      const int64_t at0 = (int64_t(batch) * M + row0 + rl) * g.N + s * kCols + 4 * gl;
+      const int64_t at0 = int64_t(batch) * M * g.N + s * kCols + 4 * gl;
       // z = b x + c A x; a lane holds row 16 i + l % 16 and columns 16 j + 4 (l / 16) + 0..3 of its wave's rows
       f32x4v acc[TI][2];
 #pragma unroll
@@ -103,17 +112,17 @@ __global__ void __launch_bounds__(512) narrow_kernel(NarrowArgs g) {
         }
       }
       auto own = [&](int at) { return __builtin_convertvector(*reinterpret_cast<const f16x4*>(xs + at), f32x4v); };
-      const f16x4* const lo = g.lo ? reinterpret_cast<const f16x4*>(static_cast<const _Float16*>(g.lo) + at0) : nullptr;
+      const _Float16* const lo = g.lo ? static_cast<const _Float16*>(g.lo) + at0 : nullptr;
       f16x4 left[TI][2];
 #pragma unroll
       for (int i = 0; i < TI; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const int at = (row0 + 16 * i + rl) * kRow + 16 * j + 4 * gl;
+          const int at = rows[i] * kRow + 16 * j + 4 * gl;
           const f32x4v z = (own(at) * g.b + acc[i][j] * (g.c / g.scale)) * 0.25f;
           *reinterpret_cast<f16x4*>(zs + at) = __builtin_convertvector(z, f16x4);
           acc[i][j] = f32x4v{0.f, 0.f, 0.f, 0.f};
-          left[i][j] = lo ? lo[4 * i * g.N + 4 * j] : f16x4{0, 0, 0, 0};
+          left[i][j] = lo ? *reinterpret_cast<const f16x4*>(lo + int64_t(rows[i]) * g.N + 16 * j) : f16x4{0, 0, 0, 0};
         }
       __syncthreads();
 #pragma unroll
@@ -130,12 +139,12 @@ __global__ void __launch_bounds__(512) narrow_kernel(NarrowArgs g) {
       for (int i = 0; i < TI; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const int at = (row0 + 16 * i + rl) * kRow + 16 * j + 4 * gl;
+          const int at = rows[i] * kRow + 16 * j + 4 * gl;
           const f32x4v v = (own(at) + __builtin_convertvector(left[i][j], f32x4v) * 0x1p-11f) * g.a + acc[i][j] * (4.f / g.scale);
           const f16x4 hi = __builtin_convertvector(v, f16x4);
           *reinterpret_cast<f16x4*>(xs + at) = hi;
           if (g.ylo)
-            *reinterpret_cast<f16x4*>(static_cast<_Float16*>(g.ylo) + at0 + int64_t(16 * i) * g.N + 16 * j) =
+            *reinterpret_cast<f16x4*>(static_cast<_Float16*>(g.ylo) + at0 + int64_t(rows[i]) * g.N + 16 * j) =
                 __builtin_convertvector((v - __builtin_convertvector(hi, f32x4v)) * 0x1p11f, f16x4);
         }
       __syncthreads();
@@ -149,44 +158,48 @@ __global__ void __launch_bounds__(512) narrow_kernel(NarrowArgs g) {
     if constexpr (GRAM) {
       f16x8 r[TI];
 #pragma unroll
-      for (int i = 0; i < TI; ++i) r[i] = *reinterpret_cast<const f16x8*>(xs + (row0 + 16 * i + rl) * kRow + 8 * gl);
+      for (int i = 0; i < TI; ++i) r[i] = *reinterpret_cast<const f16x8*>(xs + rows[i] * kRow + 8 * gl);
 #pragma unroll
-      for (int j = 0; j < TJ; ++j) {
-        const f16x8 b = *reinterpret_cast<const f16x8*>(xs + (16 * j + rl) * kRow + 8 * gl);
-#pragma unroll
-        for (int i = 0; i < TI; ++i) gram[i][j] = mfma_h(b, r[i], gram[i][j]);
+      for (int t = 0; t < P::kBlocks; ++t) {
+        const f16x8 b = *reinterpret_cast<const f16x8*>(xs + (16 * P::col(wave, t) + rl) * kRow + 8 * gl);
+        gram[t] = mfma_h(b, P::half(wave, t) == 0 ? r[0] : r[TI - 1], gram[t]);
       }
     }
     __syncthreads();
   }
   if constexpr (GRAM) {
-    // in the accumulators' order: [wave][i][j][lane], whole lines a store
-    f32x4v* to = reinterpret_cast<f32x4v*>(g.planes) + (int64_t(blockIdx.x) * 8 + wave) * (TI * TJ * 64) + lane;
+    // in the accumulators' order: [wave][block][lane], whole lines a store
+    f32x4v* to = reinterpret_cast<f32x4v*>(g.planes) + (int64_t(blockIdx.x) * 8 + wave) * (P::kBlocks * 64) + lane;
 #pragma unroll
-    for (int i = 0; i < TI; ++i)
-#pragma unroll
-      for (int j = 0; j < TJ; ++j) to[(i * TJ + j) * 64] = gram[i][j];
+    for (int t = 0; t < P::kBlocks; ++t) to[t * 64] = gram[t];
   }
 }
 
-// A thread adds 4 elements over a part of the planes, 256 of them to a workgroup in 4 parts.
+// A wave adds a block's 4 elements a lane over a part of the planes, 4 blocks of a matrix in 4 parts to a workgroup.
 template <int M>
 __global__ void __launch_bounds__(1024) narrow_join_kernel(const f32x4v* __restrict__ planes, _Float16* __restrict__ A, int groups, float scale) {
   using P = Narrow<M>;
   __shared__ f32x4v sums[3][256];
-  constexpr int kQuads = M * M / 4;
-  const int batch = blockIdx.x / (kQuads / 256), q = blockIdx.x % (kQuads / 256) * 256 + (threadIdx.x & 255), part = threadIdx.x >> 8;
+  constexpr int kAll = 8 * P::kBlocks;
+  static_assert(kAll % 4 == 0, "whole workgroups");
+  const int batch = blockIdx.x / (kAll / 4), lane = threadIdx.x & 63, place = threadIdx.x & 255;
+  const int block = __builtin_amdgcn_readfirstlane(blockIdx.x % (kAll / 4) * 4 + place / 64), part = threadIdx.x >> 8;
   const int per = (groups + 3) / 4, g0 = part * per, g1 = min(g0 + per, groups);
   f32x4v sum = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-  for (int g = g0; g < g1; ++g) sum += planes[(int64_t(batch) * groups + g) * kQuads + q];
-  if (part) sums[part - 1][threadIdx.x & 255] = sum;
+  for (int g = g0; g < g1; ++g) sum += planes[(int64_t(batch) * groups + g) * (kAll * 64) + block * 64 + lane];
+  if (part) sums[part - 1][place] = sum;
   __syncthreads();
   if (part) return;
-  sum = ((sum + sums[0][q & 255]) + sums[1][q & 255]) + sums[2][q & 255];
-  const int lane = q & 63, j = q / 64 % P::TJ, i = q / (64 * P::TJ) % P::TI, wave = q / (64 * P::TJ * P::TI);
-  const int row = wave * P::RW + 16 * i + (lane & 15), col = 16 * j + 4 * (lane >> 4);
-  *reinterpret_cast<f16x4*>(A + (int64_t(batch) * M + row) * M + col) = __builtin_convertvector(sum * (1.f / scale), f16x4);
+  sum = ((sum + sums[0][place]) + sums[1][place]) + sums[2][place];
+  const int wave = block / P::kBlocks, t = block % P::kBlocks;
+  const int row = 16 * P::row(wave, P::half(wave, t)) + (lane & 15), col = 16 * P::col(wave, t) + 4 * (lane >> 4);
+  const f16x4 v = __builtin_convertvector(sum * (1.f / scale), f16x4);
+  _Float16* const a = A + int64_t(batch) * M * M;
+  *reinterpret_cast<f16x4*>(a + row * M + col) = v;
+  if (P::TI > 1 && row / 16 != col / 16)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) a[(col + e) * M + row] = v[e];
 }
 
 template <bool STEP, bool GRAM>
@@ -198,6 +211,8 @@ int launch_narrow(hipStream_t st, const NarrowArgs& g) {
 }
 
 }  // namespace sl2
+
+size_t narrow_plane_bytes(int M) { return size_t(8 * (M == 128 ? sl2::Narrow<128>::kBlocks : sl2::Narrow<256>::kBlocks)) * 1024; }
 
 int narrow_groups(int M, int N, int64_t batches) {
   const int64_t slices = N / sl2::kCols;
@@ -214,7 +229,7 @@ int narrow_gram(hipStream_t st, const NarrowArgs& g) { return sl2::launch_narrow
 int narrow_step(hipStream_t st, const NarrowArgs& g) { return g.planes ? sl2::launch_narrow<true, true>(st, g) : sl2::launch_narrow<true, false>(st, g); }
 
 int narrow_join(hipStream_t st, const float* planes, void* A, int M, int groups, int64_t batches, float scale) {
-  const dim3 grid(unsigned(batches * (M * M / 1024))), block(1024);
+  const dim3 grid(unsigned(batches * (M == 128 ? sl2::Narrow<128>::kBlocks : sl2::Narrow<256>::kBlocks) * 2)), block(1024);
   const sl2::f32x4v* p = reinterpret_cast<const sl2::f32x4v*>(planes);
   if (M == 128) hipLaunchKernelGGL(sl2::narrow_join_kernel<128>, grid, block, 0, st, p, static_cast<_Float16*>(A), groups, scale);
   else hipLaunchKernelGGL(sl2::narrow_join_kernel<256>, grid, block, 0, st, p, static_cast<_Float16*>(A), groups, scale);

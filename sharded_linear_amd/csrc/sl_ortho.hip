@@ -225,8 +225,10 @@ struct OrthoPlan {
   int64_t x_bytes, a_bytes, part_bytes, bytes;           // one [L, mp, np] and one [L, mp, mp] fp16 array; the norms' sums
 };
 
-// Whether the steps go to the kernels of sl_narrow_h.hip.
-bool few_rows(int64_t mp, int64_t np, int64_t L) { return mp <= kNarrowRows; }
+// Whether the steps go to the kernels of sl_narrow_h.hip (left), or to the tiles (right): [128, 1024] 58 and 119 us, 16 of
+// [128, 8192] 243 and 278; [256, 512] 80 and 127, [256, 8192] 155 and 210, 16 of [256, 512] 134 and 131, 16 of [256, 8192]
+// 597 and 473.
+bool few_rows(int64_t mp, int64_t np, int64_t L) { return mp <= kNarrowRows / 2 || (mp <= kNarrowRows && L * np <= 8192); }
 
 int ortho_plan(int64_t L, int64_t rows, int64_t cols, OrthoPlan& p) {
   if (L < 0 || rows < 0 || cols < 0) return SL_EINVAL;
@@ -245,7 +247,7 @@ int ortho_plan(int64_t L, int64_t rows, int64_t cols, OrthoPlan& p) {
   if (L == 0 || p.mp == 0 || p.np == 0) return SL_OK;
   p.narrow = few_rows(p.mp, p.np, L);
   size_t planes = 0;                                     // of the products' split sums, or of the Gram matrices' shares
-  if (p.narrow) planes = size_t(L) * size_t(narrow_groups(int(p.mp), int(p.np), L)) * size_t(p.mp * p.mp) * 4;
+  if (p.narrow) planes = size_t(L) * size_t(narrow_groups(int(p.mp), int(p.np), L)) * narrow_plane_bytes(int(p.mp));
   else for (size_t b : {half_gemm_workspace_bytes(int(p.mp), int(p.mp), int(p.np), L, true), half_gemm_workspace_bytes(int(p.mp), int(p.mp), int(p.mp), L, true),
                    half_gemm_workspace_bytes(int(p.mp), int(p.np), int(p.mp), L, false)})
     planes = b > planes ? b : planes;
