@@ -5,24 +5,27 @@
 #include <cstddef>
 #include <cstdint>
 
-// C[M][N] = alpha * A . B + beta * D + diag * I for each of `batches` matrices, summed in fp32 and rounded to fp16 once;
-// with clo, what that rounding left, times 2^11, goes there (fp16).  A is [M][K] and B [N][K] (half_gemm_sym) or [K][N]
-// (half_gemm_nn).  M, N and K are multiples of 128; matrices are dense and follow each other without gaps.
+// C[M][N] = alpha * A . B + beta * D (+ diag * I) for each of `batches` matrices, summed in fp32 and rounded to fp16 once.
+//   half_gemm_sym: A [M][K] by the transpose of B [N][K], known to be symmetric; D is fp16, like C, or null (then there is no
+//                  diagonal either)
+//   half_gemm_nn:  A [M][K] by B [K][N]; D is bytes [M][N] in E5M2, or null; with D and clo, what the rounding of C left,
+//                  times 2^11, goes there in E5M2 (clo may be D)
+// M, N and K are multiples of 128; matrices are dense and follow each other without gaps.
 struct HalfArgs {
   const void *a, *b;           // the first matrix of each
-  const void* d;               // like C, or null
-  void *c, *clo;               // C is no operand and not D; clo null, or like C, D itself if need be
+  const void* d;
+  void *c, *clo;               // C is no operand and not D
   int M, N, K;
   int64_t batches;
   float alpha, beta, diag;
   float* ws;                   // half_gemm_workspace_bytes() for split sums
   // set by the launchers
-  int tiles_m, tiles_n, full, rest, splits, kt_per_split;
+  int tiles_m, tiles_n, full, rest, splits, kt_per_split, quarters, first;
 };
 constexpr int kHalfPad = 128;
 
-// A . B^T of a product known to be symmetric (M == N): tiles on and below the diagonal are computed and those below it
-// written a second time, transposed.
+// The symmetric product (M == N) computes the tiles on and below the diagonal and writes those below it a second time,
+// transposed.
 int half_gemm_sym(hipStream_t st, HalfArgs g);
 int half_gemm_nn(hipStream_t st, HalfArgs g);
 // Workspace of either with these extents (nn: M, N, K; sym: M == N).

@@ -8,9 +8,10 @@
 // only its results' stores stand between its products and the next item's.  Results leave straight from the
 // accumulators: the 16-lane groups of a wave trade pieces, so that a lane has 8 columns of a row.
 //
-// Tiles are dealt out in whole rounds of the chip; where the last round would leave workgroups idle, its tiles' sums are
-// split into fp32 planes (kept in the accumulators' own order, whole lines a store) which a second kernel adds in order
-// and finishes through the same epilogue.
+// Tiles of 256 x 256 are dealt out in whole rounds of the chip; what remains, or the whole of a small product, goes to
+// tiles of 128 x 128 in a launch of its own, and where its last round would leave places idle, sums are split into fp32
+// planes (kept in the accumulators' own order, whole lines a store) which another kernel adds in order and finishes through
+// the same epilogue.
 #include <hip/hip_runtime.h>
 
 #include <atomic>
@@ -25,7 +26,8 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 // ---- items ---------------------------------------------------------------------------------------
 
-struct HalfItem { int batch, m0, n0, kt0, kt1, plane; };      // plane < 0: the whole sum; all wave-uniform
+// plane < 0: the whole sum; mirror: the transposed tile too; all wave-uniform
+struct HalfItem { int batch, m0, n0, kt0, kt1, plane; bool mirror; };
 
 // Row and column of tile `t` of a lower triangle of n x n tiles in groups of 4 rows, column by column, so that tiles near each other in the
 // order share rows and columns: group q holds (4 q + 1) columns of all its rows, then the corner at the diagonal.
@@ -43,23 +45,31 @@ __device__ __forceinline__ int2 triangle(int t, int n) {
 
 template <class P, bool SYM>
 __device__ __forceinline__ HalfItem half_item(const HalfArgs& g, int x) {
-  const int per = SYM ? g.tiles_m * (g.tiles_m + 1) / 2 : g.tiles_m * g.tiles_n, stages = g.K / P::BK;
+  const int stages = g.K / P::BK;
   const bool part = x >= g.full;               // the parts of a tile are neighbours in the order
   const int plane = part ? x - g.full : -1, tile = part ? g.full + plane / g.splits : x;
   const int kt0 = part ? plane % g.splits * g.kt_per_split : 0, kt1 = part ? min(stages, kt0 + g.kt_per_split) : stages;
-  const int batch = tile / per, t = tile % per;
+  // quarters of the tiles from g.first on of a grid of twice the edge, where g.quarters
+  const int q = g.quarters ? 1 : 0, all = g.quarters ? g.first + tile / 4 : tile;
+  const int rows = (g.tiles_m + q) >> q, cols = (g.tiles_n + q) >> q;
+  const int per = SYM ? rows * (rows + 1) / 2 : rows * cols, batch = all / per, t = all % per;
   int tm, tn;
   if constexpr (SYM) {
-    const int2 at = triangle(t, g.tiles_m);
+    const int2 at = triangle(t, rows);
     tm = at.x;
     tn = at.y;
   } else {
     constexpr int GR = 4;
-    const int first = t / (GR * g.tiles_n) * GR, rows = min(g.tiles_m - first, GR), in = t % (GR * g.tiles_n);
-    tm = first + in % rows;
-    tn = in / rows;
+    const int first = t / (GR * cols) * GR, high = min(rows - first, GR), in = t % (GR * cols);
+    tm = first + in % high;
+    tn = in / high;
   }
-  return HalfItem{batch, __builtin_amdgcn_readfirstlane(tm * P::BM), __builtin_amdgcn_readfirstlane(tn * P::BN), kt0, kt1, plane};
+  const bool mirror = SYM && tm != tn;
+  if (g.quarters) {                            // those past the matrix's edge load zeros and store nothing
+    tm = 2 * tm + (tile >> 1 & 1);
+    tn = 2 * tn + (tile & 1);
+  }
+  return HalfItem{batch, __builtin_amdgcn_readfirstlane(tm * P::BM), __builtin_amdgcn_readfirstlane(tn * P::BN), kt0, kt1, plane, mirror};
 }
 
 // ---- epilogue ------------------------------------------------------------------------------------
@@ -73,14 +83,42 @@ __device__ __forceinline__ u32x4 trade(u32x4 v) {
   return u32x4{a[0], b[0], a[1], b[1]};
 }
 
+// Words of the four blocks of a row of blocks, transposed between them and the lane groups: afterwards group g holds all 4
+// words of block g (its own inverse).
+__device__ __forceinline__ u32x4 gather(u32x4 v) {
+  const auto a = __builtin_amdgcn_permlane16_swap(v[0], v[1], false, false), b = __builtin_amdgcn_permlane16_swap(v[2], v[3], false, false);
+  const auto c = __builtin_amdgcn_permlane32_swap(a[0], b[0], false, false), d = __builtin_amdgcn_permlane32_swap(a[1], b[1], false, false);
+  return u32x4{c[0], d[0], c[1], d[1]};
+}
+
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t half_rows(const void* p, int64_t first, int64_t bytes, bool in) {
   return __builtin_amdgcn_make_buffer_rsrc(static_cast<char*>(const_cast<void*>(p)) + first, 0, in ? int(bytes) : 0, kRsrcWord3);
 }
 
 constexpr int kStageBytes = 32 * 64 * 2;       // a wave's piece in LDS, for its transposed copy
 
+// What a kernel's epilogue adds: nothing; D in fp16 and the diagonal; what roundings left (E5M2); that, and keeping it anew.
+enum HalfEpi { kPlain, kAdd, kLeft, kLeftKeep };
+
+// D's part of a piece, in the order in which results are stored: rows of 64 fp16 elements, two loads of half a row's columns, or
+// rows of 64 bytes.
+template <int EPI>
+__device__ __forceinline__ void half_fetch(const HalfArgs& g, u32x4 (&d)[2][2], int batch, int m, int n, int lane) {
+  constexpr int E = EPI == kAdd ? 2 : 1;
+  const int rl = lane & 15, gl = lane >> 4;
+  const uint32_t off = uint32_t(rl) * uint32_t(g.N) * E + uint32_t(n + 16 * (E == 2 ? gl & 1 : gl) + (E == 2 ? 8 * (gl >> 1) : 0)) * E;
+  const auto rd = half_rows(g.d, (int64_t(batch) * g.M + m) * g.N * E, int64_t(32) * g.N * E, m < g.M && n < g.N);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int p = 0; p < E; ++p)
+      d[i][p] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rd, off + 64 * p + i * uint32_t(g.N) * 16 * E, 0, 0));
+}
+
 // `lds`: kStageBytes of the wave's own, used where `mirror` asks for the transposed copy too.
-__device__ __forceinline__ void half_finish(const HalfArgs& g, f32x4v (&acc)[2][4], int batch, int m, int n, bool mirror, uint32_t lds, int lane) {
+template <int EPI>
+__device__ __forceinline__ void half_finish(const HalfArgs& g, f32x4v (&acc)[2][4], const u32x4 (&d)[2][2], int batch, int m, int n, bool mirror,
+                                            uint32_t lds, int lane) {
   const bool in = m < g.M && n < g.N;
   const int64_t first = (int64_t(batch) * g.M + m) * g.N * 2, bytes = int64_t(32) * g.N * 2;
   const int rl = lane & 15, gl = lane >> 4;
@@ -92,13 +130,7 @@ __device__ __forceinline__ void half_finish(const HalfArgs& g, f32x4v (&acc)[2][
   for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] *= g.alpha;
-  if (g.d) {
-    const auto rd = half_rows(g.d, first, bytes, in);
-    u32x4 d[2][2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int p = 0; p < 2; ++p) d[i][p] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rd, off + 64 * p + i * down, 0, 0));
+  if constexpr (EPI == kAdd) {
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -108,7 +140,18 @@ __device__ __forceinline__ void half_finish(const HalfArgs& g, f32x4v (&acc)[2][
         acc[i][2 * p + 1] += wide(w[2], w[3]) * g.beta;
       }
   }
-  if (g.diag != 0.f && m < n + 64 && n < m + 32) {
+  if constexpr (EPI >= kLeft) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const u32x4 w = gather(d[i][0]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const auto lo = __builtin_amdgcn_cvt_pk_f32_bf8(int(w[j]), false), hi = __builtin_amdgcn_cvt_pk_f32_bf8(int(w[j]), true);
+        acc[i][j] += f32x4v{lo[0], lo[1], hi[0], hi[1]} * g.beta;
+      }
+    }
+  }
+  if (EPI == kAdd && m < n + 64 && n < m + 32) {
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -127,20 +170,18 @@ __device__ __forceinline__ void half_finish(const HalfArgs& g, f32x4v (&acc)[2][
       hi[i][p] = trade(u32x4{a.x, a.y, b.x, b.y});
       __builtin_amdgcn_raw_buffer_store_b128(hi[i][p], rc, off + 64 * p + i * down, 0, 0);
     }
-  if (g.clo) {
-    const auto rl_ = half_rows(g.clo, first, bytes, in);
+  if constexpr (EPI == kLeftKeep) {
+    const auto rk = half_rows(g.clo, first / 2, bytes / 2, in);
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 2; ++i) {
+      u32x4 w;
 #pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        uint2 w[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const f32x4v v = acc[i][2 * p + h];
-          w[h] = words((v - __builtin_convertvector(__builtin_convertvector(v, f16x4), f32x4v)) * 0x1p11f);
-        }
-        __builtin_amdgcn_raw_buffer_store_b128(trade(u32x4{w[0].x, w[0].y, w[1].x, w[1].y}), rl_, off + 64 * p + i * down, 0, 0);
+      for (int j = 0; j < 4; ++j) {
+        const f32x4v v = acc[i][j], left = (v - __builtin_convertvector(__builtin_convertvector(v, f16x4), f32x4v)) * 0x1p11f;
+        w[j] = uint32_t(__builtin_amdgcn_cvt_pk_bf8_f32(left[2], left[3], __builtin_amdgcn_cvt_pk_bf8_f32(left[0], left[1], 0, false), true));
       }
+      __builtin_amdgcn_raw_buffer_store_b128(gather(w), rk, uint32_t(rl) * uint32_t(g.N) + uint32_t(n + 16 * gl) + i * uint32_t(g.N) * 16, 0, 0);
+    }
   }
   if (!mirror) return;
   // Rows of 8 chunks in LDS, chunks XOR-swizzled by row; a group of 16 lanes then reads 4 x 16 blocks through transposing
@@ -169,7 +210,7 @@ __device__ __forceinline__ void half_finish(const HalfArgs& g, f32x4v (&acc)[2][
 
 // ---- the kernel ----------------------------------------------------------------------------------
 
-template <class P, bool SYM, int OCC>
+template <class P, bool SYM, int EPI, int OCC>
 __global__ void __launch_bounds__(P::WAVES * 64, OCC) half_gemm(HalfArgs g) {
   constexpr int BK = P::BK, WAVES = P::WAVES, WM = P::WM, WN = P::WN, TM = P::TM, TN = P::TN, KS = P::KS;
   constexpr int LA = P::LA, LB = P::LB, LPS = LA + LB, kStage = P::kStage, NR = TM + TN;
@@ -313,6 +354,13 @@ __global__ void __launch_bounds__(P::WAVES * 64, OCC) half_gemm(HalfArgs g) {
     }
     const int m = it.m0 + wm * WM, n = it.n0 + wn * WN;
     if (it.plane < 0) {
+      int l = lane;                            // from here on: what follows from it is not kept in registers over the stages
+      asm volatile("" : "+v"(l));
+      u32x4 d[2][2][2];                        // two pieces ahead
+      if constexpr (EPI != kPlain) {
+        half_fetch<EPI>(g, d[0], it.batch, m, n, l);
+        half_fetch<EPI>(g, d[1], it.batch, m + 32, n, l);
+      }
 #pragma unroll
       for (int i = 0; i < TM / 2; ++i) {
         f32x4v piece[2][4];
@@ -320,7 +368,9 @@ __global__ void __launch_bounds__(P::WAVES * 64, OCC) half_gemm(HalfArgs g) {
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int j = 0; j < 4; ++j) piece[h][j] = acc[2 * i + h][j];
-        half_finish(g, piece, it.batch, m + 32 * i, n, SYM && it.m0 != it.n0, lds0 + 2 * kStage + wave * kStageBytes, lane);
+        half_finish<EPI>(g, piece, d[i % 2], it.batch, m + 32 * i, n, SYM && it.mirror, lds0 + 2 * kStage + wave * kStageBytes, l);
+        if (EPI != kPlain && i + 2 < TM / 2) half_fetch<EPI>(g, d[i % 2], it.batch, m + 32 * (i + 2), n, l);
+        __builtin_amdgcn_sched_barrier(0);
       }
     } else {
       f32x4v* to = reinterpret_cast<f32x4v*>(g.ws) + (int64_t(it.plane) * WAVES + wave) * (TM * TN * 64) + lane;
@@ -332,6 +382,9 @@ __global__ void __launch_bounds__(P::WAVES * 64, OCC) half_gemm(HalfArgs g) {
     asm volatile("" ::: "memory");
     if (++q == count) break;
     stores = true;
+    // the next item's first fragments once more: kept over the results, they would push what the results need out of registers
+    static_for<NR>([&](auto mc) { read_one(mc, ic<0>{}, ic<0>{}, cur); });
+    __builtin_amdgcn_sched_barrier(0);
     clear();
     it = nth(q);
   }
@@ -339,16 +392,21 @@ __global__ void __launch_bounds__(P::WAVES * 64, OCC) half_gemm(HalfArgs g) {
 }
 
 // Adds the planes of the tiles from g.full on, in order, and finishes them: a wave to 32 rows by 64 columns.
-template <class P, bool SYM>
+template <class P, bool SYM, int EPI>
 __global__ void __launch_bounds__(64) half_join(HalfArgs g) {
   __shared__ __attribute__((aligned(16))) char stage[kStageBytes];
   constexpr int PIECES = P::TM / 2;
   const int lane = threadIdx.x, piece = blockIdx.x % PIECES, wave = blockIdx.x / PIECES % P::WAVES, tile = blockIdx.x / (PIECES * P::WAVES);
+  const HalfItem it = half_item<P, SYM>(g, g.full + tile * g.splits);
+  const int m = it.m0 + wave / P::WGN * P::WM + 32 * piece, n = it.n0 + wave % P::WGN * P::WN;
+  u32x4 d[2][2];
+  if constexpr (EPI != kPlain) half_fetch<EPI>(g, d, it.batch, m, n, lane);
   f32x4v acc[2][4];
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = f32x4v{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
   for (int s = 0; s < g.splits; ++s) {
     const f32x4v* from = reinterpret_cast<const f32x4v*>(g.ws) + (int64_t(tile * g.splits + s) * P::WAVES + wave) * (P::TM * P::TN * 64) + lane;
 #pragma unroll
@@ -356,8 +414,7 @@ __global__ void __launch_bounds__(64) half_join(HalfArgs g) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[i][j] += from[((2 * piece + i) * P::TN + j) * 64];
   }
-  const HalfItem it = half_item<P, SYM>(g, g.full + tile * g.splits);
-  half_finish(g, acc, it.batch, it.m0 + wave / P::WGN * P::WM + 32 * piece, it.n0 + wave % P::WGN * P::WN, SYM && it.m0 != it.n0, lds_addr(stage), lane);
+  half_finish<EPI>(g, acc, d, it.batch, m, n, SYM && it.mirror, lds_addr(stage), lane);
 }
 
 // ---- host ----------------------------------------------------------------------------------------
@@ -366,84 +423,106 @@ __global__ void __launch_bounds__(64) half_join(HalfArgs g) {
 template <bool B_KM> using Big = G4<true, B_KM, false, 2, 2, 4, 64, 256, 16, 256, true>;
 template <bool B_KM> using Small = G4<true, B_KM, false, 2, 2, 2, 64, 128, 16, 128, true>;
 
+// A product: `big` tiles of 256x256, from the first on, and `small` tiles of 128x128 for the rest, or for all of it (big ==
+// 0); of these `rest` are split in `splits` parts.
 struct HalfPlan {
-  bool big;
-  int64_t tiles, full, rest;
+  int64_t big, small, rest;
   int splits, kt_per_split;
   double us;
 };
 
-// Estimated time of a product in tiles of `edge`: whole rounds over the `places` of the chip, and a last one of `rest`
-// tiles whose sums may be split into up to `places` parts.
-HalfPlan half_plan_of(int M, int N, int K, int64_t batches, bool sym, bool big) {
-  const int edge = big ? 256 : 128, places = big ? 256 : 512;
-  const double stage = big ? 1.4 : 1.0, fixed = big ? 6.0 : 4.0;         // us of a 64 k stage, and of an item beside its stages
-  const int64_t m = (M + edge - 1) / edge, n = (N + edge - 1) / edge;
-  HalfPlan p{};
-  p.big = big;
-  p.tiles = batches * (sym ? m * (m + 1) / 2 : m * n);
-  p.rest = p.tiles % places;
-  p.full = p.tiles - p.rest;
-  const int stages = K / 64;
+// Adds the time of `small` tiles: whole rounds over 512 places, and a last one whose sums may be split.
+void plan_small(HalfPlan& p, int stages) {
+  constexpr int64_t places = 512;
+  auto stage = [](int64_t items) { return items > 256 ? 0.92 : 0.62; };         // us, with two workgroups on a CU or one
+  constexpr double fixed = 4.0, launch = 3.0;                                   // of an item beside its stages; of a kernel
+  p.rest = p.small % places;
   p.splits = 1;
   p.kt_per_split = stages;
-  double last = p.rest ? fixed + stages * stage : 0;
+  double last = p.rest ? fixed + stages * stage(p.rest) : 0;
   for (int s = 2; p.rest && s <= places / p.rest && s <= stages / 4; ++s) {
     const int per = (stages + s - 1) / s, parts = (stages + per - 1) / per;
-    const double t = fixed + per * stage + 5.0 + double(p.rest * parts) * edge * edge * 8 / 4.0e6;   // planes out and back at 4 TB/s
+    // planes out and back at 4 TB/s
+    const double t = fixed + per * stage(p.rest * parts) + launch + 2.0 + double(p.rest * parts) * (128 * 128 * 8) / 4.0e6;
     if (t < last) {
       last = t;
       p.splits = parts;
       p.kt_per_split = per;
     }
   }
-  if (p.splits == 1) {
-    p.full = p.tiles;
-    p.rest = 0;
-  }
-  p.us = double(p.tiles / places) * (fixed + stages * stage) + last;
-  return p;
+  if (p.splits == 1) p.rest = 0;
+  p.us += launch + double(p.small / places) * (fixed + stages * stage(places)) + last;
 }
 
 HalfPlan half_plan(int M, int N, int K, int64_t batches, bool sym) {
-  const HalfPlan a = half_plan_of(M, N, K, batches, sym, true), b = half_plan_of(M, N, K, batches, sym, false);
-  return a.us <= b.us ? a : b;
+  const int stages = K / 64;
+  auto tiles = [&](int edge) {
+    const int64_t m = (M + edge - 1) / edge, n = (N + edge - 1) / edge;
+    return batches * (sym ? m * (m + 1) / 2 : m * n);
+  };
+  constexpr double stage = 1.35, fixed = 8.0, launch = 3.0;
+  HalfPlan best{};
+  const int64_t all = tiles(256);
+  for (int64_t big : {int64_t(0), all / 256 * 256, all}) {
+    HalfPlan p{};
+    p.big = big;
+    p.small = big == 0 ? tiles(128) : 4 * (all - big);
+    if (big) p.us = launch + double((big + 255) / 256) * (fixed + stages * stage);
+    if (p.small) plan_small(p, stages);
+    if (best.us == 0 || p.us < best.us) best = p;
+  }
+  return best;
 }
 
-template <class P, bool SYM, int OCC>
-int launch_half(hipStream_t st, HalfArgs g, const HalfPlan& p) {
-  auto kfn = half_gemm<P, SYM, OCC>;
+template <class P, bool SYM, int EPI, int OCC>
+int launch_half(hipStream_t st, const HalfArgs& g) {
+  auto kfn = half_gemm<P, SYM, EPI, OCC>;
   constexpr int kLds = 2 * P::kStage + (SYM ? P::WAVES * kStageBytes : 0);
   static_assert(OCC * kLds <= 160 * 1024, "LDS");
   static std::atomic<uint64_t> attr{0};
   if (smem_attr_once(reinterpret_cast<const void*>(kfn), kLds, attr)) return -5;
-  g.tiles_m = (g.M + P::BM - 1) / P::BM;
-  g.tiles_n = (g.N + P::BN - 1) / P::BN;
-  g.full = int(p.full);
-  g.rest = int(p.rest);
-  g.splits = p.splits;
-  g.kt_per_split = p.kt_per_split;
-  const int64_t items = p.full + p.rest * p.splits, places = OCC * 256;
+  const int64_t items = g.full + int64_t(g.rest) * g.splits, places = OCC * 256;
   hipLaunchKernelGGL(kfn, dim3(unsigned(items < places ? items : places)), dim3(P::WAVES * 64), kLds, st, g);
-  if (hipGetLastError() != hipSuccess) return -5;
-  if (!p.rest) return 0;
-  hipLaunchKernelGGL((half_join<P, SYM>), dim3(unsigned(p.rest * P::WAVES * P::TM / 2)), dim3(64), 0, st, g);
   return hipGetLastError() == hipSuccess ? 0 : -5;
 }
 
-template <bool B_KM, bool SYM>
-int run_half(hipStream_t st, const HalfArgs& g) {
+template <bool SYM, int EPI>
+int run_half(hipStream_t st, HalfArgs g) {
   const HalfPlan p = half_plan(g.M, g.N, g.K, g.batches, SYM);
-  return p.big ? launch_half<Big<B_KM>, SYM, 1>(st, g, p) : launch_half<Small<B_KM>, SYM, 2>(st, g, p);
+  if (p.big) {
+    g.tiles_m = (g.M + 255) / 256;
+    g.tiles_n = (g.N + 255) / 256;
+    g.full = int(p.big);
+    g.rest = 0;
+    g.splits = 1;
+    g.quarters = 0;
+    if (launch_half<Big<SYM>, SYM, EPI, 1>(st, g)) return -5;
+  }
+  if (!p.small) return 0;
+  using P = Small<SYM>;
+  g.tiles_m = g.M / 128;
+  g.tiles_n = g.N / 128;
+  g.full = int(p.small - p.rest);
+  g.rest = int(p.rest);
+  g.splits = p.splits;
+  g.kt_per_split = p.kt_per_split;
+  g.quarters = p.big != 0;
+  g.first = int(p.big);
+  if (launch_half<P, SYM, EPI, 2>(st, g)) return -5;
+  if (!p.rest) return 0;
+  hipLaunchKernelGGL((half_join<P, SYM, EPI>), dim3(unsigned(p.rest * P::WAVES * P::TM / 2)), dim3(64), 0, st, g);
+  return hipGetLastError() == hipSuccess ? 0 : -5;
 }
 
 }  // namespace sl2
 
-int half_gemm_sym(hipStream_t st, HalfArgs g) { return sl2::run_half<true, true>(st, g); }
+int half_gemm_sym(hipStream_t st, HalfArgs g) { return g.d ? sl2::run_half<true, sl2::kAdd>(st, g) : sl2::run_half<true, sl2::kPlain>(st, g); }
 
-int half_gemm_nn(hipStream_t st, HalfArgs g) { return sl2::run_half<false, false>(st, g); }
+int half_gemm_nn(hipStream_t st, HalfArgs g) {
+  return !g.d ? sl2::run_half<false, sl2::kPlain>(st, g) : g.clo ? sl2::run_half<false, sl2::kLeftKeep>(st, g) : sl2::run_half<false, sl2::kLeft>(st, g);
+}
 
 size_t half_gemm_workspace_bytes(int M, int N, int K, int64_t batches, bool sym) {
   const sl2::HalfPlan p = sl2::half_plan(M, N, K, batches, sym);
-  return size_t(p.rest) * size_t(p.splits) * (p.big ? 256 * 256 * 4 : 128 * 128 * 4);
+  return size_t(p.rest) * size_t(p.splits) * (128 * 128 * 4);
 }

@@ -11,7 +11,7 @@ struct NarrowArgs {
   const void* A;               // [batches][M][M] fp16: the Gram matrices of x, times `scale`
   const void* x;               // [batches][M][N] fp16, times `scale`
   void* y;                     // the step's result, like x
-  const void* lo;              // what the rounding of x left, times scale 2^11, or null
+  const void* lo;              // what the rounding of x left, times scale 2^11, in E5M2, or null
   void* ylo;                   // the same of y, or null; may be lo
   float* planes;               // [batches][groups] partial Gram matrices of the result, or null
   int M, N, groups;

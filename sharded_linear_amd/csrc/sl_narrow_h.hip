@@ -112,8 +112,8 @@ __global__ void __launch_bounds__(512) narrow_kernel(NarrowArgs g) {
         }
       }
       auto own = [&](int at) { return __builtin_convertvector(*reinterpret_cast<const f16x4*>(xs + at), f32x4v); };
-      const _Float16* const lo = g.lo ? static_cast<const _Float16*>(g.lo) + at0 : nullptr;
-      f16x4 left[TI][2];
+      const uint8_t* const lo = g.lo ? static_cast<const uint8_t*>(g.lo) + at0 : nullptr;
+      uint32_t left[TI][2];
 #pragma unroll
       for (int i = 0; i < TI; ++i)
 #pragma unroll
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(512) narrow_kernel(NarrowArgs g) {
           const f32x4v z = (own(at) * g.b + acc[i][j] * (g.c / g.scale)) * 0.25f;
           *reinterpret_cast<f16x4*>(zs + at) = __builtin_convertvector(z, f16x4);
           acc[i][j] = f32x4v{0.f, 0.f, 0.f, 0.f};
-          left[i][j] = lo ? *reinterpret_cast<const f16x4*>(lo + int64_t(rows[i]) * g.N + 16 * j) : f16x4{0, 0, 0, 0};
+          left[i][j] = lo ? *reinterpret_cast<const uint32_t*>(lo + int64_t(rows[i]) * g.N + 16 * j) : 0u;
         }
       __syncthreads();
 #pragma unroll
@@ -140,12 +140,15 @@ __global__ void __launch_bounds__(512) narrow_kernel(NarrowArgs g) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int at = rows[i] * kRow + 16 * j + 4 * gl;
-          const f32x4v v = (own(at) + __builtin_convertvector(left[i][j], f32x4v) * 0x1p-11f) * g.a + acc[i][j] * (4.f / g.scale);
+          const auto l0 = __builtin_amdgcn_cvt_pk_f32_bf8(int(left[i][j]), false), l1 = __builtin_amdgcn_cvt_pk_f32_bf8(int(left[i][j]), true);
+          const f32x4v v = (own(at) + f32x4v{l0[0], l0[1], l1[0], l1[1]} * 0x1p-11f) * g.a + acc[i][j] * (4.f / g.scale);
           const f16x4 hi = __builtin_convertvector(v, f16x4);
           *reinterpret_cast<f16x4*>(xs + at) = hi;
-          if (g.ylo)
-            *reinterpret_cast<f16x4*>(static_cast<_Float16*>(g.ylo) + at0 + int64_t(rows[i]) * g.N + 16 * j) =
-                __builtin_convertvector((v - __builtin_convertvector(hi, f32x4v)) * 0x1p11f, f16x4);
+          if (g.ylo) {
+            const f32x4v r = (v - __builtin_convertvector(hi, f32x4v)) * 0x1p11f;
+            *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(g.ylo) + at0 + int64_t(rows[i]) * g.N + 16 * j) =
+                uint32_t(__builtin_amdgcn_cvt_pk_bf8_f32(r[2], r[3], __builtin_amdgcn_cvt_pk_bf8_f32(r[0], r[1], 0, false), true));
+          }
         }
       __syncthreads();
       _Float16* y = static_cast<_Float16*>(g.y) + int64_t(batch) * M * g.N;

@@ -8,8 +8,8 @@
 // every element of X, A and P lies within fp16's range at one fixed scale, 2^12, where fp16 keeps 11 bits and
 // bf16 would keep 8.  Measured against 64 bits on [512, 2048] of normal values the result is 1.5e-3 off in fp16 and
 // 1.2e-2 in bf16 (relative, in the 2-norm).  A rounding of X in a direction whose singular value is small is multiplied
-// by up to a each step, so the first kLoSteps steps add a times what the rounding of X left (kept in fp16 beside it) to
-// P X: with singular values falling over four decades the error is 1.5e-3 with it and 9e-3 without.  (P has a on its
+// by up to a each step, so the first kLoSteps steps add a times what the rounding of X left (kept in E5M2 beside it: the
+// whole is then held to 2^-14) to P X: with singular values falling over four decades the error is 1.5e-3 with it and 9e-3 without.  (P has a on its
 // diagonal rather than the epilogue adding a X: P's rounding scales X and so leaves small singular values their place,
 // P is nearer to 1 than P - a I in the last steps, and X is not read a second time.)
 //
@@ -47,7 +47,8 @@ struct PassArgs {
   bool nesterov, has_m, g_bf16, tall, vec; // vec: rows begin at multiples of 4 elements
   double* part;                            // [matrices][kNormBlocks]
   int blocks;
-  _Float16 *x, *lo;
+  _Float16* x;
+  uint32_t* lo;                            // four E5M2 bytes a word
   float keep, step;                        // W <- keep W - step X
   bool update, has_master;
 };
@@ -122,7 +123,7 @@ __global__ void __launch_bounds__(512) ortho_norm(Mats mats, PassArgs a) {
 
 constexpr int kEdge = 64;                  // tiles of the passes below
 
-// X = U / |U| * 2^12 in fp16, and what the rounding left times 2^11, padded with zeros; one tile of U to a workgroup.
+// X = U / |U| * 2^12 in fp16, and what the rounding left times 2^11 in E5M2, padded with zeros; one tile of U to a workgroup.
 __global__ void __launch_bounds__(256) ortho_scale(Mats mats, PassArgs a) {
   __shared__ double red[4];
   __shared__ float tile[kEdge][kEdge + 1];
@@ -168,7 +169,8 @@ __global__ void __launch_bounds__(256) ortho_scale(Mats mats, PassArgs a) {
     const int64_t at = (int64_t(l) * a.mp + xr + tr + 16 * k) * a.np + xc + 4 * tc;
     const f16x4 hi = __builtin_convertvector(x[k], f16x4);
     *reinterpret_cast<f16x4*>(a.x + at) = hi;
-    *reinterpret_cast<f16x4*>(a.lo + at) = __builtin_convertvector((x[k] - __builtin_convertvector(hi, f32x4)) * 0x1p11f, f16x4);
+    const f32x4 left = (x[k] - __builtin_convertvector(hi, f32x4)) * 0x1p11f;
+    a.lo[at / 4] = uint32_t(__builtin_amdgcn_cvt_pk_bf8_f32(left[2], left[3], __builtin_amdgcn_cvt_pk_bf8_f32(left[0], left[1], 0, false), true));
   }
 }
 
@@ -243,7 +245,7 @@ int ortho_plan(int64_t L, int64_t rows, int64_t cols, OrthoPlan& p) {
   p.x_bytes = L * p.mp * p.np * 2;
   p.a_bytes = L * p.mp * p.mp * 2;
   p.part_bytes = L * kNormBlocks * 8;
-  p.bytes = 3 * p.x_bytes + 2 * p.a_bytes + p.part_bytes;
+  p.bytes = 2 * p.x_bytes + p.x_bytes / 2 + 2 * p.a_bytes + p.part_bytes;
   if (L == 0 || p.mp == 0 || p.np == 0) return SL_OK;
   p.narrow = few_rows(p.mp, p.np, L);
   size_t planes = 0;                                     // of the products' split sums, or of the Gram matrices' shares
@@ -300,12 +302,12 @@ int iterate(hipStream_t st, const Mats& mats, PassArgs a, const OrthoPlan& p, in
   _Float16* x[2];
   x[0] = reinterpret_cast<_Float16*>(at); at += p.x_bytes;
   x[1] = reinterpret_cast<_Float16*>(at); at += p.x_bytes;
-  _Float16* lo = reinterpret_cast<_Float16*>(at); at += p.x_bytes;
+  uint32_t* lo = reinterpret_cast<uint32_t*>(at); at += p.x_bytes / 2;
   _Float16* A = reinterpret_cast<_Float16*>(at); at += p.a_bytes;
   _Float16* P = reinterpret_cast<_Float16*>(at); at += p.a_bytes;
   a.part = reinterpret_cast<double*>(at) + first * kNormBlocks; at += p.part_bytes;
   a.x = x[0] + first * p.mp * p.np;
-  a.lo = lo + first * p.mp * p.np;
+  a.lo = lo + first * p.mp * p.np / 4;
   const int64_t groups = (a.rows * a.cols + 3) / 4;
   a.blocks = int((groups + 2047) / 2048 < kNormBlocks ? (groups + 2047) / 2048 : kNormBlocks);
   const int64_t left = L - first < kMats ? L - first : kMats;
