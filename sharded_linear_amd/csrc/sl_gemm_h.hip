@@ -431,19 +431,22 @@ struct HalfPlan {
   double us;
 };
 
-// Adds the time of `small` tiles: whole rounds over 512 places, and a last one whose sums may be split.
+// Times in us, fitted to measured products with every split count (36 to 504 items of 5 to 128 stages: [1024, 1024] over 4096
+// unsplit 41 us, in 2, 4, 6, 8 and 14 parts 28, 19, 19, 21 and 23; [2048, 2048] over 8192 in 1, 2 and 3 parts 88, 68 and 57).
+// 128x128 tiles: a 64 k stage by the workgroups under way on 256 CUs; what an item costs beside its stages; a launch; and a
+// split, by the planes that go out and come back.
 void plan_small(HalfPlan& p, int stages) {
   constexpr int64_t places = 512;
-  auto stage = [](int64_t items) { return items > 256 ? 0.92 : 0.62; };         // us, with two workgroups on a CU or one
-  constexpr double fixed = 4.0, launch = 3.0;                                   // of an item beside its stages; of a kernel
+  auto stage = [](int64_t items) { return items <= 256 ? 0.57 : 0.92; };
+  constexpr double full_stage = 1.05, fixed = 3.0, launch = 4.0, join = 3.0, plane = 0.018;
   p.rest = p.small % places;
   p.splits = 1;
   p.kt_per_split = stages;
   double last = p.rest ? fixed + stages * stage(p.rest) : 0;
   for (int s = 2; p.rest && s <= places / p.rest && s <= stages / 4; ++s) {
     const int per = (stages + s - 1) / s, parts = (stages + per - 1) / per;
-    // planes out and back at 4 TB/s
-    const double t = fixed + per * stage(p.rest * parts) + launch + 2.0 + double(p.rest * parts) * (128 * 128 * 8) / 4.0e6;
+    const int64_t items = p.rest * parts;
+    const double t = fixed + per * stage(items) + join + double(items) * plane;
     if (t < last) {
       last = t;
       p.splits = parts;
@@ -451,23 +454,26 @@ void plan_small(HalfPlan& p, int stages) {
     }
   }
   if (p.splits == 1) p.rest = 0;
-  p.us += launch + double(p.small / places) * (fixed + stages * stage(places)) + last;
+  p.us += launch + double(p.small / places) * (fixed + stages * full_stage) + last;
 }
 
+// 256x256 tiles: rounds of the chip, each with its stores behind it.  16 x [1536, 2048]: the Gram products (336 tiles) 107 us in
+// two rounds, 108 as one round and quarters, 104 in 128x128 tiles; the squares 93, 91 and 83; P X (768 tiles) 140 in three
+// rounds, 173 in 128x128 tiles.  2 x [4096, 5504], Gram products (272 tiles): 240, 179 and 199.
 HalfPlan half_plan(int M, int N, int K, int64_t batches, bool sym) {
   const int stages = K / 64;
   auto tiles = [&](int edge) {
     const int64_t m = (M + edge - 1) / edge, n = (N + edge - 1) / edge;
     return batches * (sym ? m * (m + 1) / 2 : m * n);
   };
-  constexpr double stage = 1.35, fixed = 8.0, launch = 3.0;
+  constexpr double stage = 1.38, fixed = 15.0, launch = 6.0, quarters = 3.0;
   HalfPlan best{};
   const int64_t all = tiles(256);
   for (int64_t big : {int64_t(0), all / 256 * 256, all}) {
     HalfPlan p{};
     p.big = big;
     p.small = big == 0 ? tiles(128) : 4 * (all - big);
-    if (big) p.us = launch + double((big + 255) / 256) * (fixed + stages * stage);
+    if (big) p.us = launch + double((big + 255) / 256) * (fixed + stages * stage) + (p.small ? quarters : 0);
     if (p.small) plan_small(p, stages);
     if (best.us == 0 || p.us < best.us) best = p;
   }
