@@ -15,7 +15,7 @@ from torch.autograd.function import once_differentiable
 from .ops import (sl_embedding_fwd, sl_embedding_wgrad_accum, sl_linear_dgrad, sl_linear_dgrad_mxfp4, sl_linear_dgrad_mxfp8,
                   sl_linear_fwd, sl_linear_fwd_mxfp4, sl_linear_fwd_mxfp8, sl_linear_wgrad_accum, sl_linear_wgrad_accum_mxfp4,
                   sl_linear_wgrad_accum_mxfp8, sl_mxfp4_quantize, sl_mxfp8_quantize, sl_rmsnorm_bwd, sl_rmsnorm_fwd,
-                  sl_rmsnorm_fwd_mxfp8)
+                  sl_rmsnorm_fwd_mxfp8, _raw_stream)
 
 
 class LinearWithGradAccumulation(torch.autograd.Function):
@@ -115,6 +115,24 @@ def _need_main_grad(weight, needed):
         raise ValueError("gradient accumulation fusion needs weight.main_grad (a grad_data view)")
 
 
+def _accumulators(*tensors):
+    """The gradient accumulators of the leaves among ``tensors``, to be held until the call has joined them to its graph.
+
+    A leaf has one accumulator for all its living graphs, and it belongs to the stream on which the first of them was made.
+    A backward pass that is captured joins that stream to the capture, which ends the process if the stream is not the
+    capture's: such a call is refused here."""
+    held = []
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad and t.is_leaf and t.is_cuda:
+                node, stream = torch.autograd.graph.get_gradient_edge(t).node, _raw_stream(t.device.index)
+                held.append(node)
+                if node.metadata.setdefault("sl_stream", stream) != stream and torch.cuda.is_current_stream_capturing():
+                    raise RuntimeError("a graph of these leaves that was made on another stream lives: drop its results "
+                                       "before the capture, for its backward pass cannot be captured beside them")
+    return held
+
+
 class EmbeddingWithGradAccumulation(torch.autograd.Function):
     @staticmethod
     def forward(ctx, ids, weight, vocab_start, scale):
@@ -138,6 +156,7 @@ def embedding_with_grad_accumulation(ids: torch.Tensor, weight: torch.Tensor, vo
     vocab_start .. vocab_start + V - 1), so that the ranks' results add up.  Backward adds into weight.main_grad."""
     if not torch.is_grad_enabled():
         weight = weight.detach()
+    held = _accumulators(weight)  # noqa: F841
     return EmbeddingWithGradAccumulation.apply(ids, weight, vocab_start, scale)
 
 
@@ -189,6 +208,7 @@ def rmsnorm_with_grad_accumulation(input: torch.Tensor, weight: torch.Tensor, re
     the residual stream that the next block adds to.  The weight's gradient goes to weight.main_grad."""
     if not torch.is_grad_enabled():
         weight = weight.detach()
+    held = _accumulators(input, weight, residual)  # noqa: F841
     return RMSNormWithGradAccumulation.apply(input, weight, residual, eps)
 
 
@@ -251,4 +271,5 @@ def norm_linear_mxfp8_with_grad_accumulation(input: torch.Tensor, norm_weight: t
     """Y = norm(input + residual) . weight^T with every product of the step on MXFP8 operands: returns Y, or (Y, h) with a
     residual, h = input + residual.  Both weights' gradients go to their main_grad.  ``weight_mxfp8`` is
     sl_mxfp8_quantize(weight), made once and passed to every micro-batch; without it the weight is quantised in each call."""
+    held = _accumulators(input, norm_weight, residual, weight)  # noqa: F841
     return NormLinearMXFP8WithGradAccumulation.apply(input, norm_weight, residual, weight, eps, weight_mxfp8)

@@ -198,6 +198,19 @@ def test_large_tiles(rows, cols):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("L,rows,cols", [(50, 640, 640), (60, 600, 520), (9, 1408, 1300), (1, 1800, 5000), (2, 4096, 2048)])
+def test_rounds_of_tiles(L, rows, cols):
+    """Products of whole rounds of the largest tiles with quarters for the rest, tiles half outside the matrix among them, and split
+    sums of either."""
+    say(f"case orthogonalize {L} x [{rows}, {cols}]")
+    G = _randn(_gen(L), L, rows, cols)
+    O = sl.sl_orthogonalize(G)
+    for l in range(L):
+        assert _off(O[l], _iterate(G[l])) <= _bound(), l
+    assert torch.equal(sl.sl_orthogonalize(G), O)
+
+
+@pytest.mark.gpu
 def test_singular_values_over_decades():
     """Where singular values fall over four decades and over two steps of rank, the small ones are reached as the formula
     has it: a rounding of X would be multiplied by up to 3.4^5 there, but the first three steps carry what it left."""
