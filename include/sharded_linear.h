@@ -353,7 +353,7 @@ int sl_linear_dgrad_mxfp4w(void* stream, const void* dY, const uint8_t* Wq, cons
  *   wgrad: main_grad[v] += scale * sum of dY[t] over the t with ids[t] - vocab_start = v, fp32, in place;
  *                          rows that no token names are not touched
  * ids[T] are int32 or int64 (ids_bytes 4 or 8, aligned to that).  H % 8 == 0; V up to 2^24; the gradient
- * takes up to 2^26 tokens, and T * H up to about 2^39 (SL_ESHAPE).  vocab_start >= 0 and scale finite
+ * takes up to 2^26 tokens, T * H up to 2^37 and H up to 2^23 (SL_ESHAPE).  vocab_start >= 0 and scale finite
  * (SL_EINVAL).  The gradient's sums are fp32 in an order that depends on the ids alone: the same call gives
  * the same bits.  It takes a workspace of its query's bytes (0 for few tokens, workspace may then be NULL; 16-byte
  * aligned; initial contents do not matter; calls that may run concurrently need distinct ones) and makes up to three
@@ -404,7 +404,7 @@ int sl_rmsnorm_bwd(void* stream, const void* dY, const void* h, const void* w, c
  * sl_orthogonalize: O[L, rows, cols] (bf16) = X for U = G[L, rows, cols] (fp32 or bf16: g_bytes 4 or 2).
  * sl_muon_step: one optimiser step of L weights.  W, G, M and master are host arrays of L device pointers, read
  * during the call: bf16 weights, fp32 gradients (main_grad views), fp32 momenta, and fp32 master weights (master NULL:
- * none).  No two matrices of W, M and master may overlap.
+ * none).  A matrix of W, M or master overlaps no other of the call's.
  *   M <- momentum * M + G;   U = nesterov ? G + momentum * M : M
  *   W <- (1 - lr * weight_decay) * W - lr * scale * X   (of the master where there is one, which is then rounded to W)
  * lr, momentum, weight_decay and scale must be finite, steps 0 .. 64 (SL_EINVAL); L <= 65535 and a padded matrix under

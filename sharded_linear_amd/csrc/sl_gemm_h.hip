@@ -259,8 +259,8 @@ __global__ void __launch_bounds__(P::WAVES * 64, OCC) half_gemm(HalfArgs g) {
 
   // The item being loaded: operands as descriptors from the tile's first element to the matrix's end.  A tile's second
   // half of rows may lie past the end as a whole (extents are multiples of 128): its descriptor then has no bytes, and the
-  // loads write zeros.  Columns past a K x N operand's edge read what follows in the workspace, and no result of theirs is
-  // stored.
+  // loads write zeros.  Columns past a K x N operand's edge read the next row's first ones (zeros behind the last row), and no
+  // result of theirs is stored.
   i32x4 ra, rb;
   int a_high, b_high;                          // bytes of the second halves' descriptors
   uint32_t ka, kb;

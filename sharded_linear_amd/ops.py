@@ -740,6 +740,16 @@ def sl_orthogonalize(G, out=None, steps=5, coefficients=NEWTON_SCHULZ, workspace
     return out
 
 
+def _want_apart(written, read):
+    """No matrix that a call writes overlaps another of its matrices; those that it only reads may be the same."""
+    end, last_written = 0, False
+    for start, stop, w in sorted((t.data_ptr(), t.data_ptr() + t.nbytes, w) for ts, w in ((written, True), (read, False)) for t in ts):
+        if start < end and (w or last_written):
+            raise ValueError("a weight, momentum or master overlaps another of the matrices, or is given twice")
+        if stop >= end:
+            end, last_written = stop, w
+
+
 def sl_muon_step(weights, main_grads, momenta, lr, momentum=0.95, nesterov=True, weight_decay=0.0, scale=None, masters=None,
                  steps=5, coefficients=NEWTON_SCHULZ, workspace=None):
     """One step of bf16 weights of one shape, in place, from their fp32 main_grads: M <- momentum M + G, U = G + momentum M
@@ -758,9 +768,7 @@ def sl_muon_step(weights, main_grads, momenta, lr, momentum=0.95, nesterov=True,
     for x, name, dtype in zip(lists, ("a weight", "a main_grad", "a momentum", "a master"), (BF16, F32, F32, F32)):
         for t in x or ():
             _want(t, name, dtype, (rows, cols), dev)
-    written = [t.data_ptr() for x in (lists[0], lists[2], lists[3]) for t in x or ()]
-    if rows and cols and len(set(written)) < len(written) or {t.data_ptr() for t in lists[1]} & set(written):
-        raise ValueError("a weight, momentum or master is given twice")
+    _want_apart([t for x in (lists[0], lists[2], lists[3]) for t in x or ()], lists[1])
     if scale is None:
         scale = max(1.0, rows / cols) ** 0.5 if cols else 1.0
     steps, k = _coefficients(steps, coefficients)

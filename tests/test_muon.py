@@ -122,6 +122,33 @@ def test_binding_refusals(monkeypatch):
     assert sl.sl_muon_step([], [], [], 0.1) is None
 
 
+@pytest.mark.parametrize("weights,grads,momenta,masters,ok", [
+    ((0, 24), (0, 24), (100, 124), None, True),          # neighbours
+    ((0, 24), (0, 0), (100, 124), None, True),           # one gradient for both
+    ((0, 23), (0, 24), (100, 124), None, False),         # weights overlap
+    ((0, 24), (0, 24), (100, 120), None, False),         # momenta overlap
+    ((0, 24), (0, 24), (100, 47), None, False),          # a momentum over a gradient
+    ((0, 24), (0, 24), (100, 124), (148, 172), True),
+    ((0, 24), (0, 24), (100, 124), (148, 171), False),   # masters overlap
+    ((0, 24), (0, 24), (100, 124), (76, 148), True),     # a master just before a momentum
+    ((0, 24), (0, 24), (100, 124), (77, 148), False),    # and over its first element
+])
+def test_overlaps_are_refused(weights, grads, momenta, masters, ok, monkeypatch):
+    """Matrices of 24 elements that begin at the given elements of one fp32 and one bf16 array."""
+    from sharded_linear_amd import ops
+    monkeypatch.setattr(ops, "_device", lambda t: t.device)
+    monkeypatch.setattr(ops, "_scratch", lambda *a: (None, 0))
+    monkeypatch.setattr(ops, "_launch", lambda *a: None)
+    data, params = torch.zeros(300), torch.zeros(300, dtype=BF16)
+    at = lambda a, starts: None if starts is None else [a[k:k + 24].view(4, 6) for k in starts]  # noqa: E731
+    args = at(params, weights), at(data, grads), at(data, momenta), 0.1
+    if ok:
+        sl.sl_muon_step(*args, masters=at(data, masters))
+    else:
+        with pytest.raises(ValueError, match="overlaps"):
+            sl.sl_muon_step(*args, masters=at(data, masters))
+
+
 # ---- on the GPU -----------------------------------------------------------------------------------
 
 def _gen(seed):
@@ -328,6 +355,8 @@ def test_empty_extents():
     say("case orthogonalize nothing")
     assert sl.sl_orthogonalize(torch.zeros((0, 5, 6), device="cuda")).shape == (0, 5, 6)
     assert sl.sl_orthogonalize(torch.zeros((2, 0, 6), device="cuda")).shape == (2, 0, 6)
+    w, g, m = (torch.zeros((0, 6), device="cuda", dtype=t) for t in (BF16, torch.float32, torch.float32))
+    sl.sl_muon_step([w, w], [g, g], [m, m], 0.1)
 
 
 @pytest.mark.gpu
