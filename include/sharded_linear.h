@@ -397,8 +397,8 @@ int sl_rmsnorm_bwd(void* stream, const void* dY, const void* h, const void* w, c
  * [m, n], m <= n (a tall one is transposed on the way in and out):
  *   X = U / |U|_F (zeros stay zeros);   `steps` times:  A = X.X^T,  X <- a X + (b A + c A.A).X
  * coeffs is a host array of a, b, c for each step.  Products run in fp16 at one fixed scale with fp32 sums; the
- * host checks that the coefficients keep singular values that start in [0, 1] below 3 and a I + b A + c A.A
- * below 15, and b X + c A.X below 60 (SL_EINVAL otherwise), which keeps every element in fp16's range.  A gradient with an infinity or a NaN gives
+ * host checks that the coefficients keep singular values that start in [0, 1] below 3, a I + b A + c A.A
+ * below 15 and c A.X below 60 (SL_EINVAL otherwise), which keeps every element in fp16's range.  A gradient with an infinity or a NaN gives
  * NaN.
  *
  * sl_orthogonalize: O[L, rows, cols] (bf16) = X for U = G[L, rows, cols] (fp32 or bf16: g_bytes 4 or 2).

@@ -6,12 +6,12 @@
 // The polynomial a + b z^3 + c z^5 moves every singular value towards 1; all of the work is products of [m, m] and
 // [m, n] matrices.  They run in fp16: singular values stay below 3 (checked on the host for the coefficients given), so
 // every element of X, A and P lies within fp16's range at one fixed scale, 2^12, where fp16 keeps 11 bits and
-// bf16 would keep 8.  Measured against 64 bits on [512, 2048] of normal values the result is 1.5e-3 off in fp16 and
-// 1.2e-2 in bf16 (relative, in the 2-norm).  A rounding of X in a direction whose singular value is small is multiplied
-// by up to a each step, so the first kLoSteps steps add a times what the rounding of X left (kept in E5M2 beside it: the
-// whole is then held to 2^-14) to P X: with singular values falling over four decades the error is 1.5e-3 with it and 9e-3 without.  (P has a on its
-// diagonal rather than the epilogue adding a X: P's rounding scales X and so leaves small singular values their place,
-// P is nearer to 1 than P - a I in the last steps, and X is not read a second time.)
+// bf16 would keep 8.  Against 64 bits, on [512, 2048] of normal values, the result is 2.2e-3 off in fp16, 1.7e-3 of it its own
+// rounding to bf16, and 1.2e-2 in bf16 (relative, in the 2-norm).  A rounding of X in a direction whose singular value is
+// small is multiplied by up to a each step, so the first kLoSteps steps add a times what the rounding of X left (kept in
+// E5M2 beside it: the whole is then held to 2^-14) to P X: with singular values falling over four decades the error is 2.4e-3
+// with it and 9e-3 without.  (P has a on its diagonal rather than the epilogue adding a X: P's rounding scales X and so leaves
+// small singular values their place, P is nearer to 1 than P - a I in the last steps, and X is not read a second time.)
 //
 // Around the products: one pass for the momentum and the norm (sums of squares in 64 bits: any finite gradient has a
 // norm), one that scales, transposes a tall matrix and pads to multiples of 128 with zeros, and one that writes the
@@ -227,8 +227,8 @@ struct OrthoPlan {
   int64_t x_bytes, a_bytes, part_bytes, bytes;           // one [L, mp, np] and one [L, mp, mp] fp16 array; the norms' sums
 };
 
-// Whether the steps go to the kernels of sl_narrow_h.hip (left), or to the tiles (right): [128, 1024] 58 and 119 us, 16 of
-// [128, 8192] 243 and 278; [256, 512] 80 and 127, [256, 8192] 155 and 210, 16 of [256, 512] 134 and 131, 16 of [256, 8192]
+// Whether the steps go to the kernels of sl_narrow_h.hip (left), or to the tiles (right): [128, 1024] 57 and 119 us, 16 of
+// [128, 8192] 231 and 278; [256, 512] 80 and 127, [256, 8192] 155 and 210, 16 of [256, 512] 134 and 131, 16 of [256, 8192]
 // 597 and 473.
 bool few_rows(int64_t mp, int64_t np, int64_t L) { return mp <= kNarrowRows / 2 || (mp <= kNarrowRows && L * np <= 8192); }
 
@@ -257,17 +257,13 @@ int ortho_plan(int64_t L, int64_t rows, int64_t cols, OrthoPlan& p) {
   return SL_OK;
 }
 
-// The largest |a s + b s^3 + c s^5| and |b s + c s^3| over 0 <= s <= top, and the largest |a + b z + c z^2| over
-// 0 <= z <= top^2.
-void step_bounds(const float* k, double top, double& x, double& inner, double& rest) {
+// The largest |a s + b s^3 + c s^5| over 0 <= s <= top, and the largest |a + b z + c z^2| over 0 <= z <= top^2.
+void step_bounds(const float* k, double top, double& x, double& inner) {
   const double a = k[0], b = k[1], c = k[2];
   auto p = [&](double s) { return std::fabs(s * (a + s * s * (b + c * s * s))); };
   auto q = [&](double z) { return std::fabs(a + z * (b + c * z)); };
   x = p(top);
   inner = std::fmax(q(0), q(top * top));
-  auto r = [&](double s) { return std::fabs(s * (b + c * s * s)); };
-  rest = r(top);
-  if (c != 0 && -b / (3 * c) > 0 && -b / (3 * c) < top * top) rest = std::fmax(rest, r(std::sqrt(-b / (3 * c))));
   if (c != 0) {
     const double z = -b / (2 * c), d = 9 * b * b - 20 * a * c;
     if (z > 0 && z < top * top) inner = std::fmax(inner, q(z));
@@ -282,14 +278,14 @@ void step_bounds(const float* k, double top, double& x, double& inner, double& r
 }
 
 // Whether X, A and a I + b A + c A^2 stay in range at kScale: |X| <= 3 (12288), |A| <= 9 (36864), the third <= 15 (61440);
-// and b X + c A X at a quarter of it: <= 60.
+// and c A X at a quarter of it: <= 60.
 int check_steps(int32_t steps, const float* coeffs) {
   if (steps < 0 || steps > kMaxSteps || (steps && !coeffs)) return SL_EINVAL;
   double top = 1;
   for (int i = 0; i < steps; ++i) {
-    double x, inner, rest;
-    step_bounds(coeffs + 3 * i, top, x, inner, rest);
-    if (!(x <= 3) || !(inner <= 15) || !(rest <= 60)) return SL_EINVAL;
+    double x, inner;
+    step_bounds(coeffs + 3 * i, top, x, inner);
+    if (!(x <= 3) || !(inner <= 15) || !(std::fabs(coeffs[3 * i + 2]) * top * top * top <= 60)) return SL_EINVAL;
     top = x * 1.01;                                      // roundings
   }
   return SL_OK;
@@ -322,14 +318,14 @@ int iterate(hipStream_t st, const Mats& mats, PassArgs a, const OrthoPlan& p, in
     g.A = A; g.lo = lo;
     g.M = int(p.mp); g.N = int(p.np); g.batches = L;
     g.groups = narrow_groups(g.M, g.N, L);
-    g.scale = kScale;
+    g.unit = 1.f / kScale;
     float* const planes = reinterpret_cast<float*>(at);
     for (int k = 0; k < steps; ++k) {
       const int kept = steps < kLoSteps ? steps : kLoSteps;
       g.x = x[k & 1]; g.y = x[~k & 1];
       g.planes = planes;
       if (k == 0 && narrow_gram(st, g)) return SL_EHIP;
-      if (narrow_join(st, planes, A, g.M, g.groups, L, kScale)) return SL_EHIP;
+      if (narrow_join(st, planes, A, g.M, g.groups, L, 1.f / kScale)) return SL_EHIP;
       g.planes = k + 1 < steps ? planes : nullptr;
       g.lo = k < kept ? lo : nullptr;
       g.ylo = k + 1 < kept ? lo : nullptr;
