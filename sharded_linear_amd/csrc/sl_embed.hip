@@ -17,7 +17,7 @@
 //    in fp32 registers and writes each finished run of equal ids to main_grad; a run that crosses a
 //    chunk's border goes to one of the chunk's two planes of partial sums.
 //  * Join.  The chunks in which a crossing run begins are listed as the sums find them (the list's order is not fixed, and
-//    no result depends on it); a workgroup adds the planes of such a run, 8 waves a contiguous part each, in order.
+//    no result depends on it); a workgroup adds the planes of such a run, 4 waves a contiguous part each, in order.
 // Up to kFewTokens tokens one kernel does it all: a workgroup for each place whose id no earlier place has.
 #include <hip/hip_runtime.h>
 
@@ -284,8 +284,8 @@ __global__ void __launch_bounds__(256) embed_sums(const uint4* __restrict__ dY, 
   }
 }
 
-constexpr int kJoinWaves = 8;
-constexpr int64_t kJoinBlocks = 1024;
+constexpr int kJoinWaves = 4;              // most runs have one or two planes: few waves to each, and many at once
+constexpr int64_t kJoinBlocks = 2048;      // 8 a CU
 
 // The runs that cross chunks: planes 2c + 1 (begins in chunk c) and 2k (goes on in chunk k > c).  Workgroups walk the
 // list of (run, 512 columns).
@@ -293,26 +293,19 @@ __global__ void __launch_bounds__(kJoinWaves * 64) embed_join(float* __restrict_
                                                               const int* __restrict__ key, const float* __restrict__ part,
                                                               int64_t H, int slices, float scale) {
   __shared__ f32x8 sums[kJoinWaves][64];
-  __shared__ int last;
   const int64_t n = head[0], chunks = (n + kChunk - 1) / kChunk, items = int64_t(head[1]) * slices;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   for (int64_t x = blockIdx.x; x < items; x += gridDim.x) {
     const int64_t c = cross[x / slices];
     const int k = key[(c + 1) * kChunk];
-    // chunks c + 1 .. last hold the rest: the first chunk that does not begin with k ends the search
-    int64_t from = c + 2;
-    for (;; from += kJoinWaves * 64) {
-      if (threadIdx.x == 0) last = 0x7fffffff;
-      __syncthreads();
-      const int64_t y = from + threadIdx.x;
-      if (y >= chunks || key[y * kChunk] != k) atomicMin(&last, int(threadIdx.x));
-      __syncthreads();
-      const int found = last;
-      __syncthreads();
-      if (found != 0x7fffffff) {
-        from += found - 1;
-        break;
-      }
+    // Chunks c + 1 .. from hold the rest.  The chunks that begin with k follow each other, so 64 are asked at a time, in steps
+    // that grow until one does not and shrink again.
+    int64_t from = c + 1;
+    for (int64_t step = 1; step > 0;) {
+      const int64_t y = from + (lane + 1) * step;
+      const uint64_t past = __ballot(y >= chunks || key[y * kChunk] != k);
+      from += step * (past ? __builtin_ctzll(past) : 64);
+      step = past ? step / 64 : step * 64;
     }
     const int64_t col = (x % slices * 64 + lane) * 8;
     const int64_t per = (from - c + kJoinWaves - 1) / kJoinWaves;

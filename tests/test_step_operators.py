@@ -200,6 +200,7 @@ def test_norm_past_32_bits():
 
 
 @pytest.mark.gpu
+@pytest.mark.filterwarnings("ignore:The CUDA Graph is empty")
 def test_captured_gradients():
     """Forward and gradients of all three autograd functions in a captured graph.  While an eager graph of the same leaves
     lives, whose accumulators belong to its stream, the capture is refused."""
