@@ -168,14 +168,10 @@ __device__ __forceinline__ void load_pre(i32x4 rs, char* lds, int wave, const ui
 // MF selects the matrix instruction: 32 for v_mfma_f32_32x32x16_bf16 (k16 steps, 32x32 blocks),
 // 16 for v_mfma_f32_16x16x32_bf16 (k32 steps, 16x16 blocks).  Both run at the same rate per clock,
 // but the 16x16 form draws less power, so the part holds a higher clock under it.
-//
-// HALF takes both operands as fp16 instead of bf16 (16x16 blocks only).
-template <bool A_KM_, bool B_KM_, bool ACC, int S_, int WGM, int WGN_, int BK_, int BN_ = 256, int MF_ = 32, int BM_ = 256,
-          bool HALF_ = false>
+template <bool A_KM_, bool B_KM_, bool ACC, int S_, int WGM, int WGN_, int BK_, int BN_ = 256, int MF_ = 32, int BM_ = 256>
 struct G4 {
-  static constexpr bool A_KM = A_KM_, B_KM = B_KM_, HALF = HALF_;
+  static constexpr bool A_KM = A_KM_, B_KM = B_KM_;
   static constexpr int S = S_, WGN = WGN_, MF = MF_;
-  static_assert(!HALF || MF == 16, "fp16 operands run on the 16x16x32 instruction");
   static constexpr int BM = BM_, BN = BN_, BK = BK_, WAVES = WGM * WGN, WM = BM / WGM, WN = BN / WGN;
   static constexpr int TM = WM / MF, TN = WN / MF;
   static constexpr int KS = 512 / MF;                   // k per MFMA step
@@ -243,12 +239,6 @@ __device__ __forceinline__ bf16x8 lds_rd_tr(uint32_t addr) {
 
 template <int N>
 __device__ __forceinline__ void asm_wait_vm() { asm volatile("s_waitcnt vmcnt(%0)" : : "i"(N) : "memory"); }
-
-template <bool HALF>
-__device__ __forceinline__ f32x4v mfma16(bf16x8 b, bf16x8 a, f32x4v c) {
-  if constexpr (HALF) return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, b), __builtin_bit_cast(f16x8, a), c, 0, 0, 0);
-  else return __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, a, c, 0, 0, 0);
-}
 
 // acc = the product of rows m0 .. of A and n0 .. of B over the k tiles kt0 .. kt0 + nk - 1 (at least S of them).
 // G provides a, b, a_bytes, b_bytes, lda, ldb, M, N and K.  On return loads may be in flight and other waves may
@@ -381,7 +371,7 @@ __device__ __forceinline__ void gemm4_core(const G& g, char* smem, int lane, int
       if constexpr (MF == 32)
         acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[cur][j], fa[cur][i], acc[i][j], 0, 0, 0);
       else
-        acc[i][j] = mfma16<P::HALF>(fb[cur][j], fa[cur][i], acc[i][j]);
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[cur][j], fa[cur][i], acc[i][j], 0, 0, 0);
       constexpr int NQ = TM * TN, NRD = NR < NM ? NR : NM, NL = NM - NRD;
       constexpr int RQ = NQ * 3 / 4 > 0 ? NQ * 3 / 4 : 1;
       constexpr int rlo = q < RQ ? q * NRD / RQ : NRD, rhi = q < RQ ? (q + 1) * NRD / RQ : NRD;

@@ -295,18 +295,19 @@ __global__ void __launch_bounds__(P::WAVES * 64, OCC) half_gemm(HalfArgs g) {
   };
 
   f32x4v acc[TM][TN];
-  bf16x8 fa[2][TM], fb[2][TN];
+  f16x8 fa[2][TM], fb[2][TN];
   auto clear = [&]() {
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
       for (int j = 0; j < TN; ++j) acc[i][j] = f32x4v{0.f, 0.f, 0.f, 0.f};
   };
+  auto half8 = [](bf16x8 v) __attribute__((always_inline)) { return __builtin_bit_cast(f16x8, v); };    // 16 bits either way
   auto read_one = [&](auto ic_m, auto ic_to, auto ic_ks, uint32_t base) {
     constexpr int m = decltype(ic_m)::value, to = decltype(ic_to)::value, ks = decltype(ic_ks)::value;
-    if constexpr (m < TM) fa[to][m] = lds_rd128<m * 16 * OA::kRowBytes>((base + ofa) ^ (64 * ks));
-    else if constexpr (B_KM) fb[to][m - TM] = lds_rd128<(m - TM) * 16 * OB::kRowBytes>((base + ofb[0]) ^ (64 * ks));
-    else fb[to][m - TM] = lds_rd_tr<ks * KS * OB::kRowBytes, (ks * KS + 4) * OB::kRowBytes>(base + ofb[m - TM]);
+    if constexpr (m < TM) fa[to][m] = half8(lds_rd128<m * 16 * OA::kRowBytes>((base + ofa) ^ (64 * ks)));
+    else if constexpr (B_KM) fb[to][m - TM] = half8(lds_rd128<(m - TM) * 16 * OB::kRowBytes>((base + ofb[0]) ^ (64 * ks)));
+    else fb[to][m - TM] = half8(lds_rd_tr<ks * KS * OB::kRowBytes, (ks * KS + 4) * OB::kRowBytes>(base + ofb[m - TM]));
   };
   // One step: the products on buffer CUR, with the next step's fragment reads over the first three quarters of them and,
   // in a stage's second step, the loads spread over all.
@@ -314,7 +315,7 @@ __global__ void __launch_bounds__(P::WAVES * 64, OCC) half_gemm(HalfArgs g) {
     constexpr int cur = decltype(ic_cur)::value, NL = cur ? LPS : 0, NQ = TM * TN, RQ = NQ * 3 / 4;
     static_for<NQ>([&](auto qc) {
       constexpr int q = decltype(qc)::value, i = q / TN, j = (i & 1) ? TN - 1 - q % TN : q % TN;
-      acc[i][j] = mfma16<true>(fb[cur][j], fa[cur][i], acc[i][j]);
+      acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fb[cur][j], fa[cur][i], acc[i][j], 0, 0, 0);
       constexpr int rlo = q < RQ ? q * NR / RQ : NR, rhi = q < RQ ? (q + 1) * NR / RQ : NR;
       static_for<rhi - rlo>([&](auto mc) { read_one(ic<rlo + decltype(mc)::value>{}, ic<cur ^ 1>{}, ic<cur ^ 1>{}, rbase); });
       constexpr int llo = (2 * q * NL + NQ) / (2 * NQ), lhi = (2 * (q + 1) * NL + NQ) / (2 * NQ);
@@ -420,8 +421,8 @@ __global__ void __launch_bounds__(64) half_join(HalfArgs g) {
 // ---- host ----------------------------------------------------------------------------------------
 
 // 256x256 tiles of 8 waves, one workgroup a CU, and 128x128 tiles of 4 waves, two a CU.
-template <bool B_KM> using Big = G4<true, B_KM, false, 2, 2, 4, 64, 256, 16, 256, true>;
-template <bool B_KM> using Small = G4<true, B_KM, false, 2, 2, 2, 64, 128, 16, 128, true>;
+template <bool B_KM> using Big = G4<true, B_KM, false, 2, 2, 4, 64, 256, 16, 256>;
+template <bool B_KM> using Small = G4<true, B_KM, false, 2, 2, 2, 64, 128, 16, 128>;
 
 // A product: `big` tiles of 256x256, from the first on, and `small` tiles of 128x128 for the rest, or for all of it (big ==
 // 0); of these `rest` are split in `splits` parts.
