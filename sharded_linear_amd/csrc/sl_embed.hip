@@ -18,7 +18,10 @@
 //    chunk's border goes to one of the chunk's two planes of partial sums.
 //  * Join.  The chunks in which a crossing run begins are listed as the sums find them (the list's order is not fixed, and
 //    no result depends on it); a workgroup adds the planes of such a run, 4 waves a contiguous part each, in order.
-// Up to kFewTokens tokens one kernel does it all: a workgroup for each place whose id no earlier place has.
+// 8192 tokens, half of them here, rows of 2048: sort 8.3 us, sums 13.6 (53 MB, 3.9 TB/s), join 5.0; the first and the last are
+// chains of short loads behind each other, not bytes.
+// Up to kFewTokens tokens one kernel does it all: a workgroup for each place whose id no earlier place has (1013 tokens, rows of
+// 1032: 6.1 us, of which the walk over the ids is most).
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -47,8 +50,10 @@ __device__ __forceinline__ int64_t local_row(const I* ids, int64_t t, int64_t st
 }
 
 // ---- lookup --------------------------------------------------------------------------------------
-// LPR lanes to a row, so that narrow rows leave no lane idle; a lane's chunks of a row are all loaded
-// before the first is stored, four at a time.
+// LPR lanes to a row, so that a lane has four chunks of it where the row is long enough; they are all loaded before the first is
+// stored.  8192 tokens, half of them here, in us with 8, 16, 32 and 64 lanes: rows of 2048 elements 11.6, 11.2, 10.2, 10.0; of 512
+// 5.4, 5.2, 5.3, 5.8; of 256 4.4, 4.7, 4.7, 5.0.  Bound by HBM (33.5 MB written, up to as many read) for wide rows, by the launch
+// for narrow ones.
 template <int LPR, typename I>
 __global__ void __launch_bounds__(256) embed_lookup(const I* __restrict__ ids, const uint4* __restrict__ W, uint4* __restrict__ Y,
                                                     int64_t T, int64_t V, int chunks, int64_t start, float scale) {
@@ -74,8 +79,13 @@ __global__ void __launch_bounds__(256) embed_lookup(const I* __restrict__ ids, c
 
 constexpr int kSortWaves = 16;
 constexpr int kSortBins = 1000;           // most ids of one bucket, kSortWaves counters each in LDS
-constexpr int kChunk = 8;                // sorted places to a workgroup of the sums
-constexpr int kFewTokens = 1024;          // tokens up to which one kernel does it all
+// Sorted places to a workgroup of the sums, its rows all in flight: 4 took 29.5 us, 16 58.8 where 8 took 28.7 (8192 tokens, rows
+// of 2048).
+constexpr int kChunk = 8;
+// Tokens up to which one kernel does it all.  In us, one kernel against three: 1024 tokens of a uniform vocabulary 8.1 and 13.8,
+// 2048 12.7 and 16.3; but a frequent token's rows are one workgroup's there, and of skewed ids 1024 take 8.3 and 11.6, 1500
+// 17.4 and 13.3.
+constexpr int kFewTokens = 1024;
 
 struct EmbedPlan {
   int bits;               // log2 of the number of buckets
@@ -430,7 +440,7 @@ extern "C" int sl_embedding_fwd(void* stream, const void* ids, int32_t ids_bytes
   if (!aligned16(W) || !aligned16(Y)) return SL_EALIGN;
   const hipStream_t st = static_cast<hipStream_t>(stream);
   const int chunks = int(H / 8);
-  (chunks > 32 ? launch_lookup<64> : chunks > 16 ? launch_lookup<32> : chunks > 8 ? launch_lookup<16> : launch_lookup<8>)(
+  (chunks > 128 ? launch_lookup<64> : chunks > 64 ? launch_lookup<32> : chunks > 32 ? launch_lookup<16> : launch_lookup<8>)(
       st, ids, ids_bytes, W, Y, T, V, chunks, vocab_start, scale);
   return hipGetLastError() == hipSuccess ? SL_OK : SL_EHIP;
 }

@@ -15,7 +15,9 @@
 //
 // Around the products: one pass for the momentum and the norm (sums of squares in 64 bits: any finite gradient has a
 // norm), one that scales, transposes a tall matrix and pads to multiples of 128 with zeros, and one that writes the
-// result or the weight.  The three are bound by HBM.
+// result or the weight.  The three are bound by HBM: for 2 x [4096, 5504] 91 us (541 MB, 6.0 TB/s), 101 (496 MB, 4.9) and 46
+// (271 MB, 5.9) of 3250.  G and M are read twice, for the norm has to be known before the first element of X, and U in fp32
+// would be as many bytes.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
