@@ -4,13 +4,18 @@
 //   g = w * dY                  dX = dresidual + rstd * (g - h * rstd^2 * mean(g * h))
 //   w_grad += sum over rows of dY * h * rstd
 //
-// y is rounded once: to bf16, or from fp32 straight to MXFP8 (the OCP MX rule of the quantiser in
+// y is rounded to bf16, or straight to MXFP8 (the OCP MX rule of the quantiser in
 // sl_quant.hip), rowwise and columnwise, as the products of the all-MXFP8 step read it.  The norm is
 // of the rounded h, which is what the next layer adds to and what the gradient reads again.
 //
+// MXFP8 has borders: where a block's largest magnitude lies within an error of a power of two, the whole block is encoded with
+// another scale.  With y in plain fp32 that befell one block in some ten million, so the forward's sums end in 64 bits, rstd is
+// held in two floats, and h * w (exact in fp32) times rstd is rounded to odd: the code is then that of the exact product, up to
+// fp32 sums of a lane's few squares.  That takes 1.6 us of 22 in the rowwise kernel and 2 of 15 in the columnwise one.
+//
 // Every kernel here is bound by HBM, so each row passes through registers once: TPR threads hold a
-// row, NC chunks of 8 elements a thread.  Means are fp32 sums: of each of a lane's 8 columns in order, then of those, of the
-// lanes by DPP and half-wave swaps, and of the waves in order.
+// row, NC chunks of 8 elements a thread.  Means are fp32 sums of each of a lane's 8 columns in order, then of those; then
+// of the lanes by DPP and half-wave swaps, and of the waves in order (in 64 bits in the forward).
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -32,30 +37,48 @@ template <int CTRL>
 __device__ __forceinline__ float add_dpp(float x) {
   return x + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xF, 0xF, false));
 }
+template <int CTRL>
+__device__ __forceinline__ double add_dpp(double x) {
+  const int2 v = __builtin_bit_cast(int2, x);
+  return x + __builtin_bit_cast(double, make_int2(__builtin_amdgcn_update_dpp(0, v.x, CTRL, 0xF, 0xF, false),
+                                                  __builtin_amdgcn_update_dpp(0, v.y, CTRL, 0xF, 0xF, false)));
+}
+
+// Both halves' values of a swap of 16- or 32-lane halves, added.
+template <int LANES>
+__device__ __forceinline__ float add_halves(float x) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, x);
+  const auto r = LANES == 16 ? __builtin_amdgcn_permlane16_swap(b, b, false, false) : __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  return __builtin_bit_cast(float, uint32_t(r[0])) + __builtin_bit_cast(float, uint32_t(r[1]));
+}
+template <int LANES>
+__device__ __forceinline__ double add_halves(double x) {
+  const uint2 b = __builtin_bit_cast(uint2, x);
+  const auto r = LANES == 16 ? __builtin_amdgcn_permlane16_swap(b.x, b.x, false, false) : __builtin_amdgcn_permlane32_swap(b.x, b.x, false, false);
+  const auto s = LANES == 16 ? __builtin_amdgcn_permlane16_swap(b.y, b.y, false, false) : __builtin_amdgcn_permlane32_swap(b.y, b.y, false, false);
+  return __builtin_bit_cast(double, make_uint2(r[0], s[0])) + __builtin_bit_cast(double, make_uint2(r[1], s[1]));
+}
 
 // Sum over the 64 lanes, in every lane: pairs, quads, 8 and 16 lanes by DPP, then the 16- and 32-lane halves.
-__device__ __forceinline__ float wave_sum(float x) {
+template <typename S>
+__device__ __forceinline__ S wave_sum(S x) {
   x = add_dpp<0xB1>(x);     // quad_perm [1,0,3,2]
   x = add_dpp<0x4E>(x);     // quad_perm [2,3,0,1]
   x = add_dpp<0x141>(x);    // row_half_mirror
   x = add_dpp<0x140>(x);    // row_mirror
-  uint32_t b = __builtin_bit_cast(uint32_t, x);
-  auto r = __builtin_amdgcn_permlane16_swap(b, b, false, false);
-  b = __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, uint32_t(r[0])) + __builtin_bit_cast(float, uint32_t(r[1])));
-  r = __builtin_amdgcn_permlane32_swap(b, b, false, false);
-  return __builtin_bit_cast(float, uint32_t(r[0])) + __builtin_bit_cast(float, uint32_t(r[1]));
+  return add_halves<32>(add_halves<16>(x));
 }
 
 __device__ __forceinline__ float fold(f32x8 v) { return ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7])); }
 
 // Sum over the TPR threads of a row (a wave, or a whole workgroup).  `turn` alternates between calls, so that one
 // barrier a call is enough.
-template <int TPR>
-__device__ __forceinline__ float row_sum(float x, float* red, int turn) {
+template <int TPR, typename S>
+__device__ __forceinline__ S row_sum(S x, S* red, int turn) {
   x = wave_sum(x);
   if constexpr (TPR > 64) {
     constexpr int W = TPR / 64;
-    float* r = red + turn * W;
+    S* r = red + turn * W;
     if ((threadIdx.x & 63) == 0) r[threadIdx.x >> 6] = x;
     __syncthreads();
     x = r[0];
@@ -65,11 +88,21 @@ __device__ __forceinline__ float row_sum(float x, float* red, int turn) {
   return x;
 }
 
-// x^-1/2 to about half a unit in the last place: one correction with the residual 1 - x r^2 in exact products.
-__device__ __forceinline__ float inverse_root(float x) {
-  const float r = 1.0f / sqrtf(x), t = x * r, off = fmaf(-t, r, 1.0f) - fmaf(x, r, -t) * r;
-  const float c = fmaf(0.5f * r, off, r);
-  return c - c == 0.f ? c : r;                 // zeros, infinities and NaN as they come
+// x^-1/2 as the nearest float and what it leaves: two terms of the series in 1 - x r^2 from the fp32 root r.
+__device__ __forceinline__ float2 inverse_root(double x) {
+  const float r = 1.0f / sqrtf(float(x));
+  const double off = fma(-x * r, double(r), 1.0), c = r + r * off * fma(0.375, off, 0.5);
+  const float hi = float(c);
+  return hi - hi == 0.f ? make_float2(hi, float(c - hi)) : make_float2(r, 0.f);      // zeros, infinities and NaN as they come
+}
+
+// p times the two floats of r, rounded to odd: the last bit is set where anything was left, so that a later rounding to fewer bits
+// is that of the exact product.  Only where the last 19 bits of p r.x are zeros can that make a difference: borders of E4M3's four
+// bits, subnormal codes' among them, and powers of two have no bits there.
+__device__ __forceinline__ float odd_product(float p, float2 r) {
+  const float y = p * r.x, left = fmaf(p, r.y, fmaf(p, r.x, -y));
+  const uint32_t b = __float_as_uint(y), away = (__float_as_uint(left) ^ b) >> 31 ? ~0u : 1u;
+  return __uint_as_float(left != 0.f && left - left == 0.f && !(b & 1) ? b + away : b);
 }
 
 // E8M0 byte of a block whose largest magnitude has the fp32 bits `amax`: floor(log2 amax) - 8, biased; 255 (NaN) for
@@ -95,6 +128,10 @@ __device__ __forceinline__ uint32_t mx8_codes(float a, float b, float c, float d
 
 __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 
+// Below kBorder for a magnitude other than zero whose last 19 bits are zeros (zeros of either sign are frequent, and no border).
+constexpr uint32_t kBorder = 0x1000;
+__device__ __forceinline__ uint32_t border_key(uint32_t magnitude) { return __builtin_amdgcn_alignbit(magnitude, magnitude, 19) - 1; }
+
 enum Out { kBF16, kRows, kNothing };
 
 struct FwdArgs {
@@ -102,17 +139,18 @@ struct FwdArgs {
   uint4 *y, *h;
   uint2* q;
   uint8_t* s;
-  float* rstd;
+  float *rstd, *left;  // left: what the rounding of rstd left, or null
   int64_t T;
   int chunks;          // H / 8
-  float h_float, eps;
+  double h_inv;        // 1 / H
+  float eps;
 };
 
-// With a residual, rowwise MXFP8: [8192, 2048] 20.8 us, 118 MB, 5.7 TB/s, as a copy; one row of 4096 2.6 us, the launch.
+// With a residual, rowwise MXFP8: [8192, 2048] 22.1 us, 118 MB, 5.3 TB/s, as a copy; one row of 4096 2.7 us, the launch.
 template <int TPR, int NC, bool RES, int OUT>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_fwd(FwdArgs g) {
   constexpr int ROWS = TPR < 256 ? 256 / TPR : 1;
-  __shared__ float red[TPR > 64 ? 2 * TPR / 64 : 1];
+  __shared__ double red[TPR > 64 ? 2 * TPR / 64 : 1];
   const int lane = threadIdx.x % TPR;
   uint4 w[NC];
   if constexpr (OUT != kNothing)
@@ -142,16 +180,27 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_fwd(FwdArgs g) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) squares[e] = fmaf(a[e], a[e], squares[e]);
     }
-    const float rstd = inverse_root(row_sum<TPR>(fold(squares), red, turn) / g.h_float + g.eps);
-    if (lane == 0) g.rstd[t] = rstd;
+    const float2 rstd = inverse_root(row_sum<TPR>(double(fold(squares)), red, turn) * g.h_inv + g.eps);
+    if (lane == 0) {
+      g.rstd[t] = rstd.x;
+      if (g.left) g.left[t] = rstd.y;
+    }
     if constexpr (OUT != kNothing) {
 #pragma unroll
       for (int j = 0; j < NC; ++j) {
         const int c = lane + j * TPR;
-        const f32x8 y = widen(v[j]) * widen(w[j]) * rstd;        // the first product is exact
+        f32x8 y = widen(v[j]) * widen(w[j]);                     // exact
         if constexpr (OUT == kBF16) {
-          if (c < g.chunks) g.y[t * g.chunks + c] = narrow(y);
+          if (c < g.chunks) g.y[t * g.chunks + c] = narrow(y * rstd.x);
         } else {
+          const f32x8 p = y;
+          y = p * rstd.x;
+          uint32_t border = ~0u;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) border = min(border, border_key(magnitude(y[e])));
+          if (border < kBorder)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = odd_product(p[e], rstd);
           // a block is the 4 chunks of a quad of lanes (chunks % 4 == 0: whole quads are in range)
           uint32_t amax = 0;
 #pragma unroll
@@ -171,14 +220,14 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_fwd(FwdArgs g) {
 // ---- columnwise MXFP8 copy -----------------------------------------------------------------------
 // One workgroup takes a 128 x 128 tile of h: rows of 16-byte chunks into LDS, from which each thread reads two blocks
 // of 32 rows down a column by transposing reads, scales them (rstd by row, w by column) and encodes them; codes leave
-// as whole 128-byte lines of the transposed copy.  The LDS layout is the quantiser's (sl_quant.hip).  [8192, 2048]: 13.1 us,
-// 51 MB, 3.9 TB/s; rstd needs whole rows before the first column, so h is read again here (from the last-level cache).
+// as whole 128-byte lines of the transposed copy.  The LDS layout is the quantiser's (sl_quant.hip).  [8192, 2048]: 15.1 us,
+// 51 MB, 3.4 TB/s; rstd needs whole rows before the first column, so h is read again here (from the last-level cache).
 constexpr int kTile = 128, kStride = kTile + 16;
 
 __global__ void __launch_bounds__(256) norm_cols(const uint16_t* __restrict__ h, const uint16_t* __restrict__ w, const float* __restrict__ rstd,
-                                                 int64_t R, int64_t C, uint8_t* __restrict__ qc, uint8_t* __restrict__ sc) {
+                                                 const float* __restrict__ left, int64_t R, int64_t C, uint8_t* __restrict__ qc, uint8_t* __restrict__ sc) {
   __shared__ __attribute__((aligned(16))) uint16_t tile[kTile * kStride];
-  __shared__ float inv[kTile];
+  __shared__ float inv[kTile], left_lds[kTile];
   uint8_t* const qbuf = reinterpret_cast<uint8_t*>(tile);
   uint8_t* const sbuf = qbuf + kTile * kTile;
   const int64_t ntc = (C + kTile - 1) / kTile;
@@ -190,7 +239,10 @@ __global__ void __launch_bounds__(256) norm_cols(const uint16_t* __restrict__ h,
     const int64_t gr = r0 + (t >> 4) + 16 * k, gc = c0 + 8 * ch;
     raw[k] = (gr < R && gc < C) ? *reinterpret_cast<const uint4*>(h + gr * C + gc) : make_uint4(0, 0, 0, 0);
   }
-  if (t < kTile) inv[t] = r0 + t < R ? rstd[r0 + t] : 0.f;
+  if (t < kTile) {
+    inv[t] = r0 + t < R ? rstd[r0 + t] : 0.f;
+    left_lds[t] = r0 + t < R ? left[r0 + t] : 0.f;
+  }
 #pragma unroll
   for (int k = 0; k < 8; ++k) reinterpret_cast<uint4*>(tile + ((t >> 4) + 16 * k) * kStride)[ch] = raw[k];
   __syncthreads();
@@ -205,7 +257,7 @@ __global__ void __launch_bounds__(256) norm_cols(const uint16_t* __restrict__ h,
     const int col4 = ((idx & (kTile - 1)) & ~15) + 4 * qc4;
     const uint32_t a0 = sl2::lds_addr(tile + (rb * 32 + jr) * kStride + col4);
     float y[32];
-    uint32_t amax = 0;
+    uint32_t amax = 0, border = ~0u;
 #pragma unroll
     for (int r4 = 0; r4 < 8; ++r4) {
       const sl2::i16x4q v = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
@@ -214,7 +266,18 @@ __global__ void __launch_bounds__(256) norm_cols(const uint16_t* __restrict__ h,
       for (int e = 0; e < 4; ++e) {
         const float x = __uint_as_float(uint32_t(uint16_t(v[e])) << 16);
         y[4 * r4 + e] = x * wc * inv[rb * 32 + 4 * r4 + e];
-        amax = max(amax, magnitude(y[4 * r4 + e]));
+        const uint32_t m = magnitude(y[4 * r4 + e]);
+        border = min(border, border_key(m));
+        amax = max(amax, m);
+      }
+    }
+    if (border < kBorder) {                   // a column's elements once more, from the tile as it stands
+      amax = 0;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const float x = __uint_as_float(uint32_t(tile[(rb * 32 + i) * kStride + (idx & (kTile - 1))]) << 16);
+        y[i] = odd_product(x * wc, make_float2(inv[rb * 32 + i], left_lds[rb * 32 + i]));
+        amax = max(amax, magnitude(y[i]));
       }
     }
     s[b] = mx8_scale(amax);
@@ -422,7 +485,7 @@ extern "C" int sl_rmsnorm_fwd(void* stream, const void* x, const void* residual,
   if (!aligned16(x) || !aligned16(residual) || !aligned16(w) || !aligned16(y) || (residual && !aligned16(h)) || reinterpret_cast<uintptr_t>(rstd) & 3u)
     return SL_EALIGN;
   FwdArgs g{static_cast<const uint4*>(x), static_cast<const uint4*>(residual), static_cast<const uint4*>(w), static_cast<uint4*>(y),
-            static_cast<uint4*>(h), nullptr, nullptr, rstd, T, int(H / 8), float(H), eps};
+            static_cast<uint4*>(h), nullptr, nullptr, rstd, nullptr, T, int(H / 8), 1.0 / double(H), eps};
   return run_fwd(static_cast<hipStream_t>(stream), g, kBF16);
 }
 
@@ -441,11 +504,11 @@ extern "C" int sl_rmsnorm_fwd_mxfp8(void* stream, const void* x, const void* res
   if (q_cols && tiles >= (int64_t(1) << 24)) return SL_ESHAPE;            // of 256 threads: a launch has fewer than 2^32
   const hipStream_t st = static_cast<hipStream_t>(stream);
   FwdArgs g{static_cast<const uint4*>(x), static_cast<const uint4*>(residual), static_cast<const uint4*>(w), nullptr, static_cast<uint4*>(h),
-            reinterpret_cast<uint2*>(q_rows), s_rows, rstd, T, int(H / 8), float(H), eps};
+            reinterpret_cast<uint2*>(q_rows), s_rows, rstd, q_cols ? rstd + T : nullptr, T, int(H / 8), 1.0 / double(H), eps};
   const int f = run_fwd(st, g, q_rows ? kRows : kNothing);
   if (f || !q_cols) return f;
   hipLaunchKernelGGL(norm_cols, dim3(unsigned(tiles)), dim3(256), 0, st, static_cast<const uint16_t*>(residual ? h : x),
-                     static_cast<const uint16_t*>(w), rstd, T, H, q_cols, s_cols);
+                     static_cast<const uint16_t*>(w), rstd, rstd + T, T, H, q_cols, s_cols);
   return hipGetLastError() == hipSuccess ? SL_OK : SL_EHIP;
 }
 

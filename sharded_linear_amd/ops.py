@@ -621,8 +621,8 @@ def sl_embedding_wgrad_accum(ids, dY, main_grad, vocab_start=0, scale=1.0, works
 
 # ---- root-mean-square norm ----------------------------------------------------------------------
 
-def _norm_inputs(x, w, residual, h):
-    """Checks a norm's inputs; returns (device, T, H, h, rstd), h being x itself without a residual."""
+def _norm_inputs(x, w, residual, h, parts=1):
+    """Checks a norm's inputs; returns (device, T, H, h, rstd[parts * T]), h being x itself without a residual."""
     dev = _device(x)
     T, H = _want_matrix(x, "x", BF16, dev)
     _want(w, "w", BF16, (H,), dev)
@@ -636,7 +636,7 @@ def _norm_inputs(x, w, residual, h):
             h = _new(dev, BF16, T, H)
         else:
             _want(h, "h", BF16, (T, H), dev)
-    return dev, T, H, h, _new(dev, F32, T)
+    return dev, T, H, h, _new(dev, F32, parts * T)
 
 
 def sl_rmsnorm_fwd(x, w, eps, residual=None, y=None, h=None):
@@ -653,10 +653,12 @@ def sl_rmsnorm_fwd(x, w, eps, residual=None, y=None, h=None):
 
 
 def sl_rmsnorm_fwd_mxfp8(x, w, eps, residual=None, rows=True, cols=True, out=None, h=None):
-    """sl_rmsnorm_fwd with y in MXFP8, rounded once from fp32: returns (q_rows, s_rows, q_cols, s_cols, h, rstd); a copy not
+    """sl_rmsnorm_fwd with y in MXFP8, rounded once: returns (q_rows, s_rows, q_cols, s_cols, h, rstd); a copy not
     asked for is None.  The copies are laid out as sl_mxfp8_quantize's: rowwise [T, H] + [T, H/32] (H % 32 == 0), columnwise,
     stored transposed, [H, T] + [H, T/32] (T % 32 == 0).  ``out`` may supply the four tensors."""
-    dev, T, H, h, rstd = _norm_inputs(x, w, residual, h)
+    if out is not None:
+        cols = out[2] is not None
+    dev, T, H, h, rstd = _norm_inputs(x, w, residual, h, 2 if cols else 1)
     if out is None:
         qr, sr = (_new(dev, U8, T, H), _new(dev, U8, T, H // 32)) if rows else (None, None)
         qc, sc = (_new(dev, U8, H, T), _new(dev, U8, H, T // 32)) if cols else (None, None)
@@ -670,7 +672,7 @@ def sl_rmsnorm_fwd_mxfp8(x, w, eps, residual=None, rows=True, cols=True, out=Non
             _want(sc, "s_cols", U8, (H, T // 32), dev)
     _launch("sl_rmsnorm_fwd_mxfp8", dev, _addr(x), _addr(residual), _addr(w), eps, _addr(qr), _addr(sr), _addr(qc), _addr(sc),
             None if residual is None else _addr(h), _addr(rstd), T, H)
-    return qr, sr, qc, sc, h, rstd
+    return qr, sr, qc, sc, h, rstd[:T] if cols else rstd
 
 
 def sl_rmsnorm_bwd_workspace_bytes(T: int, H: int) -> int:

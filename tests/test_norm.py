@@ -213,6 +213,23 @@ def test_forward_mxfp8(T, H, residual):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,H", [(2048, 2048), (64, 4096), (96, 544)])
+def test_mxfp8_codes_are_those_of_the_exact_product(T, H):
+    """Rows of small integers: sums of squares are exact, so rstd in two floats is off by less than 2^-45 and each code has to be the
+    exact product's."""
+    say(f"case norm mxfp8 exact codes T={T} H={H}")
+    g = _gen(T)
+    x = torch.randint(-15, 16, (T, H), generator=g, device="cuda").to(BF16)
+    w = (1 + 0.2 * torch.randn(H, generator=g, device="cuda")).to(BF16)
+    qr, sr, qc, sc, _, rstd = sl.sl_rmsnorm_fwd_mxfp8(x, w, 2.0 ** -17)
+    inv = 1 / torch.sqrt(x.double().square().mean(1) + 2.0 ** -17)
+    assert torch.equal(rstd, inv.float())
+    y = x.double() * w.double() * inv[:, None]
+    _check_mx(qr, sr, y, 2.0 ** -45)
+    _check_mx(qc, sc, y.t().contiguous(), 2.0 ** -45)
+
+
+@pytest.mark.gpu
 def test_columnwise_copy_alone_takes_any_width():
     say("case norm mxfp8 columns of width 1032")
     x, r, w = _inputs(96, 1032, True, 5)
