@@ -11,8 +11,9 @@
 // What bounds it: a 64 k stage of 256 x 256 takes 1.45 us on all CUs, 1.48 PFLOP/s, which is what the power limit leaves a large
 // product here (the library's reaches 1.47 to 1.51).  On top of it come 15 us a round: 3.4 from the start to the first data, the
 // results' loads and stores, and the drain at the end; two accumulator tiles, which would let the results leave under the next
-// tile's products, do not fit into the registers.  P X of 2 x [4096, 5504]: 291 us without what roundings left (1.27 PFLOP/s,
-// matrix units 0.67 busy), 318 with it read and written; of 16 x [1536, 2048] 140 and 165 in three rounds.
+// tile's products, do not fit into the registers.  P X of 2 x [4096, 5504]: 279 to 291 us without what roundings left (1.27 to
+// 1.32 PFLOP/s, matrix units 0.66 busy), 307 to 318 with it read and written; of 16 x [1536, 2048] 137 to 140 and 162 to 165 in
+// three rounds.
 //
 // Tiles of 256 x 256 are dealt out in whole rounds of the chip; what remains, or the whole of a small product, goes to
 // tiles of 128 x 128 in a launch of its own, and where its last round would leave places idle, sums are split into fp32
