@@ -93,7 +93,8 @@ struct EmbedPlan {
   int64_t cross_off, key_off, part_off, bytes;
 };
 
-// Buckets: 256, one workgroup a CU, or as many as leave kSortBins ids to each.
+// Buckets: 256, one workgroup a CU (a call of 8192 tokens, rows of 2048: 24.8 us; 128 buckets 27.1, 512 25.8), or as many as
+// leave kSortBins ids to each.
 EmbedPlan embed_plan(int64_t T, int64_t V, int64_t H) {
   EmbedPlan p{};
   if (T <= kFewTokens) return p;
