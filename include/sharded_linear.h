@@ -371,7 +371,7 @@ int sl_embedding_wgrad_accum(void* stream, const void* ids, int32_t ids_bytes, c
  *   h = bf16(x + residual) (x itself without one)    rstd[t] = (mean(h[t]^2) + eps)^-1/2 (fp32)
  *   y = h * rstd * w
  * sl_rmsnorm_fwd writes y in bf16.  sl_rmsnorm_fwd_mxfp8 writes it in MXFP8 by the rule of
- * sl_mxfp8_quantize, from the exact product of h, w and rstd in two floats (no rounding between): rowwise codes q_rows[T, H] +
+ * sl_mxfp8_quantize, from the product of h, w and rstd in two floats as if it were exact (to 2^-100; below, from its fp32 rounding): rowwise codes q_rows[T, H] +
  * s_rows[T, H/32] (H % 32 == 0) and/or columnwise ones, stored transposed, q_cols[H, T] + s_cols[H, T/32]
  * (T % 32 == 0); a NULL pair is skipped.  A block with an infinity or a NaN has scale 255 (NaN) and codes 0.
  * Both write h (only with a residual; else h may be NULL) and rstd, which the gradient reads; with q_cols rstd has 2 T

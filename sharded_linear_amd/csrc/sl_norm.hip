@@ -10,8 +10,8 @@
 //
 // MXFP8 has borders: where a block's largest magnitude lies within an error of a power of two, the whole block is encoded with
 // another scale.  With y in plain fp32 that befell one block in some ten million, so the forward's sums end in 64 bits, rstd is
-// held in two floats, and h * w (exact in fp32) times rstd is rounded to odd: the code is then that of the exact product, up to
-// fp32 sums of a lane's few squares.  That takes 1.6 us of 22 in the rowwise kernel and 2 of 15 in the columnwise one.
+// held in two floats (to 2^-47), and h * w (exact in fp32) times rstd is rounded to odd: the code is then that of h * w by this
+// rstd, which is off by the fp32 sums of a lane's few squares.  (Of results below 2^-100, fp32 cannot hold what a product leaves.)
 //
 // Every kernel here is bound by HBM, so each row passes through registers once: TPR threads hold a
 // row, NC chunks of 8 elements a thread.  Means are fp32 sums of each of a lane's 8 columns in order, then of those; then
@@ -97,12 +97,13 @@ __device__ __forceinline__ float2 inverse_root(double x) {
 }
 
 // p times the two floats of r, rounded to odd: the last bit is set where anything was left, so that a later rounding to fewer bits
-// is that of the exact product.  Only where the last 19 bits of p r.x are zeros can that make a difference: borders of E4M3's four
-// bits, subnormal codes' among them, and powers of two have no bits there.
+// is that of the product.  p r.x is off by up to half a unit in its last place and p r.y adds up to a whole one, so what is left is
+// added before the last bit is looked at.
 __device__ __forceinline__ float odd_product(float p, float2 r) {
-  const float y = p * r.x, left = fmaf(p, r.y, fmaf(p, r.x, -y));
-  const uint32_t b = __float_as_uint(y), away = (__float_as_uint(left) ^ b) >> 31 ? ~0u : 1u;
-  return __uint_as_float(left != 0.f && left - left == 0.f && !(b & 1) ? b + away : b);
+  const float y = p * r.x, left = fmaf(p, r.y, fmaf(p, r.x, -y)), z = y + left, rest = left - (z - y);
+  const uint32_t b = __float_as_uint(z), away = (__float_as_uint(rest) ^ b) >> 31 ? ~0u : 1u;
+  if (left == 0.f || rest - rest != 0.f) return y;     // zeros with their sign; infinities, NaN, and what would become one
+  return __uint_as_float(rest != 0.f && !(b & 1) ? b + away : b);
 }
 
 // E8M0 byte of a block whose largest magnitude has the fp32 bits `amax`: floor(log2 amax) - 8, biased; 255 (NaN) for
@@ -128,9 +129,15 @@ __device__ __forceinline__ uint32_t mx8_codes(float a, float b, float c, float d
 
 __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 
-// Below kBorder for a magnitude other than zero whose last 19 bits are zeros (zeros of either sign are frequent, and no border).
-constexpr uint32_t kBorder = 0x1000;
-__device__ __forceinline__ uint32_t border_key(uint32_t magnitude) { return __builtin_amdgcn_alignbit(magnitude, magnitude, 19) - 1; }
+// Below kBorder for a magnitude p r.x other than zero (zeros of either sign are frequent, and no border) whose odd_product may
+// lie on the other side of a border, or on it: borders of E4M3's four bits, subnormal codes' among them, and powers of two have no
+// bits in their last 19 places, and the product is less than two units in the last place from p r.x.  Of the unit above it, the
+// last 19 bits are then 0 to 2 (3 passes the comparison too).
+constexpr uint32_t kBorder = 0x7000;
+__device__ __forceinline__ uint32_t border_key(uint32_t magnitude) {
+  const uint32_t next = magnitude + 1;
+  return (__builtin_amdgcn_alignbit(next, next, 19) ^ 0x2000) - 1;
+}
 
 enum Out { kBF16, kRows, kNothing };
 

@@ -1,4 +1,7 @@
 """The root-mean-square norm with the residual's addition: refusals on the CPU, results and gradients on the GPU against 64 bits."""
+import math
+from fractions import Fraction
+
 import numpy as np
 import pytest
 import torch
@@ -467,3 +470,36 @@ def test_captured_and_replayed():
         want = work(before)
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(outs[k], want)) and torch.equal(grads[k], before)
+
+
+def _row_of_integers(h, squares, H):
+    """H integers of up to 255, h first, whose squares add up to ``squares``; zeros at the end."""
+    row, left = [h], squares - h * h
+    while left:
+        row.append(min(math.isqrt(left), 100))
+        left -= row[-1] ** 2
+    return row + [0] * (H - len(row))
+
+
+# Sums of squares S, h and w for which p = h w lies so that p rstd, S / 4096 + 2^-17 being 1 / rstd^2, is within 2^-25 of a border, and the
+# fp32 product with the rounded rstd one unit in the last place away from it: below a power of two with the product above it, and
+# above a tie of two codes with the product below it.
+@pytest.mark.gpu
+@pytest.mark.parametrize("S,h,w", [(126358, 130, 175), (604652, 149, 167), (2225318, 153, 156), (671613, 13, 197), (230861, 13, 231), (59898, 7, 236)])
+def test_mxfp8_codes_beside_a_border(S, h, w):
+    say(f"case norm mxfp8 beside a border S={S} h={h} w={w}")
+    T, H, eps = 32, 4096, 2.0 ** -17
+    x = torch.ones((T, H), dtype=BF16, device="cuda")
+    x[3] = torch.tensor(_row_of_integers(h, S, H), dtype=BF16, device="cuda")
+    weight = torch.full((H,), 2.0 ** -10, dtype=BF16, device="cuda")
+    weight[0] = w
+    square = Fraction(h * w) ** 2 / (Fraction(S, H) + Fraction(1, 1 << 17))
+    exact = 1 / torch.sqrt(x.double().square().mean(1) + eps)[:, None] * x.double() * weight.double()
+    v = exact[3, 0].item()
+    unit = 2.0 ** (math.floor(math.log2(v)) - (0 if h > 100 else 4))      # borders are whole numbers of it, or twice it
+    border = unit * round(v / unit) if round(v / unit) else unit
+    assert 0 < abs(square / Fraction(border) ** 2 - 1) < 2.0 ** -24
+    assert (square > Fraction(border) ** 2) == (v > border)
+    qr, sr, qc, sc, _, _ = sl.sl_rmsnorm_fwd_mxfp8(x, weight, eps)
+    _check_mx(qr, sr, exact, 2.0 ** -45)
+    _check_mx(qc, sc, exact.t().contiguous(), 2.0 ** -45)
