@@ -410,8 +410,12 @@ int sl_rmsnorm_bwd(void* stream, const void* dY, const void* h, const void* w, c
  *   W <- (1 - lr * weight_decay) * W - lr * scale * X   (of the master where there is one, which is then rounded to W)
  * lr, momentum, weight_decay and scale must be finite, steps 0 .. 64 (SL_EINVAL); L <= 65535 and a padded matrix under
  * 2 GiB in fp16 (SL_ESHAPE).  All matrices are 16-byte aligned.  Both take a workspace of the query's bytes, as above.
+ * sl_orthogonalize_tiles (host only, for measurement and tests): how the three products of a step, X.X^T, A.A and P.X, are
+ * taken apart, tiles[12] = for each the number of 256x256 tiles, of 128x128 tiles, of the latter with split sums, and of
+ * their parts (1: none are split); zeros where the steps go to the kernels for few rows.
  * --------------------------------------------------------------------------------------------- */
 size_t sl_orthogonalize_workspace_bytes(int64_t L, int64_t rows, int64_t cols);
+int sl_orthogonalize_tiles(int64_t L, int64_t rows, int64_t cols, int64_t* tiles);
 int sl_orthogonalize(void* stream, const void* G, int32_t g_bytes, void* O, int64_t L, int64_t rows, int64_t cols,
                      int32_t steps, const float* coeffs, void* workspace, size_t workspace_bytes);
 int sl_muon_step(void* stream, void* const* W, float* const* master, const float* const* G, float* const* M,

@@ -14,7 +14,8 @@ from .ops import (sl_grad_buffer_zero, sl_linear_dgrad, sl_linear_dgrad_mxfp8, s
                   sl_linear_fwd_mxfp4w, sl_linear_dgrad_mxfp4w, sl_mxfp4w_fwd_workspace_bytes,
                   sl_mxfp4w_dgrad_workspace_bytes, sl_embedding_fwd, sl_embedding_wgrad_accum,
                   sl_embedding_wgrad_workspace_bytes, sl_rmsnorm_fwd, sl_rmsnorm_fwd_mxfp8, sl_rmsnorm_bwd,
-                  sl_rmsnorm_bwd_workspace_bytes, sl_orthogonalize, sl_orthogonalize_workspace_bytes, sl_muon_step)
+                  sl_rmsnorm_bwd_workspace_bytes, sl_orthogonalize, sl_orthogonalize_workspace_bytes,
+                  sl_orthogonalize_tiles, sl_muon_step)
 from .buffer import ParamAndGradBuffer, sl_bucket_divisor, sl_default_bucket_size, sl_layout_build
 from .autograd import (EmbeddingWithGradAccumulation, LinearMXFP4WithGradAccumulation, LinearWithGradAccumulation,
                        NormLinearMXFP8WithGradAccumulation, RMSNormWithGradAccumulation, embedding_with_grad_accumulation,
@@ -33,7 +34,8 @@ __all__ = [
     "sl_linear_wgrad_accum_mxfp4", "sl_mxfp4_fwd_workspace_bytes", "sl_mxfp4_dgrad_workspace_bytes", "sl_mxfp4_wgrad_workspace_bytes", "sl_linear_fwd_mxfp4w", "sl_linear_dgrad_mxfp4w",
     "sl_mxfp4w_fwd_workspace_bytes", "sl_mxfp4w_dgrad_workspace_bytes",
     "sl_embedding_fwd", "sl_embedding_wgrad_accum", "sl_embedding_wgrad_workspace_bytes", "sl_rmsnorm_fwd", "sl_rmsnorm_fwd_mxfp8",
-    "sl_rmsnorm_bwd", "sl_rmsnorm_bwd_workspace_bytes", "sl_orthogonalize", "sl_orthogonalize_workspace_bytes", "sl_muon_step",
+    "sl_rmsnorm_bwd", "sl_rmsnorm_bwd_workspace_bytes", "sl_orthogonalize", "sl_orthogonalize_workspace_bytes",
+    "sl_orthogonalize_tiles", "sl_muon_step",
     "EmbeddingWithGradAccumulation", "embedding_with_grad_accumulation", "RMSNormWithGradAccumulation",
     "rmsnorm_with_grad_accumulation", "NormLinearMXFP8WithGradAccumulation", "norm_linear_mxfp8_with_grad_accumulation",
 ]

@@ -68,6 +68,7 @@ PROTOTYPES = {
     "sl_rmsnorm_bwd_workspace_bytes": (c_sz, [c_i64, c_i64]),
     "sl_rmsnorm_bwd": (ctypes.c_int, [c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_vp, c_sz]),
     "sl_orthogonalize_workspace_bytes": (c_sz, [c_i64, c_i64, c_i64]),
+    "sl_orthogonalize_tiles": (ctypes.c_int, [c_i64, c_i64, c_i64, P_I64]),
     "sl_orthogonalize": (ctypes.c_int, [c_vp, c_vp, c_i32, c_vp, c_i64, c_i64, c_i64, c_i32, c_vp, c_vp, c_sz]),
     "sl_muon_step": (ctypes.c_int, [c_vp, c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_f32, c_f32, c_i32, c_f32, c_f32, c_i32,
                                     c_vp, c_vp, c_sz]),

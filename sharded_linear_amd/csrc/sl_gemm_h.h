@@ -30,3 +30,7 @@ int half_gemm_sym(hipStream_t st, HalfArgs g);
 int half_gemm_nn(hipStream_t st, HalfArgs g);
 // Workspace of either with these extents (nn: M, N, K; sym: M == N).
 size_t half_gemm_workspace_bytes(int M, int N, int K, int64_t batches, bool sym);
+// What either takes its result apart into: tiles of 256x256, tiles of 128x128 for the rest or for all of it, how many of
+// these have their sums split, and in how many parts.
+struct HalfTiles { int64_t big, small, split, parts; };
+HalfTiles half_gemm_tiles(int M, int N, int K, int64_t batches, bool sym);

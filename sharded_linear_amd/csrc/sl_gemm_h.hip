@@ -536,7 +536,12 @@ int half_gemm_nn(hipStream_t st, HalfArgs g) {
   return !g.d ? sl2::run_half<false, sl2::kPlain>(st, g) : g.clo ? sl2::run_half<false, sl2::kLeftKeep>(st, g) : sl2::run_half<false, sl2::kLeft>(st, g);
 }
 
-size_t half_gemm_workspace_bytes(int M, int N, int K, int64_t batches, bool sym) {
+HalfTiles half_gemm_tiles(int M, int N, int K, int64_t batches, bool sym) {
   const sl2::HalfPlan p = sl2::half_plan(M, N, K, batches, sym);
-  return size_t(p.rest) * size_t(p.splits) * (128 * 128 * 4);
+  return HalfTiles{p.big, p.small, p.rest, p.rest ? p.splits : 1};
+}
+
+size_t half_gemm_workspace_bytes(int M, int N, int K, int64_t batches, bool sym) {
+  const HalfTiles t = half_gemm_tiles(M, N, K, batches, sym);
+  return size_t(t.split) * size_t(t.parts) * (128 * 128 * 4);
 }

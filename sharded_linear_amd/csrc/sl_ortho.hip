@@ -374,6 +374,22 @@ extern "C" size_t sl_orthogonalize_workspace_bytes(int64_t L, int64_t rows, int6
   return size_t(p.bytes);
 }
 
+extern "C" int sl_orthogonalize_tiles(int64_t L, int64_t rows, int64_t cols, int64_t* tiles) {
+  OrthoPlan p{};
+  if (!tiles) return SL_EINVAL;
+  const int e = ortho_plan(L, rows, cols, p);
+  if (e) return e;
+  for (int i = 0; i < 12; ++i) tiles[i] = 0;
+  if (L == 0 || rows == 0 || cols == 0 || p.narrow) return SL_OK;
+  const int m = int(p.mp), n = int(p.np);
+  const HalfTiles t[3] = {half_gemm_tiles(m, m, n, L, true), half_gemm_tiles(m, m, m, L, true), half_gemm_tiles(m, n, m, L, false)};
+  for (int i = 0; i < 3; ++i) {
+    const int64_t v[4] = {t[i].big, t[i].small, t[i].split, t[i].parts};
+    for (int k = 0; k < 4; ++k) tiles[4 * i + k] = v[k];
+  }
+  return SL_OK;
+}
+
 extern "C" int sl_orthogonalize(void* stream, const void* G, int32_t g_bytes, void* O, int64_t L, int64_t rows, int64_t cols, int32_t steps,
                                 const float* coeffs, void* workspace, size_t workspace_bytes) {
   OrthoPlan p{};

@@ -723,6 +723,14 @@ def sl_orthogonalize_workspace_bytes(L: int, rows: int, cols: int) -> int:
     return int(lib().sl_orthogonalize_workspace_bytes(L, rows, cols))
 
 
+def sl_orthogonalize_tiles(L: int, rows: int, cols: int):
+    """For measurement and tests: how the products X X^T, A A and P X of a step are taken apart, for each (tiles of 256x256, of
+    128x128, of the latter with split sums, their parts); None where the steps go to the kernels for few rows."""
+    t = (ctypes.c_int64 * 12)()
+    check("sl_orthogonalize_tiles", lib().sl_orthogonalize_tiles(L, rows, cols, t))
+    return [tuple(t[4 * k:4 * k + 4]) for k in range(3)] if any(t) else None
+
+
 def sl_orthogonalize(G, out=None, steps=5, coefficients=NEWTON_SCHULZ, workspace=None):
     """bf16 Newton-Schulz iterate of G[rows, cols] or of each of G[L, rows, cols] (fp32 or bf16): X = G / |G|_F, and
     ``steps`` times X <- a X + (b A + c A A) X with A = X X^T."""

@@ -387,3 +387,86 @@ def test_captured_and_replayed():
         want = sl.sl_orthogonalize(G)
         torch.cuda.synchronize()
         assert torch.equal(O, want) and torch.equal(W, W2) and torch.equal(M, M2)
+
+
+# ---- the ways in which the tiled products are taken apart ------------------------------------------
+
+# Ragged, so that padding is in every plan; as (L, rows, cols).
+PLANS = [(1, 384, 380), (1, 512, 600), (1, 400, 760), (1, 850, 1000), (3, 3195, 890), (24, 1024, 1277), (12, 1400, 1390), (8, 2048, 2040), (4, 2680, 3570),
+         (11, 1790, 1700), (4, 2944, 2900), (3, 1402, 3190), (4, 1024, 4090), (3, 1660, 3710), (3, 3330, 1790), (2, 2175, 4090), (2, 2040, 4200),
+         (2, 2688, 3199)]
+
+
+def _forms(L, rows, cols):
+    """For each product of a step: its name, the tiles that it is taken apart into, and whether tiles of 256 lie half outside it."""
+    m, n = (-(-min(rows, cols) // 128) * 128, -(-max(rows, cols) // 128) * 128)
+    for name, (big, small, split, parts), wide in zip(("X X^T", "A A", "P X"), sl.sl_orthogonalize_tiles(L, rows, cols), (m, m, n)):
+        assert (split > 0) == (parts > 1) and split <= small
+        tiles = "128" if not big else "256" if not small else "both"
+        yield name, tiles + (" split" if split else ""), bool(big and m % 256), bool(big and wide % 256)
+
+
+def test_plans_cover_every_form():
+    """The shapes that the GPU tests below run: a cost model that is fitted anew must not leave one of these without a test."""
+    seen = {f for plan in PLANS for f in _forms(*plan)}
+    tiles = {(name, t) for name, t, _, _ in seen}
+    for name in ("X X^T", "A A", "P X"):
+        for t in ("128", "128 split", "256", "both", "both split"):
+            assert (name, t) in tiles, (name, t)
+    for t in ("256", "both"):
+        assert ("X X^T", t, True, True) in seen and ("A A", t, True, True) in seen, t
+    assert ("X X^T", "both split", True, True) in seen
+    for t in ("256", "both", "both split"):
+        assert {(m, n) for name, u, m, n in seen if name == "P X" and u == t} >= {(True, True)}, t
+    assert {(m, n) for name, _, m, n in seen if name == "P X"} == {(False, False), (False, True), (True, False), (True, True)}
+    assert sl.sl_orthogonalize_tiles(1, 100, 60) is None and sl.sl_orthogonalize_tiles(0, 512, 512) is None
+    with pytest.raises(RuntimeError):
+        sl.sl_orthogonalize_tiles(1, 1 << 31, 5)
+
+
+def _cosines(g, n, k):
+    """k orthonormal columns of n elements: cosines under random signs (float64)."""
+    i, j = torch.arange(n, device="cuda").double()[:, None], torch.arange(k, device="cuda").double()
+    c = torch.cos(torch.pi / n * (i + 0.5) * j) * (2 / n) ** 0.5
+    c[:, 0] = n ** -0.5
+    signs = torch.randint(0, 2, (n, 1), generator=g, device="cuda").double() * 2 - 1
+    return c * signs
+
+
+def _falling(g, rows, cols, s):
+    """A matrix with the singular values s."""
+    k = min(rows, cols)
+    return ((_cosines(g, rows, k) * s) @ _cosines(g, cols, k).t().contiguous()).float()
+
+
+def _decades(k, how):
+    at = torch.arange(k, device="cuda").double()
+    return 10.0 ** (-4 * at / max(1, k - 1)) if how == "logarithmic" else torch.where(at < k // 4, 1.0, 1e-3).double()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("how", ["logarithmic", "two steps"])
+@pytest.mark.parametrize("L,rows,cols", [(1, 384, 640), (3, 640, 384), (1, 100, 640), (3, 640, 100), (2, 33, 70), (3, 250, 500), (5, 128, 128),
+                                         (2, 1000, 1160)])
+def test_falling_singular_values(L, rows, cols, how):
+    """As test_singular_values_over_decades, whose matrices have 256 rows: fewer rows, tiles, batches, tall and wide.  By the argument
+    there the bound is the same; without what the roundings of X left, [384, 640] is 7.5e-3 off."""
+    say(f"case orthogonalize falling singular values {L} x [{rows}, {cols}] {how}")
+    g = _gen(L * rows + cols)
+    G = torch.stack([_falling(g, rows, cols, _decades(min(rows, cols), how)) for _ in range(L)])
+    O = sl.sl_orthogonalize(G)
+    for l in range(L):
+        assert _off(O[l], _iterate(G[l])) <= _bound(), l
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("L,rows,cols", PLANS)
+def test_every_form_of_tiles(L, rows, cols):
+    """Matrices with falling singular values among normal ones."""
+    say(f"case orthogonalize {L} x [{rows}, {cols}] {list(_forms(L, rows, cols))}")
+    g = _gen(L + rows)
+    G = torch.stack([_randn(g, rows, cols) if l % 2 else _falling(g, rows, cols, _decades(min(rows, cols), "logarithmic")) for l in range(L)])
+    O = sl.sl_orthogonalize(G)
+    for l in range(L):
+        assert _off(O[l], _iterate(G[l])) <= _bound(), l
+    assert torch.equal(sl.sl_orthogonalize(G), O)
