@@ -315,3 +315,19 @@ def test_on_a_side_stream():
         y, got = sl.sl_embedding_fwd(late, W), sl.sl_embedding_wgrad_accum(late, dY, torch.zeros((V, H), device="cuda"))
     s.synchronize()
     assert torch.equal(y, want) and torch.equal(got, grad)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("V", [255000, 256001, 513000, 1100000, 2500000, 5000000, 9000000, 1 << 24])
+def test_sorted_gradient_of_large_tables(V):
+    """Tokens enough for the sort, and more ids than 256 buckets hold: 2^8 to 2^15 buckets; first and last rows met, repeated ids, and ids
+    of one bucket (equal low bits)."""
+    say(f"case embedding gradient, sorted, V={V}")
+    g = _gen(V % 1000)
+    ids = _ids(g, 1500, 0, V, torch.int64)
+    ids[:4] = torch.tensor([0, V - 1, V - 1, 0], device="cuda")
+    ids[100:400] = torch.arange(300, device="cuda") % 60 * 32768 % V
+    ids[1000:1300] = ids[400:700]
+    for dtype in (torch.int32, torch.int64):
+        _exact_case(ids.to(dtype), V, 8, 0, V)
+    _exact_case(ids + 12345, V, 8, 12345 + V // 3, V)
