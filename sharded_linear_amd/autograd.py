@@ -18,6 +18,38 @@ from .ops import (sl_embedding_fwd, sl_embedding_wgrad_accum, sl_linear_dgrad, s
                   sl_rmsnorm_fwd_mxfp8, _raw_stream)
 
 
+# A leaf has one gradient accumulator for all its living graphs, and it belongs to the stream on which it was made.  The functions below
+# leave a weight's gradient in main_grad and return none, so a captured backward pass meets the accumulator's stream only at its
+# end, where the engine joins that stream to the capture: if it is not the capture's, that ends the process.  So the functions
+# note the stream on the accumulators that they meet, and refuse a capture that meets one noted on another.  What they
+# cannot know: an accumulator that other operators made, of a graph in which none of these functions has met the leaf, or
+# on another stream than that of the first of these calls; and leaves behind an operator that comes before the call.
+
+def _refuse_foreign_accumulators(*leaves):
+    """Raises, while a graph is captured, for a leaf whose accumulator was noted on another stream."""
+    for t in leaves:
+        if t is not None and t.requires_grad and t.is_leaf and t.is_cuda:
+            if not torch.is_grad_enabled() or not torch.cuda.is_current_stream_capturing():
+                return
+            stream = _raw_stream(t.device.index)
+            if torch.autograd.graph.get_gradient_edge(t).node.metadata.get("sl_stream", stream) != stream:
+                raise RuntimeError("a leaf's gradient accumulator belongs to another stream than the capture's and lives, held by a graph "
+                                   "that was made there (drop its results before the capture) or by a hook on the accumulator: "
+                                   "a backward pass cannot be captured beside it")
+
+
+_AccumulateGrad = torch._C._functions.AccumulateGrad
+
+
+def _note_accumulators(out):
+    """Notes the current stream on the accumulators next to the node that made ``out``."""
+    fn = out.grad_fn
+    if fn is not None:
+        for node, _ in fn.next_functions:
+            if node.__class__ is _AccumulateGrad:
+                node.metadata.setdefault("sl_stream", _raw_stream(out.device.index))
+
+
 class LinearWithGradAccumulation(torch.autograd.Function):
     @staticmethod
     def forward(ctx, input: torch.Tensor, weight: torch.Tensor):
@@ -40,7 +72,10 @@ class LinearWithGradAccumulation(torch.autograd.Function):
 
 
 def linear_with_grad_accumulation(input: torch.Tensor, weight: torch.Tensor) -> torch.Tensor:
-    return LinearWithGradAccumulation.apply(input, weight)
+    _refuse_foreign_accumulators(weight)
+    y = LinearWithGradAccumulation.apply(input, weight)
+    _note_accumulators(y)
+    return y
 
 
 def _check_copies(copies, n_out, n_in, cols):
@@ -107,30 +142,15 @@ def linear_mxfp4_with_grad_accumulation(input: torch.Tensor, weight: torch.Tenso
     rounds dY stochastically, which keeps the gradients unbiased; a training loop gives every call its
     own.  ``weight_mxfp4`` is sl_mxfp4_quantize(weight), made once and passed to every micro-batch that
     uses the same weight; without it the weight is cast in each call."""
-    return LinearMXFP4WithGradAccumulation.apply(input, weight, seed, weight_mxfp4)
+    _refuse_foreign_accumulators(weight)
+    y = LinearMXFP4WithGradAccumulation.apply(input, weight, seed, weight_mxfp4)
+    _note_accumulators(y)
+    return y
 
 
 def _need_main_grad(weight, needed):
     if needed and not hasattr(weight, "main_grad"):
         raise ValueError("gradient accumulation fusion needs weight.main_grad (a grad_data view)")
-
-
-def _accumulators(*tensors):
-    """The gradient accumulators of the leaves among ``tensors``, to be held until the call has joined them to its graph.
-
-    A leaf has one accumulator for all its living graphs, and it belongs to the stream on which the first of them was made.
-    A backward pass that is captured joins that stream to the capture, which ends the process if the stream is not the
-    capture's: such a call is refused here."""
-    held = []
-    if torch.is_grad_enabled():
-        for t in tensors:
-            if t is not None and t.requires_grad and t.is_leaf and t.is_cuda:
-                node, stream = torch.autograd.graph.get_gradient_edge(t).node, _raw_stream(t.device.index)
-                held.append(node)
-                if node.metadata.setdefault("sl_stream", stream) != stream and torch.cuda.is_current_stream_capturing():
-                    raise RuntimeError("a graph of these leaves that was made on another stream lives: drop its results "
-                                       "before the capture, for its backward pass cannot be captured beside them")
-    return held
 
 
 class EmbeddingWithGradAccumulation(torch.autograd.Function):
@@ -156,8 +176,10 @@ def embedding_with_grad_accumulation(ids: torch.Tensor, weight: torch.Tensor, vo
     vocab_start .. vocab_start + V - 1), so that the ranks' results add up.  Backward adds into weight.main_grad."""
     if not torch.is_grad_enabled():
         weight = weight.detach()
-    held = _accumulators(weight)  # noqa: F841
-    return EmbeddingWithGradAccumulation.apply(ids, weight, vocab_start, scale)
+    _refuse_foreign_accumulators(weight)
+    y = EmbeddingWithGradAccumulation.apply(ids, weight, vocab_start, scale)
+    _note_accumulators(y)
+    return y
 
 
 def _norm_rows(x, weight, residual):
@@ -208,8 +230,10 @@ def rmsnorm_with_grad_accumulation(input: torch.Tensor, weight: torch.Tensor, re
     the residual stream that the next block adds to.  The weight's gradient goes to weight.main_grad."""
     if not torch.is_grad_enabled():
         weight = weight.detach()
-    held = _accumulators(input, weight, residual)  # noqa: F841
-    return RMSNormWithGradAccumulation.apply(input, weight, residual, eps)
+    _refuse_foreign_accumulators(input, weight, residual)
+    out = RMSNormWithGradAccumulation.apply(input, weight, residual, eps)
+    _note_accumulators(out if residual is None else out[0])
+    return out
 
 
 class NormLinearMXFP8WithGradAccumulation(torch.autograd.Function):
@@ -271,5 +295,7 @@ def norm_linear_mxfp8_with_grad_accumulation(input: torch.Tensor, norm_weight: t
     """Y = norm(input + residual) . weight^T with every product of the step on MXFP8 operands: returns Y, or (Y, h) with a
     residual, h = input + residual.  Both weights' gradients go to their main_grad.  ``weight_mxfp8`` is
     sl_mxfp8_quantize(weight), made once and passed to every micro-batch; without it the weight is quantised in each call."""
-    held = _accumulators(input, norm_weight, residual, weight)  # noqa: F841
-    return NormLinearMXFP8WithGradAccumulation.apply(input, norm_weight, residual, weight, eps, weight_mxfp8)
+    _refuse_foreign_accumulators(input, norm_weight, residual, weight)
+    out = NormLinearMXFP8WithGradAccumulation.apply(input, norm_weight, residual, weight, eps, weight_mxfp8)
+    _note_accumulators(out if residual is None else out[0])
+    return out

@@ -298,3 +298,89 @@ def test_a_training_step_of_one_rank():
         step = (old[s:e].double() - buf.param_data[s:e].double()).view(shapes[n]) / (0.02 * max(1.0, shapes[n][0] / shapes[n][1]) ** 0.5)
         sv = torch.linalg.svdvals(step)
         assert sv.max() <= 1.3 and sv[: len(sv) // 2].min() >= 0.5         # orthogonalised: singular values near 1
+
+
+def _linear_calls(g):
+    """Both linear functions with one weight and its gradient buffer, an input that is no leaf, and a gradient of the results."""
+    T, H, O = 128, 256, 384
+    buf = sl.ParamAndGradBuffer({"fc": (O, H)}, "cuda", bucket_size=None)
+    w = buf.attach("fc", torch.nn.Parameter(_bf16(g, O, H, std=0.1)))
+    x = _bf16(g, T, H)
+    return buf, w, x, _bf16(g, T, O), {"linear": lambda: sl.linear_with_grad_accumulation(x, w),
+                                       "mxfp4": lambda: sl.linear_mxfp4_with_grad_accumulation(x, w)}
+
+
+@pytest.mark.gpu
+@pytest.mark.filterwarnings("ignore:The CUDA Graph is empty")
+@pytest.mark.parametrize("name", ["linear", "mxfp4"])
+def test_captured_linear_gradients(name):
+    """The linear functions leave a weight's gradient in main_grad as the others do: a capture beside a living eager graph of the same weight
+    is refused, and without one its gradients are the eager ones."""
+    say(f"case captured gradients of {name}")
+    buf, w, x, c, calls = _linear_calls(_gen(4))
+    call = calls[name]
+
+    def both():
+        y = call()
+        torch.autograd.grad(y, w, c, allow_unused=True)
+        return y.detach()
+
+    eager = call()
+    with pytest.raises(RuntimeError, match="drop its results"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            call()
+    del eager
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        both()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = both()
+    for k in range(3):
+        x.copy_(_bf16(_gen(10 + k), *x.shape))
+        buf.zero_grad_buffer()
+        graph.replay()
+        got = buf.grad_data.clone()
+        buf.zero_grad_buffer()
+        want = both()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(got, buf.grad_data) and got.any()
+
+
+@pytest.mark.gpu
+@pytest.mark.filterwarnings("ignore:The CUDA Graph is empty")
+def test_capture_beside_a_graph_of_another_function():
+    """The accumulator is the leaf's, whichever function met it first; one that a hook's owner holds is refused by a message that names it."""
+    say("case captures beside graphs of other functions")
+    g = _gen(6)
+    buf = sl.ParamAndGradBuffer({"table": (304, 256)}, "cuda", bucket_size=None)
+    w = buf.attach("table", torch.nn.Parameter(_bf16(g, 304, 256)))
+    ids, x = torch.randint(0, 304, (64,), generator=g, device="cuda"), _bf16(g, 32, 256)
+    lookup, product = lambda: sl.embedding_with_grad_accumulation(ids, w), lambda: sl.linear_with_grad_accumulation(x, w)
+    for first, second in ((lookup, product), (product, lookup)):          # a tied table
+        eager = first()
+        with pytest.raises(RuntimeError, match="drop its results"):
+            with torch.cuda.graph(torch.cuda.CUDAGraph()):
+                second()
+        del eager
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            second()
+    node = torch.autograd.graph.get_gradient_edge(w).node
+    lookup()
+    with pytest.raises(RuntimeError, match="hook"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            lookup()
+    del node
+    with torch.cuda.graph(torch.cuda.CUDAGraph()):
+        lookup()
+    # results made on the capture's own stream may live
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        eager = lookup()
+        s.synchronize()
+        with torch.cuda.graph(torch.cuda.CUDAGraph(), stream=s):
+            lookup()
+    assert eager.requires_grad
