@@ -44,7 +44,7 @@ _AccumulateGrad = torch._C._functions.AccumulateGrad
 def _note_accumulators(out):
     """Notes the current stream on the accumulators next to the node that made ``out``."""
     fn = out.grad_fn
-    if fn is not None:
+    if fn is not None and out.is_cuda:
         for node, _ in fn.next_functions:
             if node.__class__ is _AccumulateGrad:
                 node.metadata.setdefault("sl_stream", _raw_stream(out.device.index))
