@@ -6,6 +6,7 @@ import types
 
 import pytest
 import torch
+from torch.utils._python_dispatch import TorchDispatchMode
 
 import sharded_linear_amd as sl
 from sharded_linear_amd import ops
@@ -384,3 +385,40 @@ def test_capture_beside_a_graph_of_another_function():
         with torch.cuda.graph(torch.cuda.CUDAGraph(), stream=s):
             lookup()
     assert eager.requires_grad
+
+
+class _Made(TorchDispatchMode):
+    """Notes the storages of what the dispatcher's operations return."""
+
+    def __init__(self):
+        super().__init__()
+        self.storages = set()
+
+    def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+        out = func(*args, **(kwargs or {}))
+        if isinstance(out, torch.Tensor):
+            self.storages.add(out.untyped_storage().data_ptr())
+        return out
+
+
+@pytest.mark.gpu
+def test_results_are_seen_by_the_dispatcher():
+    """Modes that follow or fill new tensors see every result."""
+    say("case step operators under a dispatch mode")
+    g = _gen(7)
+    x, w, ids = _bf16(g, 64, 64), _bf16(g, 64), torch.zeros(64, dtype=I32, device="cuda")
+    rstd = sl.sl_rmsnorm_fwd(x, w, 1e-5)[2]
+    q, s, _, _ = sl.sl_mxfp8_quantize(x)
+    calls = {
+        "embedding": lambda: (sl.sl_embedding_fwd(ids, x),),
+        "norm": lambda: sl.sl_rmsnorm_fwd(x, w, 1e-5, residual=x),
+        "norm mxfp8": lambda: sl.sl_rmsnorm_fwd_mxfp8(x, w, 1e-5, residual=x),
+        "norm gradient": lambda: (sl.sl_rmsnorm_bwd(x, x, w, rstd, None),),
+        "orthogonalize": lambda: (sl.sl_orthogonalize(x),),
+        "dequantize": lambda: (sl.sl_mxfp8_dequantize(q, s),),
+    }
+    for name, call in calls.items():
+        with _Made() as made:
+            outs = call()
+        for out in outs:
+            assert out.untyped_storage().data_ptr() in made.storages, name
