@@ -182,14 +182,24 @@ def embedding_with_grad_accumulation(ids: torch.Tensor, weight: torch.Tensor, vo
     return y
 
 
+def _result(x, features):
+    """A new result of ``features`` for each row of x, in x's shape from the start: what a Function returns as a view cannot be
+    modified in place."""
+    return torch.empty(*x.shape[:-1], features, dtype=torch.bfloat16, device=x.device)
+
+
+def _rows(t):
+    """t as contiguous rows of its last axis."""
+    return None if t is None else t.reshape(-1, t.shape[-1]).contiguous()
+
+
 def _norm_rows(x, weight, residual):
     """x and the residual as contiguous rows of the norm's width."""
     if weight.dim() != 1 or x.shape[-1] != weight.shape[0]:
         raise ValueError(f"input of {x.shape[-1]} features by a norm weight of shape {tuple(weight.shape)}")
     if residual is not None and residual.shape != x.shape:
         raise ValueError(f"residual has shape {tuple(residual.shape)}, the input {tuple(x.shape)}")
-    rows = lambda t: None if t is None else t.reshape(-1, t.shape[-1]).contiguous()  # noqa: E731
-    return rows(x), rows(residual)
+    return _rows(x), _rows(residual)
 
 
 class RMSNormWithGradAccumulation(torch.autograd.Function):
@@ -197,12 +207,12 @@ class RMSNormWithGradAccumulation(torch.autograd.Function):
     def forward(ctx, input, weight, residual, eps):
         _need_main_grad(weight, ctx.needs_input_grad[1])
         x2, r2 = _norm_rows(input, weight, residual)
-        y, h, rstd = sl_rmsnorm_fwd(x2, weight.detach(), eps, residual=r2)
+        y, h = _result(input, input.shape[-1]), x2 if residual is None else _result(input, input.shape[-1])
+        _, _, rstd = sl_rmsnorm_fwd(x2, weight.detach(), eps, residual=r2, y=_rows(y), h=None if residual is None else _rows(h))
         ctx.save_for_backward(h, weight, rstd)
         ctx.set_materialize_grads(False)
         ctx.shape = input.shape
-        y = y.view(input.shape)
-        return y if residual is None else (y, h.view(input.shape))
+        return y if residual is None else (y, h)
 
     @staticmethod
     @once_differentiable
@@ -215,10 +225,9 @@ def _norm_backward(ctx, grad_y, grad_h, h, weight, rstd):
     """Gradients of input, weight (into main_grad) and residual."""
     if grad_y is None:
         return grad_h, None, grad_h if ctx.needs_input_grad[2] else None
-    rows = lambda t: None if t is None else t.reshape(-1, t.shape[-1]).contiguous()  # noqa: E731
     need_w = ctx.needs_input_grad[1]
-    dx = sl_rmsnorm_bwd(rows(grad_y), h, weight.detach(), rstd, weight.main_grad if need_w else None,
-                        dresidual=rows(grad_h)).view(ctx.shape)
+    dx = sl_rmsnorm_bwd(_rows(grad_y), _rows(h), weight.detach(), rstd, weight.main_grad if need_w else None,
+                        dresidual=_rows(grad_h)).view(ctx.shape)
     if need_w:
         weight.grad_added_to_main_grad = True
     return dx, None, dx if ctx.needs_input_grad[2] else None
@@ -227,7 +236,8 @@ def _norm_backward(ctx, grad_y, grad_h, h, weight, rstd):
 def rmsnorm_with_grad_accumulation(input: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None,
                                    eps: float = 1e-5):
     """The root-mean-square norm of ``input`` over its last axis, or of h = input + residual: returns y, or (y, h), h being
-    the residual stream that the next block adds to.  The weight's gradient goes to weight.main_grad."""
+    the residual stream that the next block adds to (out of place: backward reads h, and refuses one that was modified).  The
+    weight's gradient goes to weight.main_grad."""
     if not torch.is_grad_enabled():
         weight = weight.detach()
     _refuse_foreign_accumulators(input, weight, residual)
@@ -266,12 +276,14 @@ class NormLinearMXFP8WithGradAccumulation(torch.autograd.Function):
         wr, wrs, wc, wcs = weight_mxfp8
         if need_x and wc is None:
             raise ValueError("the input gradient needs the weight's columnwise MXFP8 copy")
-        xr, xrs, xc, xcs, h, rstd = sl_rmsnorm_fwd_mxfp8(x2, norm_weight.detach(), eps, residual=r2, cols=need_w)
-        y = sl_linear_fwd_mxfp8(xr, xrs, wr, wrs).view(*input.shape[:-1], n_out)
+        y, h = _result(input, n_out), x2 if residual is None else _result(input, n_in)
+        xr, xrs, xc, xcs, _, rstd = sl_rmsnorm_fwd_mxfp8(x2, norm_weight.detach(), eps, residual=r2, cols=need_w,
+                                                         h=None if residual is None else _rows(h))
+        sl_linear_fwd_mxfp8(xr, xrs, wr, wrs, _rows(y))
         ctx.save_for_backward(h, norm_weight, rstd, weight, xc, xcs, wc, wcs)
         ctx.set_materialize_grads(False)
         ctx.shape = input.shape
-        return y if residual is None else (y, h.view(input.shape))
+        return y if residual is None else (y, h)
 
     @staticmethod
     @once_differentiable
@@ -293,7 +305,7 @@ class NormLinearMXFP8WithGradAccumulation(torch.autograd.Function):
 def norm_linear_mxfp8_with_grad_accumulation(input: torch.Tensor, norm_weight: torch.Tensor, weight: torch.Tensor,
                                              residual: torch.Tensor | None = None, eps: float = 1e-5, weight_mxfp8=None):
     """Y = norm(input + residual) . weight^T with every product of the step on MXFP8 operands: returns Y, or (Y, h) with a
-    residual, h = input + residual.  Both weights' gradients go to their main_grad.  ``weight_mxfp8`` is
+    residual, h = input + residual (which backward reads again).  Both weights' gradients go to their main_grad.  ``weight_mxfp8`` is
     sl_mxfp8_quantize(weight), made once and passed to every micro-batch; without it the weight is quantised in each call."""
     _refuse_foreign_accumulators(input, norm_weight, residual, weight)
     out = NormLinearMXFP8WithGradAccumulation.apply(input, norm_weight, residual, weight, eps, weight_mxfp8)

@@ -582,9 +582,7 @@ def sl_embedding_fwd(ids, W, Y=None, vocab_start=0, scale=1.0):
     V, H = _want_matrix(W, "W", BF16, dev)
     T = ids.numel()
     if Y is None:
-        Y = torch.empty(T, H, dtype=BF16, device=dev)
-        if ids.dim() != 1:
-            Y = Y.view(*ids.shape, H)
+        Y = torch.empty(*ids.shape, H, dtype=BF16, device=dev)
     else:
         _want(Y, "Y", BF16, (*ids.shape, H), dev)
     _launch("sl_embedding_fwd", dev, _addr(ids), size, _addr(W), _addr(Y), T, V, H, vocab_start, scale)

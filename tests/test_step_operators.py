@@ -422,3 +422,47 @@ def test_results_are_seen_by_the_dispatcher():
             outs = call()
         for out in outs:
             assert out.untyped_storage().data_ptr() in made.storages, name
+
+
+@pytest.mark.gpu
+def test_results_are_modified_in_place():
+    """No result of the embedding and the norms is a view made inside the function.  The residual stream h is read again by backward, which refuses a modified one; the
+    other results are not."""
+    say("case results modified in place")
+    g = _gen(8)
+    shapes = {"table": (64, 256), "norm": (256,), "fc": (128, 256)}
+    buf = sl.ParamAndGradBuffer(shapes, "cuda", bucket_size=None)
+    p = {n: buf.attach(n, torch.nn.Parameter(_bf16(g, *s, std=0.1))) for n, s in shapes.items()}
+    x, r = _bf16(g, 2, 64, 256).requires_grad_(), _bf16(g, 2, 64, 256).requires_grad_()
+    ids = torch.randint(0, 64, (2, 64), generator=g, device="cuda")
+    calls = {
+        "embedding": lambda: sl.embedding_with_grad_accumulation(ids, p["table"]),
+        "norm": lambda: sl.rmsnorm_with_grad_accumulation(x, p["norm"]),
+        "norm residual": lambda: sl.rmsnorm_with_grad_accumulation(x, p["norm"], r),
+        "norm linear": lambda: sl.norm_linear_mxfp8_with_grad_accumulation(x, p["norm"], p["fc"]),
+        "norm linear residual": lambda: sl.norm_linear_mxfp8_with_grad_accumulation(x, p["norm"], p["fc"], r),
+    }
+    for name, call in calls.items():
+        say(f"case {name}")
+        grads = []
+        for inplace in (True, False):
+            buf.zero_grad_buffer()
+            out = call()
+            y = out[0] if isinstance(out, tuple) else out
+            assert y.shape[:2] == (2, 64) and not y._is_view()
+            y = y.mul_(2.0) if inplace else y * 2.0
+            dx = torch.autograd.grad(y, [x, p["table"]], torch.ones_like(y), allow_unused=True)[0]
+            grads.append((dx, buf.grad_data.clone()))
+        assert torch.equal(grads[0][1], grads[1][1]) and grads[0][1].any(), name
+        assert (grads[0][0] is None) == (name == "embedding") and (grads[0][0] is None or torch.equal(grads[0][0], grads[1][0])), name
+        if isinstance(out, tuple):
+            y, h = call()
+            assert h.shape == x.shape and not h._is_view()
+            kept = h.detach().clone()
+            h += y.detach()[..., :1]
+            assert torch.equal(h.detach(), kept + y.detach()[..., :1])
+            with pytest.raises(RuntimeError, match="inplace"):
+                torch.autograd.grad(y, x, torch.ones_like(y))
+            with torch.no_grad():
+                y, h = call()
+                h += 1
