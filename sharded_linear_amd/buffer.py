@@ -15,7 +15,7 @@ from dataclasses import dataclass
 import torch
 
 from ._lib import check, lib
-from .ops import sl_grad_buffer_zero, sl_muon_step
+from .ops import _muon_steps, sl_grad_buffer_zero
 
 
 @dataclass
@@ -105,14 +105,31 @@ class ParamAndGradBuffer:
     def zero_grad_buffer(self) -> None:
         sl_grad_buffer_zero(self.grad_data)
 
-    def muon_step(self, names, momentum_data: torch.Tensor, lr: float, **options) -> None:
+    def muon_step(self, names, momentum_data: torch.Tensor, lr: float, masters=None, **options) -> None:
         """sl_muon_step of the named matrices, from grad_data into param_data.  ``momentum_data`` is laid out as grad_data
-        (zeros at first); weights of one shape share a call."""
-        if momentum_data.shape != self.grad_data.shape:
-            raise ValueError(f"momentum_data has shape {tuple(momentum_data.shape)}, expected {tuple(self.grad_data.shape)}")
-        by_shape = {}
-        for name in names:
-            by_shape.setdefault(self.shapes[name], []).append(name)
-        for shape, group in by_shape.items():
-            momenta = [momentum_data[s:e].view(shape) for s, e, _ in (self.index[n] for n in group)]
-            sl_muon_step([self.param(n) for n in group], [self.main_grad(n) for n in group], momenta, lr, **options)
+        (zeros at first); so are ``masters``, unless they are given as a list, one of each name.  Weights of one shape share a call.  All
+        names are checked before the first call.
+
+        The buffer holds one rank's slices, and each is orthogonalised by itself and scaled by its own rows and columns: of a
+        tensor-parallel weight this is the block-wise update, not that of the whole matrix.  grad_data is taken as it stands, so it
+        has to be reduced over the data-parallel ranks first."""
+        names = list(names)
+        if isinstance(masters, torch.Tensor) and len(names) == 1 and masters.shape == self.shapes[names[0]]:
+            masters = [masters]
+        for name, data in (("momentum_data", momentum_data), ("masters", masters)):
+            if isinstance(data, torch.Tensor) and data.shape != self.grad_data.shape:
+                raise ValueError(f"{name} has shape {tuple(data.shape)}, expected {tuple(self.grad_data.shape)}")
+        at = lambda data, n: data[self.index[n][0]:self.index[n][1]].view(self.shapes[n])  # noqa: E731
+        if isinstance(masters, torch.Tensor):
+            masters = [at(masters, n) for n in names]
+        if masters is not None and len(masters) != len(names):
+            raise ValueError(f"{len(masters)} masters of {len(names)} names")
+        groups = {}
+        for k, n in enumerate(names):
+            w, g, m, p = groups.setdefault(self.shapes[n], ([], [], [], None if masters is None else []))
+            w.append(self.param(n))
+            g.append(self.main_grad(n))
+            m.append(at(momentum_data, n))
+            if masters is not None:
+                p.append(masters[k])
+        _muon_steps(list(groups.values()), lr, **options)

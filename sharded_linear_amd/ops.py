@@ -14,6 +14,7 @@ import torch
 from ._lib import check, lib
 
 BF16, F32, U8 = torch.bfloat16, torch.float32, torch.uint8
+SL_EALIGN, SL_ESHAPE, SL_EWORKSPACE = -2, -3, -4
 
 
 def _ptr(t):
@@ -748,30 +749,62 @@ def _want_apart(written, read):
             end, last_written = stop, w
 
 
-def sl_muon_step(weights, main_grads, momenta, lr, momentum=0.95, nesterov=True, weight_decay=0.0, scale=None, masters=None,
-                 steps=5, coefficients=NEWTON_SCHULZ, workspace=None):
-    """One step of bf16 weights of one shape, in place, from their fp32 main_grads: M <- momentum M + G, U = G + momentum M
-    (``nesterov``) or M, W <- (1 - lr weight_decay) W - lr scale orthogonalize(U).  Arguments are matrices or lists of them; a
-    list's products run together, so weights of one shape belong in one call.  ``masters`` are fp32 weights that take the step in W's
-    place; W is then their rounding.  ``scale`` None is sqrt(max(1, rows / cols))."""
+def _muon_call(weights, main_grads, momenta, lr, momentum=0.95, nesterov=True, weight_decay=0.0, scale=None, masters=None, steps=5,
+               coefficients=NEWTON_SCHULZ, workspace=None):
+    """Checks sl_muon_step's arguments and launches nothing: (the matrices that it writes, those that it reads, the call itself)."""
     lists = [[t] if isinstance(t, torch.Tensor) else list(t) for t in (weights, main_grads, momenta)]
     lists.append(None if masters is None else [masters] if isinstance(masters, torch.Tensor) else list(masters))
     W = lists[0]
     if any(x is not None and len(x) != len(W) for x in lists):
         raise ValueError("weights, main_grads, momenta and masters differ in number")
     if not W:
-        return
+        return [], [], lambda: None
     dev = _device(W[0])
     rows, cols = _want_matrix(W[0], "a weight", BF16, dev)
     for x, name, dtype in zip(lists, ("a weight", "a main_grad", "a momentum", "a master"), (BF16, F32, F32, F32)):
         for t in x or ():
             _want(t, name, dtype, (rows, cols), dev)
-    _want_apart([t for x in (lists[0], lists[2], lists[3]) for t in x or ()], lists[1])
     if scale is None:
         scale = max(1.0, rows / cols) ** 0.5 if cols else 1.0
     steps, k = _coefficients(steps, coefficients)
     table = lambda x: None if x is None else (ctypes.c_void_p * len(x))(*(t.data_ptr() for t in x))  # noqa: E731
-    w, g, m, p = (table(x) for x in lists)
-    workspace, nbytes = _scratch(dev, sl_orthogonalize_workspace_bytes(len(W), rows, cols), workspace)
-    _launch("sl_muon_step", dev, w, p, g, m, len(W), rows, cols, lr, momentum, int(nesterov), weight_decay, scale, steps, k,
-            _addr(workspace), nbytes)
+    need = sl_orthogonalize_workspace_bytes(len(W), rows, cols)
+
+    def call():
+        w, g, m, p = (table(x) for x in lists)
+        ws, nbytes = _scratch(dev, need, workspace)
+        _launch("sl_muon_step", dev, w, p, g, m, len(W), rows, cols, lr, momentum, int(nesterov), weight_decay, scale, steps, k,
+                _addr(ws), nbytes)
+
+    return [t for x in (lists[0], lists[2], lists[3]) for t in x or ()], lists[1], call
+
+
+def sl_muon_step(weights, main_grads, momenta, lr, momentum=0.95, nesterov=True, weight_decay=0.0, scale=None, masters=None,
+                 steps=5, coefficients=NEWTON_SCHULZ, workspace=None):
+    """One step of bf16 weights of one shape, in place, from their fp32 main_grads: M <- momentum M + G, U = G + momentum M
+    (``nesterov``) or M, W <- (1 - lr weight_decay) W - lr scale orthogonalize(U).  Arguments are matrices or lists of them; a
+    list's products run together, so weights of one shape belong in one call.  ``masters`` are fp32 weights that take the step in W's
+    place; W is then their rounding.  ``scale`` None is sqrt(max(1, rows / cols))."""
+    written, read, call = _muon_call(weights, main_grads, momenta, lr, momentum, nesterov, weight_decay, scale, masters, steps,
+                                     coefficients, workspace)
+    _want_apart(written, read)
+    call()
+
+
+def _muon_steps(groups, lr, momentum=0.95, nesterov=True, weight_decay=0.0, scale=None, steps=5, coefficients=NEWTON_SCHULZ,
+                workspace=None):
+    """sl_muon_step of each (weights, main_grads, momenta, masters) of ``groups``; all are checked before the first is launched, so
+    that a refusal leaves every weight and momentum as it was."""
+    calls = [_muon_call(w, g, m, lr, momentum, nesterov, weight_decay, scale, p, steps, coefficients, workspace) for w, g, m, p in groups]
+    _want_apart([t for c in calls for t in c[0]], [t for c in calls for t in c[1]])
+    if any(t.data_ptr() % 16 for c in calls for t in c[0] + c[1] if t.numel()):
+        check("sl_muon_step", SL_EALIGN)
+    for w, _, _, _ in groups:
+        if w[0].numel():
+            need = sl_orthogonalize_workspace_bytes(len(w), *w[0].shape)
+            if not need:
+                check("sl_muon_step", SL_ESHAPE)
+            if workspace is not None and _scratch(w[0].device, need, workspace)[1] < need:
+                check("sl_muon_step", SL_EWORKSPACE)
+    for _, _, call in calls:
+        call()

@@ -470,3 +470,96 @@ def test_every_form_of_tiles(L, rows, cols):
     for l in range(L):
         assert _off(O[l], _iterate(G[l])) <= _bound(), l
     assert torch.equal(sl.sl_orthogonalize(G), O)
+
+
+# ---- a step on the buffer is refused as a whole ----------------------------------------------------
+
+def _host_buffer(monkeypatch, shapes, **kw):
+    """A buffer on the host, and the list of the calls that would be launched on it."""
+    from sharded_linear_amd import ops
+    calls = []
+    monkeypatch.setattr(ops, "_device", lambda t: t.device)
+    monkeypatch.setattr(ops, "_launch", lambda name, dev, *a: calls.append((name, *a)))
+    monkeypatch.setattr(ops, "_scratch", lambda dev, need, ws: (ws, need if ws is None else ws.numel()))
+    buf = sl.ParamAndGradBuffer(shapes, "cpu", bucket_size=None, **kw)
+    return buf, torch.zeros_like(buf.grad_data), calls
+
+
+SHAPES_OF_TWO = {"fc": (24, 16), "norm": (24,), "out": (16, 24), "fc2": (24, 16)}
+
+
+@pytest.mark.parametrize("names,options,match", [
+    (["fc", "norm"], {}, "matrix"),
+    (["fc", "out", "fc"], {}, "twice"),
+    (["fc", "out", "missing"], {}, "missing"),
+    (["fc", "out"], {"momentum_data": torch.zeros(10)}, "momentum_data"),
+    (["fc", "out"], {"momentum_data": "bf16"}, "momentum"),
+    (["fc", "out"], {"masters": [torch.zeros(24, 16)]}, "1 masters of 2"),
+    (["fc", "out"], {"masters": [torch.zeros(24, 16), torch.zeros(24, 16)]}, "shape"),
+    (["fc", "out"], {"masters": torch.zeros(10)}, "masters"),
+    (["fc", "out"], {"masters": "momenta"}, "twice"),
+    (["fc", "out"], {"workspace": torch.zeros(16, dtype=torch.uint8)}, "EWORKSPACE"),
+    (["fc", "out"], {"other": 1}, "other"),
+])
+def test_step_on_the_buffer_is_refused_before_anything_is_launched(names, options, match, monkeypatch):
+    buf, momentum, calls = _host_buffer(monkeypatch, SHAPES_OF_TWO)
+    options = dict(options)
+    momentum = options.pop("momentum_data", momentum)
+    if isinstance(momentum, str):
+        momentum = torch.zeros_like(buf.param_data)
+    if isinstance(options.get("masters"), str):
+        options["masters"] = momentum
+    with pytest.raises((ValueError, TypeError, KeyError, RuntimeError), match=match):
+        buf.muon_step(names, momentum, 0.1, **options)
+    assert not calls
+
+
+def test_step_on_a_buffer_without_alignment_is_refused_as_a_whole(monkeypatch):
+    buf, momentum, calls = _host_buffer(monkeypatch, {"b": (3, 5), "a": (16, 24)}, param_align=1)
+    assert buf.main_grad("b").data_ptr() % 16 == 0 and buf.param("b").data_ptr() % 16 == 0
+    buf, momentum, calls = _host_buffer(monkeypatch, {"c": (3, 3), "b": (3, 5), "a": (16, 24)}, param_align=1)
+    with pytest.raises(RuntimeError, match="EALIGN"):
+        buf.muon_step(["a", "c"], momentum, 0.1)
+    assert not calls
+    buf.muon_step(["a", "b"], momentum, 0.1)
+    assert [c[0] for c in calls] == ["sl_muon_step"] * 2
+
+
+def test_masters_go_with_their_names(monkeypatch):
+    """As a buffer, as a list in the names' order, and one for one name; weights of two shapes in turn."""
+    buf, momentum, calls = _host_buffer(monkeypatch, SHAPES_OF_TWO)
+    flat = torch.zeros_like(buf.grad_data)
+    at = lambda data, n: data[buf.index[n][0]:buf.index[n][1]].view(buf.shapes[n])  # noqa: E731
+    names = ["fc", "out", "fc2"]
+    want = [[at(flat, "fc").data_ptr(), at(flat, "fc2").data_ptr()], [at(flat, "out").data_ptr()]]
+    for masters in (flat, [at(flat, n) for n in names]):
+        calls.clear()
+        buf.muon_step(names, momentum, 0.1, masters=masters)
+        assert [list(c[2]) for c in calls] == want
+        assert [list(c[1]) for c in calls] == [[buf.param("fc").data_ptr(), buf.param("fc2").data_ptr()], [buf.param("out").data_ptr()]]
+    calls.clear()
+    buf.muon_step(["out"], momentum, 0.1, masters=at(flat, "out"))
+    assert [list(c[2]) for c in calls] == [want[1]]
+
+
+@pytest.mark.gpu
+def test_masters_on_the_buffer():
+    say("case muon on the buffer with masters")
+    g = _gen(13)
+    shapes = {"a": (136, 72), "norm": (136,), "b": (72, 136), "c": (136, 72)}
+    buf = sl.ParamAndGradBuffer(shapes, "cuda", bucket_size=None)
+    buf.grad_data.copy_(_randn(g, buf.numel) * 1e-3)
+    flat = _randn(g, buf.numel) * 0.02
+    buf.param_data.copy_(flat)
+    old, kept, names, momentum = buf.param_data.clone(), flat.clone(), ["a", "b", "c"], torch.zeros_like(buf.grad_data)
+    buf.muon_step(names, momentum, 0.05, masters=flat, weight_decay=0.01)
+    for n in names:
+        s, e, _ = buf.index[n]
+        w, p, m = (t[s:e].clone().view(shapes[n]) for t in (old, kept, torch.zeros_like(momentum)))
+        sl.sl_muon_step(w, buf.main_grad(n), m, 0.05, masters=p, weight_decay=0.01)
+        # alone a matrix takes other tiles than in its group: both are within the iterate's error of the formula
+        step = (p.double() - kept[s:e].view(shapes[n]).double()).norm()
+        assert (flat[s:e].view(shapes[n]).double() - p.double()).norm() <= 2 * OFF * step
+        assert torch.equal(buf.param(n), flat[s:e].view(shapes[n]).to(BF16)) and torch.equal(momentum[s:e], m.view(-1))
+    s, e, _ = buf.index["norm"]
+    assert torch.equal(flat[s:e], kept[s:e]) and torch.equal(buf.param_data[s:e], old[s:e])
