@@ -78,18 +78,22 @@ def linear_with_grad_accumulation(input: torch.Tensor, weight: torch.Tensor) -> 
     return y
 
 
-def _check_copies(copies, n_out, n_in, cols):
-    """Checks (q_rows, s_rows, q_cols, s_cols) against the weight [n_out, n_in] whose copies they are; the
+def _check_copies(kind, copies, n_out, n_in, cols):
+    """Checks (q_rows, s_rows, q_cols, s_cols) against the weight [n_out, n_in] whose copies in MXFP4 or MXFP8 they are; the
     columnwise pair is used, and may not be absent, only with ``cols``."""
+    name = f"weight_{kind}"
     if len(copies) != 4:
-        raise ValueError(f"weight_mxfp4 has {len(copies)} tensors, expected the four of sl_mxfp4_quantize")
+        raise ValueError(f"{name} has {len(copies)} tensors, expected the four of sl_{kind}_quantize")
     if cols and (copies[2] is None or copies[3] is None):
-        raise ValueError("the input gradient needs the weight's columnwise MXFP4 copy")
+        raise ValueError(f"the input gradient needs the weight's columnwise {kind.upper()} copy")
     out_b, in_b = (n_out + 31) // 32, (n_in + 31) // 32
-    shapes = ((n_out, 16 * in_b), (n_out, in_b), (n_in, 16 * out_b), (n_in, out_b))
+    if kind == "mxfp4":
+        shapes = ((n_out, 16 * in_b), (n_out, in_b), (n_in, 16 * out_b), (n_in, out_b))
+    else:
+        shapes = ((n_out, n_in), (n_out, in_b), (n_in, n_out), (n_in, out_b))
     for k, (t, shape) in enumerate(zip(copies, shapes[:4 if cols else 2])):
         if t is None or t.shape != shape:
-            raise ValueError(f"weight_mxfp4[{k}] of a weight [{n_out}, {n_in}] has shape {shape}, "
+            raise ValueError(f"{name}[{k}] of a weight [{n_out}, {n_in}] has shape {shape}, "
                              f"got {None if t is None else tuple(t.shape)}")
 
 
@@ -111,7 +115,7 @@ class LinearMXFP4WithGradAccumulation(torch.autograd.Function):
         if weight.dim() != 2 or input.shape[-1] != weight.shape[1]:
             raise ValueError(f"input of {input.shape[-1]} features by a weight of shape {tuple(weight.shape)}")
         if weight_mxfp4 is not None:
-            _check_copies(weight_mxfp4, *weight.shape, ctx.needs_input_grad[0])
+            _check_copies("mxfp4", weight_mxfp4, *weight.shape, ctx.needs_input_grad[0])
         x2 = input.reshape(-1, input.shape[-1]).contiguous()
         xr, xrs, xc, xcs = sl_mxfp4_quantize(x2, cols=ctx.needs_input_grad[1])
         if weight_mxfp4 is None:
@@ -273,9 +277,9 @@ class NormLinearMXFP8WithGradAccumulation(torch.autograd.Function):
                              "are multiples of 128, the input's of 32")
         if weight_mxfp8 is None:
             weight_mxfp8 = sl_mxfp8_quantize(weight.detach(), cols=need_x)
+        else:
+            _check_copies("mxfp8", weight_mxfp8, n_out, n_in, need_x)
         wr, wrs, wc, wcs = weight_mxfp8
-        if need_x and wc is None:
-            raise ValueError("the input gradient needs the weight's columnwise MXFP8 copy")
         y, h = _result(input, n_out), x2 if residual is None else _result(input, n_in)
         xr, xrs, xc, xcs, _, rstd = sl_rmsnorm_fwd_mxfp8(x2, norm_weight.detach(), eps, residual=r2, cols=need_w,
                                                          h=None if residual is None else _rows(h))

@@ -503,3 +503,40 @@ def test_mxfp8_codes_beside_a_border(S, h, w):
     qr, sr, qc, sc, _, _ = sl.sl_rmsnorm_fwd_mxfp8(x, weight, eps)
     _check_mx(qr, sr, exact, 2.0 ** -45)
     _check_mx(qc, sc, exact.t().contiguous(), 2.0 ** -45)
+
+
+@pytest.mark.parametrize("other", [(256, 64), (128, 96), (64, 128)], ids=["out", "in", "turned"])
+def test_mxfp8_copies_of_another_weight_are_refused(other, monkeypatch):
+    """Before the norm or anything else runs."""
+    from sharded_linear_amd import autograd
+    ran = []
+
+    def norm(x, w, eps, residual=None, rows=True, cols=True, out=None, h=None):
+        ran.append("norm")
+        T, H = x.shape
+        return (*_copies(T, H)[:2], *((_copies(T, H)[2:]) if cols else (None, None)), x if h is None else h, torch.zeros(T))
+
+    monkeypatch.setattr(autograd, "sl_rmsnorm_fwd_mxfp8", norm)
+    monkeypatch.setattr(autograd, "sl_linear_fwd_mxfp8", lambda q, s, wq, ws, Y=None: torch.zeros((q.shape[0], wq.shape[0]), dtype=BF16) if Y is None else Y)
+    monkeypatch.setattr(autograd, "sl_mxfp8_quantize", lambda *a, **k: ran.append("cast"))
+    x = torch.zeros((128, 64), dtype=BF16, requires_grad=True)
+    nw, w = torch.ones(64, dtype=BF16), torch.nn.Parameter(torch.zeros((128, 64), dtype=BF16))
+    w.main_grad = torch.zeros((128, 64))
+    call = lambda copies: sl.norm_linear_mxfp8_with_grad_accumulation(x, nw, w, weight_mxfp8=copies)  # noqa: E731
+    good, bad = _copies(128, 64), _copies(*other)
+    assert call(good).shape == (128, 128) and ran == ["norm"]
+    del ran[:]
+    for mixed in (bad, good[:2] + bad[2:], bad[:2] + good[2:], good[:3], (None, None) + good[2:]):
+        with pytest.raises(ValueError, match="weight_mxfp8"):
+            call(mixed)
+    with pytest.raises(ValueError, match="columnwise MXFP8"):
+        call(good[:2] + (None, None))
+    assert not ran
+    with torch.no_grad():
+        assert call(good[:2] + (None, None)).shape == (128, 128)          # forward alone reads the rowwise copy
+
+
+def _copies(rows, cols):
+    """The shapes of a matrix's MXFP8 copies."""
+    u = lambda *s: torch.zeros(s, dtype=U8)  # noqa: E731
+    return u(rows, cols), u(rows, cols // 32), u(cols, rows), u(cols, rows // 32)
