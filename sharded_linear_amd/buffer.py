@@ -112,7 +112,8 @@ class ParamAndGradBuffer:
 
         The buffer holds one rank's slices, and each is orthogonalised by itself and scaled by its own rows and columns: of a
         tensor-parallel weight this is the block-wise update, not that of the whole matrix.  grad_data is taken as it stands, so it
-        has to be reduced over the data-parallel ranks first."""
+        has to be reduced over the data-parallel ranks first.  Graphs that saved a weight as ``param`` gives it refuse a backward
+        pass after the step; a parameter remapped by ``attach`` is updated as through its ``data``, unseen by them."""
         names = list(names)
         if isinstance(masters, torch.Tensor) and len(names) == 1 and masters.shape == self.shapes[names[0]]:
             masters = [masters]

@@ -775,8 +775,11 @@ def _muon_call(weights, main_grads, momenta, lr, momentum=0.95, nesterov=True, w
         ws, nbytes = _scratch(dev, need, workspace)
         _launch("sl_muon_step", dev, w, p, g, m, len(W), rows, cols, lr, momentum, int(nesterov), weight_decay, scale, steps, k,
                 _addr(ws), nbytes)
+        # as any update in place: a graph that saved a weight refuses to use the new one for the old
+        torch.autograd.graph.increment_version([t for t in written if not t.is_inference()])
 
-    return [t for x in (lists[0], lists[2], lists[3]) for t in x or ()], lists[1], call
+    written = [t for x in (lists[0], lists[2], lists[3]) for t in x or ()]
+    return written, lists[1], call
 
 
 def sl_muon_step(weights, main_grads, momenta, lr, momentum=0.95, nesterov=True, weight_decay=0.0, scale=None, masters=None,

@@ -563,3 +563,29 @@ def test_masters_on_the_buffer():
         assert torch.equal(buf.param(n), flat[s:e].view(shapes[n]).to(BF16)) and torch.equal(momentum[s:e], m.view(-1))
     s, e, _ = buf.index["norm"]
     assert torch.equal(flat[s:e], kept[s:e]) and torch.equal(buf.param_data[s:e], old[s:e])
+
+
+def test_a_graph_that_saved_a_weight_notices_its_step(monkeypatch):
+    """The step writes through addresses; autograd has to learn of it all the same."""
+    from sharded_linear_amd import ops
+    monkeypatch.setattr(ops, "_device", lambda t: t.device)
+    monkeypatch.setattr(ops, "_launch", lambda *a: None)
+    monkeypatch.setattr(ops, "_scratch", lambda *a: (None, 0))
+    w = torch.nn.Parameter(torch.ones((16, 24), dtype=BF16))
+    x = torch.ones((4, 24), dtype=BF16, requires_grad=True)
+    M, G, master = (torch.zeros((16, 24)) for _ in range(3))
+    y = x @ w.t()
+    before = [t._version for t in (M, G, master)]
+    sl.sl_muon_step(w, G, M, 0.1, masters=master)
+    with pytest.raises(RuntimeError, match="inplace"):
+        y.sum().backward()
+    assert [t._version for t in (M, G, master)] == [before[0] + 1, before[1], before[2] + 1]
+    (x @ w.t()).sum().backward()                                          # a graph made after the step
+    with torch.inference_mode():
+        inside = torch.ones((16, 24), dtype=BF16)
+        sl.sl_muon_step(inside, G, M, 0.1)
+    buf, momentum, _ = _host_buffer(monkeypatch, SHAPES_OF_TWO)
+    y = x @ buf.param("out").t()
+    buf.muon_step(["out"], momentum, 0.1)
+    with pytest.raises(RuntimeError, match="inplace"):
+        y.sum().backward()
