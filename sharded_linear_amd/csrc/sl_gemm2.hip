@@ -173,7 +173,13 @@ __global__ void __launch_bounds__(WGM * WGN * 64, OCC) gemm2(Gemm2Args g) {
 template <bool A_KM, bool B_KM, bool ACC, int S, int WGM, int WGN, int BK_, int BN_, int MF>
 __global__ void __launch_bounds__(WGM * WGN * 64, 1) gemm4(Gemm2Args g) {
   using P = G4<A_KM, B_KM, ACC, S, WGM, WGN, BK_, BN_, MF>;
-  constexpr int BK = P::BK, WM = P::WM, WN = P::WN, TM = P::TM, TN = P::TN;
+  constexpr int KS = P::KS;
+  using AccT = std::conditional_t<MF == 32, f32x16, f32x4v>;
+  constexpr int NACC = MF == 32 ? 16 : 4;
+  using OA = typename P::OA;
+  using OB = typename P::OB;
+  constexpr int BK = P::BK, WAVES = P::WAVES, WM = P::WM, WN = P::WN, TM = P::TM, TN = P::TN;
+  constexpr int LA = P::LA, LB = P::LB, LPS = P::LPS, kStage = P::kStage;
   extern __shared__ __attribute__((aligned(1024))) char smem[];
 
   const int tid = threadIdx.x, lane = tid & 63;
@@ -185,8 +191,203 @@ __global__ void __launch_bounds__(WGM * WGN * 64, 1) gemm4(Gemm2Args g) {
   const int nkt = (g.K + BK - 1) / BK;
   const int kt0 = split * g.kt_per_split;
   const int nk = min(nkt, kt0 + g.kt_per_split) - kt0;
-  typename P::AccT acc[TM][TN];
-  gemm4_core<P>(g, smem, lane, wave, m0, n0, kt0, nk, acc);
+  // The k tiles are walked from a starting point that depends on the XCD (blocks are dealt to
+  // the XCDs round-robin): stage j of this split (0 <= j < nk) is k tile kmap(j), a rotation by
+  // (3x mod 8) eighths of the split on XCD x (measured 1 % ahead of x eighths).  Without it every
+  // workgroup of the chip loads the same k column of its rows at the same time; with rows a power
+  // of two apart in HBM (K = 2048 or 8192 bf16), those loads pile onto the same memory channels.
+  // The workgroups of one XCD keep one phase, so the operand panels they share in that XCD's L2
+  // are still loaded once.  Each tile keeps one fixed k order, so results stay deterministic.
+  const int rot = ((((int(blockIdx.x) % kXCD) * 3) % kXCD) * nk) / kXCD;
+  auto kmap = [&](int j) { const int x = j + rot; return kt0 + (x >= nk ? x - nk : x); };
+
+  const i32x4 ra = rsrc(g.a, g.a_bytes), rb = rsrc(g.b, g.b_bytes);
+  // load offsets relative to a stage's first k; the ragged last stage (K % 32 != 0) uses a copy
+  // with the lanes past K sent out of range
+  uint32_t voa[LA], vob[LB], vra[LA], vrb[LB];
+  OA::template prep<WAVES>(voa, lane, wave, m0, g.M, g.lda);
+  OB::template prep<WAVES>(vob, lane, wave, n0, g.N, g.ldb);
+  {
+    const int kr = g.K - (nkt - 1) * BK;          // k extent of the last stage
+#pragma unroll
+    for (int it = 0; it < LA; ++it) {
+      const int p = (it * WAVES + wave) * 64 + lane;
+      const int kk = A_KM ? ((p % OA::kCPR) ^ OA::swz(p / OA::kCPR)) * 8 : p / OA::kCPR;
+      vra[it] = kk < kr ? voa[it] : kOOB;
+    }
+#pragma unroll
+    for (int it = 0; it < LB; ++it) {
+      const int p = (it * WAVES + wave) * 64 + lane;
+      const int kk = B_KM ? ((p % OB::kCPR) ^ OB::swz(p / OB::kCPR)) * 8 : p / OB::kCPR;
+      vrb[it] = kk < kr ? vob[it] : kOOB;
+    }
+  }
+  const uint32_t ka_step = A_KM ? BK * 2 : uint32_t(BK * g.lda * 2);
+  const uint32_t kb_step = B_KM ? BK * 2 : uint32_t(BK * g.ldb * 2);
+  const uint32_t lds0 = lds_addr(smem);
+
+  // fragment read offsets (per lane), K-major: one per MFMA step; MN-major: one per fragment
+  constexpr int NPS = BK / KS;
+  uint32_t ofa[A_KM ? NPS : TM], ofb[B_KM ? NPS : TN];
+  auto kfo_a = [&](int ks) { return MF == 32 ? kmaj_frag_off<OA>(wm * WM, ks, lane) : kmaj_frag_off16<OA>(wm * WM, ks, lane); };
+  auto kfo_b = [&](int ks) { return MF == 32 ? kmaj_frag_off<OB>(wn * WN, ks, lane) : kmaj_frag_off16<OB>(wn * WN, ks, lane); };
+  auto mfo_a = [&](int f0) { return MF == 32 ? mnmaj_frag_off<OA>(f0, lane) : mnmaj_frag_off16<OA>(f0, lane); };
+  auto mfo_b = [&](int f0) { return MF == 32 ? mnmaj_frag_off<OB>(f0, lane) : mnmaj_frag_off16<OB>(f0, lane); };
+  if constexpr (A_KM)
+#pragma unroll
+    for (int ks = 0; ks < NPS; ++ks) ofa[ks] = kfo_a(ks);
+  else
+#pragma unroll
+    for (int i = 0; i < TM; ++i) ofa[i] = mfo_a(wm * WM + MF * i);
+  if constexpr (B_KM)
+#pragma unroll
+    for (int ks = 0; ks < NPS; ++ks) ofb[ks] = OA::kBytes + kfo_b(ks);
+  else
+#pragma unroll
+    for (int j = 0; j < TN; ++j) ofb[j] = OA::kBytes + mfo_b(wn * WN + MF * j);
+
+  AccT acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int r = 0; r < NACC; ++r) acc[i][j][r] = 0.f;
+  bf16x8 fa[2][TM], fb[2][TN];
+
+  // fragment i (A) or j (B) of MFMA step ks from the stage at LDS byte `base`
+  auto read_a = [&](bf16x8& d, uint32_t base, auto ic_i, auto ic_ks) {
+    constexpr int i = decltype(ic_i)::value, ks = decltype(ic_ks)::value;
+    if constexpr (A_KM) d = lds_rd128<i * MF * OA::kRowBytes>(base + ofa[ks]);
+    else d = lds_rd_tr<ks * KS * OA::kRowBytes, (ks * KS + 4) * OA::kRowBytes>(base + ofa[i]);
+  };
+  auto read_b = [&](bf16x8& d, uint32_t base, auto ic_j, auto ic_ks) {
+    constexpr int j = decltype(ic_j)::value, ks = decltype(ic_ks)::value;
+    if constexpr (B_KM) d = lds_rd128<j * MF * OB::kRowBytes>(base + ofb[ks]);
+    else d = lds_rd_tr<ks * KS * OB::kRowBytes, (ks * KS + 4) * OB::kRowBytes>(base + ofb[j]);
+  };
+  // wave-load `l` (A: l < LA, then B) of the stage at k tile kt into LDS slot `slot`
+  auto load_one = [&](auto ic_l, int kt, int slot, bool ragged) {
+    constexpr int l = decltype(ic_l)::value;
+    const uint32_t base = lds0 + slot * kStage;
+    if constexpr (l < LA) {
+      lds_dma16s(ra, base + (l * WAVES + wave) * 1024, ragged ? vra[l] : voa[l], uint32_t(kt) * ka_step);
+    } else {
+      constexpr int lb = l - LA;
+      lds_dma16s(rb, base + OA::kBytes + (lb * WAVES + wave) * 1024, ragged ? vrb[lb] : vob[lb], uint32_t(kt) * kb_step);
+    }
+  };
+  // Memory operation m of a step: m < NR reads fragment piece m into buffer NX; after that the
+  // loads [L0, L0 + LPS/2) (or all LPS when ONE) of stage kt into slot `slot` (when `loads`).
+  // ONE (the 16x16 kernels): a stage's loads all go out in the step right after the barrier that
+  // frees its slot.  Under the 16x16 instruction the part clocks higher, a stage takes less time,
+  // and loads issued a step later than that no longer land before the barrier that waits for them.
+  constexpr bool ONE = MF == 16;
+  constexpr int NR = TM + TN, LH = LPS / 2;
+  static_assert(ONE || LPS % 2 == 0, "loads split over two steps");
+  auto memop = [&](auto ic_m, auto ic_nx, auto ic_ks, auto ic_l0, uint32_t rbase, bool loads, int kt, int slot,
+                   bool ragged) {
+    constexpr int m = decltype(ic_m)::value, nx = decltype(ic_nx)::value, l0 = decltype(ic_l0)::value;
+    if constexpr (m < NR) {
+      if constexpr (m < TM) read_a(fa[nx][m], rbase, ic<m>{}, ic_ks);
+      else read_b(fb[nx][m - TM], rbase, ic<m - TM>{}, ic_ks);
+    } else {
+      if (loads) load_one(ic<l0 + m - NR>{}, kt, slot, ragged);
+    }
+  };
+  // One MFMA step: TM x TN MFMAs on buffer CUR with NM memory operations among them.  The
+  // fragment reads go out over the first three quarters of the MFMAs, so they have landed when
+  // the step ends (the stage barrier waits for them); the loads are spread evenly over the whole
+  // step, one every NQ/NL MFMAs, which keeps the texture-address queue from filling.
+  auto step = [&](auto ic_cur, auto ic_nm, auto&& mem) {
+    constexpr int cur = decltype(ic_cur)::value, NM = decltype(ic_nm)::value;
+    // MFMAs row by row over the A fragments, the B fragments in serpentine order (odd rows run j
+    // backwards), so that every MFMA shares an operand with the one before it: the part is held
+    // at its power limit, and fewer operand changes measured 0.3-0.6 % faster per launch on every
+    // product.
+    static_for<TM * TN>([&](auto qc) {
+      constexpr int q = decltype(qc)::value, i = q / TN, j = (i & 1) ? TN - 1 - q % TN : q % TN;
+      if constexpr (MF == 32)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[cur][j], fa[cur][i], acc[i][j], 0, 0, 0);
+      else
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[cur][j], fa[cur][i], acc[i][j], 0, 0, 0);
+      constexpr int NQ = TM * TN, NRD = NR < NM ? NR : NM, NL = NM - NRD;
+      constexpr int RQ = NQ * 3 / 4 > 0 ? NQ * 3 / 4 : 1;
+      constexpr int rlo = q < RQ ? q * NRD / RQ : NRD, rhi = q < RQ ? (q + 1) * NRD / RQ : NRD;
+      static_for<rhi - rlo>([&](auto mc) { mem(ic<rlo + decltype(mc)::value>{}); });
+      constexpr int llo = NL ? (2 * q * NL + NQ) / (2 * NQ) : 0, lhi = NL ? (2 * (q + 1) * NL + NQ) / (2 * NQ) : 0;
+      static_for<lhi - llo>([&](auto mc) { mem(ic<NRD + llo + decltype(mc)::value>{}); });
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  };
+
+  {
+    // Prologue: stages 0..S-2 and the first half of stage S-1, or all S stages when ONE (the host
+    // launches this kernel only when every split has at least S stages).  From then on the loads of
+    // stage x are issued in the last step of stage x - S (just after the barrier that frees its
+    // slot): all of them when ONE, else the first half there and the second in the first step of
+    // stage x - S + 1.  Either way, at barrier B(s+1) the loads issued after stage s + 1's are the
+    // S - 2 whole stages s + 2 .. s + S - 1.
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      const bool rag = kmap(s) == nkt - 1;
+      if (ONE || s < S - 1) static_for<LPS>([&](auto lc) { load_one(lc, kmap(s), s, rag); });
+      else static_for<LH>([&](auto lc) { load_one(lc, kmap(s), s, rag); });
+    }
+    // stage 0 is complete once at most the later prologue stages' loads (S - 1 of them, the last
+    // one only half issued unless ONE) are outstanding
+    asm_wait_vm<ONE ? LPS * (S - 1) : LPS * (S - 2) + LH>();
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    static_for<TM>([&](auto ic_i) { read_a(fa[0][decltype(ic_i)::value], lds0, ic_i, ic<0>{}); });
+    static_for<TN>([&](auto ic_j) { read_b(fb[0][decltype(ic_j)::value], lds0, ic_j, ic<0>{}); });
+    __builtin_amdgcn_sched_barrier(0);
+
+    // Stage s: steps 0 .. NPS-2, each on buffer t % 2 and reading step t + 1 into the other (the
+    // first also issues the second half of stage s + S - 1); barrier; the last step on buffer 1
+    // (NPS is even), reading the next stage's step 0 into buffer 0 and issuing the first half of
+    // stage s + S into s's slot.  At the barrier the loads issued after the last one of stage
+    // s + 1 are the S - 2 whole stages s + 2 .. s + S - 1.
+    constexpr int NPS_ = BK / KS;
+    static_assert(NPS_ % 2 == 0, "steps per stage");
+    auto stage = [&](int s, auto ic_vm, auto ic_la, auto ic_lb, auto ic_last) {
+      constexpr int VM = decltype(ic_vm)::value;
+      constexpr bool LDA = decltype(ic_la)::value, LDB = decltype(ic_lb)::value, LAST = decltype(ic_last)::value;
+      const int slot = s % S;
+      const uint32_t cur = lds0 + slot * kStage;
+      static_for<NPS_ - 1>([&](auto tc) {
+        constexpr int t = decltype(tc)::value;
+        constexpr bool ld = !ONE && LDA && t == 0;
+        const int kt = kmap(s + S - 1), lslot = (s + S - 1) % S;
+        const bool rag = kt == nkt - 1;
+        step(ic<t % 2>{}, ic<ld ? NR + LH : NR>{},
+             [&](auto ic_m) { memop(ic_m, ic<(t + 1) % 2>{}, ic<t + 1>{}, ic<LH>{}, cur, ld, kt, lslot, rag); });
+      });
+      if constexpr (!LAST) {
+        asm_wait_vm<VM>();
+        asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        const uint32_t nxt = lds0 + ((s + 1) % S) * kStage;
+        const int kt = kmap(s + S);
+        const bool rag = kt == nkt - 1;
+        step(ic<1>{}, ic<LDB ? NR + (ONE ? LPS : LH) : NR>{},
+             [&](auto ic_m) { memop(ic_m, ic<0>{}, ic<0>{}, ic<0>{}, nxt, LDB, kt, slot, rag); });
+      } else {
+        step(ic<1>{}, ic<0>{}, [&](auto) {});
+      }
+    };
+    using T_ = std::true_type;
+    using F_ = std::false_type;
+    for (int s = 0; s < nk - S; ++s) stage(s, ic<LPS * (S - 2)>{}, T_{}, T_{}, F_{});
+    // The last S stages issue no new stages (the first still completes stage nk - 1); stage
+    // nk-S+j waits for stage nk-S+j+1, after which S-2-j whole stages remain outstanding.
+    static_for<S>([&](auto jc) {
+      constexpr int j = decltype(jc)::value;
+      if constexpr (j == S - 1) stage(nk - S + j, ic<0>{}, std::bool_constant<j == 0>{}, F_{}, T_{});
+      else stage(nk - S + j, ic<(S - 2 - j) * LPS>{}, std::bool_constant<j == 0>{}, F_{}, F_{});
+    });
+  }
   asm_wait_vm<0>();
   __syncthreads();    // every wave is past its last operand read: the ring becomes epilogue space
   if constexpr (MF == 32) store_tile<WM, WN, TM, TN, ACC>(g, acc, smem, m0 + wm * WM, n0 + wn * WN, split, lane, wave);
