@@ -15,6 +15,10 @@
 // 1.32 PFLOP/s, matrix units 0.66 busy), 307 to 318 with it read and written; of 16 x [1536, 2048] 137 to 140 and 162 to 165 in
 // three rounds.
 //
+// The kernels that add D and the diagonal (b A + c A^2 + a I) do not fit their registers: 62 and 50 scalar ones are spilled, with 24
+// bytes of scratch a lane that every piece of the epilogue reads back, and their join takes 126 registers where the others take 61
+// to 64.  The kernels that keep what roundings left spill 12 and 5 scalar ones; the rest spill none or 2.
+//
 // Tiles of 256 x 256 are dealt out in whole rounds of the chip; what remains, or the whole of a small product, goes to
 // tiles of 128 x 128 in a launch of its own, and where its last round would leave places idle, sums are split into fp32
 // planes (kept in the accumulators' own order, whole lines a store) which another kernel adds in order and finishes through

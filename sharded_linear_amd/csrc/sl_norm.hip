@@ -428,9 +428,10 @@ int check_norm(int64_t T, int64_t H, float eps) {
 }
 
 // Threads to a row: a wave while its lanes hold the row in 4 chunks each and there are rows enough for the chip, else
-// a workgroup.  Forward with a residual and gradient, in us, with 64 and with 256 threads: [1, 2048] 4.1 and 6.7, 4.0 and 5.7;
-// [512, 2048] 4.8 and 7.8, 4.7 and 9.1; [8192, 2048] 25.0 and 23.3, 23.8 and 27.4; [8192, 512] 8.2 and 10.8, 11.0 and 18.3.  With
-// 256 and with 1024: [8192, 4096] 41.8 and 37.4, 47.6 and 56.7; [8192, 8192] 94.1 and 80.5, 92.6 and 84.1.
+// a workgroup.  One rule serves the forward (with a residual) and the gradient; in us, forward + gradient, with 64 threads and with
+// 256: [1, 2048] 4.1 + 6.7, 4.0 + 5.7; [512, 2048] 4.8 + 7.8, 4.7 + 9.1 (here the rule takes the slower); [8192, 2048] 25.0 +
+// 23.3, 23.8 + 27.4; [8192, 512] 8.2 + 10.8, 11.0 + 18.3.  With 256 and with 1024: [8192, 4096] 41.8 + 37.4, 47.6 + 56.7;
+// [8192, 8192] 94.1 + 80.5, 92.6 + 84.1.
 int row_threads(int64_t T, int chunks) {
   if (chunks <= 256 && (T >= 1024 || chunks <= 64)) return 64;
   return chunks <= 1024 ? 256 : 1024;
