@@ -21,7 +21,8 @@ from .ops import (sl_embedding_fwd, sl_embedding_wgrad_accum, sl_linear_dgrad, s
 # A leaf has one gradient accumulator for all its living graphs, and it belongs to the stream on which it was made.  The functions below
 # leave a weight's gradient in main_grad and return none, so a captured backward pass meets the accumulator's stream only at its
 # end, where the engine joins that stream to the capture: if it is not the capture's, that ends the process.  So the functions
-# note the stream on the accumulators that they meet, and refuse a capture that meets one noted on another.  What they
+# note the stream on the accumulators that they meet, and refuse what a capture would do beside one noted on another: the
+# linear functions their backward pass, the others the forward pass already, with the other leaves that they meet.  What they
 # cannot know: an accumulator that other operators made, of a graph in which none of these functions has met the leaf, or
 # on another stream than that of the first of these calls; and leaves behind an operator that comes before the call.
 
@@ -29,7 +30,7 @@ def _refuse_foreign_accumulators(*leaves):
     """Raises, while a graph is captured, for a leaf whose accumulator was noted on another stream."""
     for t in leaves:
         if t is not None and t.requires_grad and t.is_leaf and t.is_cuda:
-            if not torch.is_grad_enabled() or not torch.cuda.is_current_stream_capturing():
+            if not torch.cuda.is_current_stream_capturing():
                 return
             stream = _raw_stream(t.device.index)
             if torch.autograd.graph.get_gradient_edge(t).node.metadata.get("sl_stream", stream) != stream:
@@ -38,15 +39,12 @@ def _refuse_foreign_accumulators(*leaves):
                                    "a backward pass cannot be captured beside it")
 
 
-_AccumulateGrad = torch._C._functions.AccumulateGrad
-
-
 def _note_accumulators(out):
     """Notes the current stream on the accumulators next to the node that made ``out``."""
     fn = out.grad_fn
     if fn is not None and out.is_cuda:
         for node, _ in fn.next_functions:
-            if node.__class__ is _AccumulateGrad:
+            if node.__class__.__name__ == "AccumulateGrad":
                 node.metadata.setdefault("sl_stream", _raw_stream(out.device.index))
 
 
@@ -63,6 +61,7 @@ class LinearWithGradAccumulation(torch.autograd.Function):
     @staticmethod
     def backward(ctx, grad_output: torch.Tensor):
         input, weight = ctx.saved_tensors
+        _refuse_foreign_accumulators(weight)
         dy = grad_output.reshape(-1, grad_output.shape[-1]).contiguous()
         x2 = input.reshape(-1, input.shape[-1]).contiguous()
         dx = sl_linear_dgrad(dy, weight.detach())
@@ -72,7 +71,6 @@ class LinearWithGradAccumulation(torch.autograd.Function):
 
 
 def linear_with_grad_accumulation(input: torch.Tensor, weight: torch.Tensor) -> torch.Tensor:
-    _refuse_foreign_accumulators(weight)
     y = LinearWithGradAccumulation.apply(input, weight)
     _note_accumulators(y)
     return y
@@ -130,6 +128,7 @@ class LinearMXFP4WithGradAccumulation(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, grad_output):
         weight, xc, xcs, wc, wcs = ctx.saved_tensors
+        _refuse_foreign_accumulators(weight)
         dy = grad_output.reshape(-1, grad_output.shape[-1]).contiguous()
         need_x, need_w = ctx.needs_input_grad[:2]
         dr, drs, dc, dcs = sl_mxfp4_quantize(dy, rows=need_x, cols=need_w, seed=ctx.seed)
@@ -146,7 +145,6 @@ def linear_mxfp4_with_grad_accumulation(input: torch.Tensor, weight: torch.Tenso
     rounds dY stochastically, which keeps the gradients unbiased; a training loop gives every call its
     own.  ``weight_mxfp4`` is sl_mxfp4_quantize(weight), made once and passed to every micro-batch that
     uses the same weight; without it the weight is cast in each call."""
-    _refuse_foreign_accumulators(weight)
     y = LinearMXFP4WithGradAccumulation.apply(input, weight, seed, weight_mxfp4)
     _note_accumulators(y)
     return y
@@ -178,9 +176,10 @@ class EmbeddingWithGradAccumulation(torch.autograd.Function):
 def embedding_with_grad_accumulation(ids: torch.Tensor, weight: torch.Tensor, vocab_start: int = 0, scale: float = 1.0) -> torch.Tensor:
     """Rows of the table shard ``weight`` [V, H] for ids of any shape, times ``scale``; zeros for ids of other ranks (outside
     vocab_start .. vocab_start + V - 1), so that the ranks' results add up.  Backward adds into weight.main_grad."""
-    if not torch.is_grad_enabled():
+    if torch.is_grad_enabled():
+        _refuse_foreign_accumulators(weight)
+    else:
         weight = weight.detach()
-    _refuse_foreign_accumulators(weight)
     y = EmbeddingWithGradAccumulation.apply(ids, weight, vocab_start, scale)
     _note_accumulators(y)
     return y
@@ -242,9 +241,10 @@ def rmsnorm_with_grad_accumulation(input: torch.Tensor, weight: torch.Tensor, re
     """The root-mean-square norm of ``input`` over its last axis, or of h = input + residual: returns y, or (y, h), h being
     the residual stream that the next block adds to (out of place: backward reads h, and refuses one that was modified).  The
     weight's gradient goes to weight.main_grad."""
-    if not torch.is_grad_enabled():
+    if torch.is_grad_enabled():
+        _refuse_foreign_accumulators(input, weight, residual)
+    else:
         weight = weight.detach()
-    _refuse_foreign_accumulators(input, weight, residual)
     out = RMSNormWithGradAccumulation.apply(input, weight, residual, eps)
     _note_accumulators(out if residual is None else out[0])
     return out
@@ -311,7 +311,8 @@ def norm_linear_mxfp8_with_grad_accumulation(input: torch.Tensor, norm_weight: t
     """Y = norm(input + residual) . weight^T with every product of the step on MXFP8 operands: returns Y, or (Y, h) with a
     residual, h = input + residual (which backward reads again).  Both weights' gradients go to their main_grad.  ``weight_mxfp8`` is
     sl_mxfp8_quantize(weight), made once and passed to every micro-batch; without it the weight is quantised in each call."""
-    _refuse_foreign_accumulators(input, norm_weight, residual, weight)
+    if torch.is_grad_enabled():
+        _refuse_foreign_accumulators(input, norm_weight, residual, weight)
     out = NormLinearMXFP8WithGradAccumulation.apply(input, norm_weight, residual, weight, eps, weight_mxfp8)
     _note_accumulators(out if residual is None else out[0])
     return out

@@ -312,11 +312,10 @@ def _linear_calls(g):
 
 
 @pytest.mark.gpu
-@pytest.mark.filterwarnings("ignore:The CUDA Graph is empty")
 @pytest.mark.parametrize("name", ["linear", "mxfp4"])
 def test_captured_linear_gradients(name):
-    """The linear functions leave a weight's gradient in main_grad as the others do: a capture beside a living eager graph of the same weight
-    is refused, and without one its gradients are the eager ones."""
+    """The linear functions leave a weight's gradient in main_grad as the others do: a captured backward pass beside a living eager graph of
+    the same weight is refused, a captured forward pass is not; without such a graph the captured gradients are the eager ones."""
     say(f"case captured gradients of {name}")
     buf, w, x, c, calls = _linear_calls(_gen(4))
     call = calls[name]
@@ -326,11 +325,19 @@ def test_captured_linear_gradients(name):
         torch.autograd.grad(y, w, c, allow_unused=True)
         return y.detach()
 
-    eager = call()
-    with pytest.raises(RuntimeError, match="drop its results"):
-        with torch.cuda.graph(torch.cuda.CUDAGraph()):
-            call()
-    del eager
+    eager, graph = call(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = call()
+        with pytest.raises(RuntimeError, match="drop its results"):
+            torch.autograd.grad(y, w, c, allow_unused=True)
+    y = y.detach()
+    for k in range(2):
+        x.copy_(_bf16(_gen(20 + k), *x.shape))
+        graph.replay()
+        want = call()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want.detach()) and not buf.grad_data.any()
+    del eager, want
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(s):
@@ -358,20 +365,21 @@ def test_capture_beside_a_graph_of_another_function():
     g = _gen(6)
     buf = sl.ParamAndGradBuffer({"table": (304, 256)}, "cuda", bucket_size=None)
     w = buf.attach("table", torch.nn.Parameter(_bf16(g, 304, 256)))
-    ids, x = torch.randint(0, 304, (64,), generator=g, device="cuda"), _bf16(g, 32, 256)
-    lookup, product = lambda: sl.embedding_with_grad_accumulation(ids, w), lambda: sl.linear_with_grad_accumulation(x, w)
-    for first, second in ((lookup, product), (product, lookup)):          # a tied table
+    ids, x, c = torch.randint(0, 304, (64,), generator=g, device="cuda"), _bf16(g, 32, 256), _bf16(g, 32, 304)
+    lookup = lambda: sl.embedding_with_grad_accumulation(ids, w)  # noqa: E731
+    product = lambda: torch.autograd.grad(sl.linear_with_grad_accumulation(x, w), w, c, allow_unused=True)  # noqa: E731
+    for first, second in ((lookup, product), (lambda: sl.linear_with_grad_accumulation(x, w), lookup)):          # a tied table
         eager = first()
-        with pytest.raises(RuntimeError, match="drop its results"):
-            with torch.cuda.graph(torch.cuda.CUDAGraph()):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            with pytest.raises(RuntimeError, match="drop its results"):
                 second()
         del eager
         with torch.cuda.graph(torch.cuda.CUDAGraph()):
             second()
     node = torch.autograd.graph.get_gradient_edge(w).node
     lookup()
-    with pytest.raises(RuntimeError, match="hook"):
-        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+    with torch.cuda.graph(torch.cuda.CUDAGraph()):
+        with pytest.raises(RuntimeError, match="hook"):
             lookup()
     del node
     with torch.cuda.graph(torch.cuda.CUDAGraph()):
@@ -384,6 +392,7 @@ def test_capture_beside_a_graph_of_another_function():
         s.synchronize()
         with torch.cuda.graph(torch.cuda.CUDAGraph(), stream=s):
             lookup()
+            product()
     assert eager.requires_grad
 
 
