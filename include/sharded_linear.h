@@ -409,7 +409,8 @@ int sl_rmsnorm_bwd(void* stream, const void* dY, const void* h, const void* w, c
  *   M <- momentum * M + G;   U = nesterov ? G + momentum * M : M
  *   W <- (1 - lr * weight_decay) * W - lr * scale * X   (of the master where there is one, which is then rounded to W)
  * lr, momentum, weight_decay and scale must be finite, steps 0 .. 64 (SL_EINVAL); L <= 65535 and a padded matrix under
- * 2 GiB in fp16 (SL_ESHAPE).  All matrices are 16-byte aligned.  Both take a workspace of the query's bytes, as above.
+ * 2 GiB in fp16 (SL_ESHAPE).  Matrices are 16-byte aligned, or as slices of a 16-byte aligned
+ * batch are: to their elements' bytes where cols % 4 != 0, bf16 ones of odd rows to 8 bytes where cols % 8 == 4.  Both take a workspace of the query's bytes, as above.
  * sl_orthogonalize_tiles (host only, for measurement and tests): how the three products of a step, X.X^T, A.A and P.X, are
  * taken apart, tiles[12] = for each the number of 256x256 tiles, of 128x128 tiles, of the latter with split sums, and of
  * their parts (1: none are split); zeros where the steps go to the kernels for few rows.

@@ -221,7 +221,13 @@ constexpr int64_t kMaxExtent = int64_t(1) << 31;
 constexpr int64_t kMaxBytes = 0x7FFFFFF0LL - 16;         // of one fp16 matrix: the products' 32-bit offsets
 constexpr int kMaxSteps = 64;
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & uintptr_t(bytes - 1)) == 0; }
+
+// What a slice of a 16-byte aligned batch has: four elements are loaded at once where rows begin at multiples of four (bf16 slices
+// then begin at multiples of 8 bytes), others element by element.
+bool aligned_matrix(const void* p, int64_t rows, int64_t cols, int bytes) {
+  return aligned(p, cols % 4 ? bytes : rows % 2 * (cols % 8) * bytes % 16 ? 8 : 16);
+}
 
 struct OrthoPlan {
   int64_t mp, np;
@@ -399,8 +405,8 @@ extern "C" int sl_orthogonalize(void* stream, const void* G, int32_t g_bytes, vo
   if ((e = check_steps(steps, coeffs))) return e;
   if (L == 0 || rows == 0 || cols == 0) return SL_OK;
   if (!G || !O) return SL_EINVAL;
-  if (!aligned16(G) || !aligned16(O)) return SL_EALIGN;
-  if (!workspace || !aligned16(workspace) || workspace_bytes < size_t(p.bytes)) return SL_EWORKSPACE;
+  if (!aligned_matrix(G, rows, cols, g_bytes) || !aligned_matrix(O, rows, cols, 2)) return SL_EALIGN;
+  if (!workspace || !aligned(workspace, 16) || workspace_bytes < size_t(p.bytes)) return SL_EWORKSPACE;
   const hipStream_t st = static_cast<hipStream_t>(stream);
   PassArgs a{};
   a.rows = rows; a.cols = cols; a.mp = int(p.mp); a.np = int(p.np);
@@ -439,9 +445,11 @@ extern "C" int sl_muon_step(void* stream, void* const* W, float* const* master, 
   if (!W || !G || !M) return SL_EINVAL;
   for (int64_t i = 0; i < L; ++i) {
     if (!W[i] || !G[i] || !M[i] || (master && !master[i])) return SL_EINVAL;
-    if (!aligned16(W[i]) || !aligned16(G[i]) || !aligned16(M[i]) || (master && !aligned16(master[i]))) return SL_EALIGN;
+    if (!aligned_matrix(W[i], rows, cols, 2) || !aligned_matrix(G[i], rows, cols, 4) || !aligned_matrix(M[i], rows, cols, 4) ||
+        (master && !aligned_matrix(master[i], rows, cols, 4)))
+      return SL_EALIGN;
   }
-  if (!workspace || !aligned16(workspace) || workspace_bytes < size_t(p.bytes)) return SL_EWORKSPACE;
+  if (!workspace || !aligned(workspace, 16) || workspace_bytes < size_t(p.bytes)) return SL_EWORKSPACE;
   const hipStream_t st = static_cast<hipStream_t>(stream);
   PassArgs a{};
   a.rows = rows; a.cols = cols; a.mp = int(p.mp); a.np = int(p.np);

@@ -800,7 +800,9 @@ def _muon_steps(groups, lr, momentum=0.95, nesterov=True, weight_decay=0.0, scal
     that a refusal leaves every weight and momentum as it was."""
     calls = [_muon_call(w, g, m, lr, momentum, nesterov, weight_decay, scale, p, steps, coefficients, workspace) for w, g, m, p in groups]
     _want_apart([t for c in calls for t in c[0]], [t for c in calls for t in c[1]])
-    if any(t.data_ptr() % 16 for c in calls for t in c[0] + c[1] if t.numel()):
+    # as slices of an aligned batch are: by whole groups of four elements, or by elements
+    unit = lambda t: t.element_size() if t.shape[1] % 4 else 8 if t.nbytes % 16 else 16  # noqa: E731
+    if any(t.data_ptr() % unit(t) for c in calls for t in c[0] + c[1] if t.numel()):
         check("sl_muon_step", SL_EALIGN)
     for w, _, _, _ in groups:
         if w[0].numel():

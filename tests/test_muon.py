@@ -517,7 +517,7 @@ def test_step_on_the_buffer_is_refused_before_anything_is_launched(names, option
 def test_step_on_a_buffer_without_alignment_is_refused_as_a_whole(monkeypatch):
     buf, momentum, calls = _host_buffer(monkeypatch, {"b": (3, 5), "a": (16, 24)}, param_align=1)
     assert buf.main_grad("b").data_ptr() % 16 == 0 and buf.param("b").data_ptr() % 16 == 0
-    buf, momentum, calls = _host_buffer(monkeypatch, {"c": (3, 3), "b": (3, 5), "a": (16, 24)}, param_align=1)
+    buf, momentum, calls = _host_buffer(monkeypatch, {"c": (3, 4), "b": (3, 5), "a": (16, 24)}, param_align=1)
     with pytest.raises(RuntimeError, match="EALIGN"):
         buf.muon_step(["a", "c"], momentum, 0.1)
     assert not calls
@@ -589,3 +589,51 @@ def test_a_graph_that_saved_a_weight_notices_its_step(monkeypatch):
     buf.muon_step(["out"], momentum, 0.1)
     with pytest.raises(RuntimeError, match="inplace"):
         y.sum().backward()
+
+
+# ---- matrices at any address ----------------------------------------------------------------------
+
+def test_alignment_of_matrices():
+    """Rows of whole groups of four elements are loaded by groups, others element by element."""
+    L = _lib.lib()
+    f, k = L.sl_orthogonalize, _arr(*COEFFS * 5)
+    for cols, g_bytes, at, ok in ((61, 4, 4, True), (61, 4, 2, False), (61, 2, 2, True), (61, 2, 1, False), (62, 4, 8, True), (60, 4, 8, False),
+                                  (64, 2, 8, False)):
+        assert f(None, A + at, g_bytes, A, 1, 100, cols, 5, k, None, 0) == (EWORKSPACE if ok else EALIGN), (cols, at)
+    assert f(None, A, 4, A + 2, 1, 100, 61, 5, k, None, 0) == EWORKSPACE and f(None, A, 4, A + 1, 1, 100, 61, 5, k, None, 0) == EALIGN
+    P = lambda *v: (ctypes.c_void_p * len(v))(*v)  # noqa: E731
+    step = lambda cols, *at: L.sl_muon_step(None, P(A + at[0]), P(A + at[1]), P(A + at[2]), P(A + at[3]), 1, 100, cols, 0.1, 0.9, 1,  # noqa: E731
+                                            0.0, 1.0, 5, k, None, 0)
+    assert step(61, 2, 4, 12, 8) == EWORKSPACE and step(60, 16, 32, 0, 16) == EWORKSPACE
+    odd = lambda w, g: L.sl_muon_step(None, P(A + w), None, P(A + g), P(A), 1, 33, 12, 0.1, 0.9, 1, 0.0, 1.0, 5, k, None, 0)  # noqa: E731
+    assert odd(8, 0) == EWORKSPACE and odd(4, 0) == EALIGN and odd(0, 8) == EALIGN
+    assert f(None, A + 8, 2, A + 8, 1, 33, 12, 5, k, None, 0) == EWORKSPACE and f(None, A + 8, 2, A, 1, 33, 16, 5, k, None, 0) == EALIGN
+    for j in range(4):
+        at = [0] * 4
+        at[j] = 1 if j == 0 else 2
+        assert step(61, *at) == EALIGN, j
+        at[j] = 8
+        assert step(60, *at) == EALIGN, j
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("L,rows,cols", [(3, 5, 7), (5, 33, 35), (4, 101, 59), (3, 61, 130), (2, 301, 333), (2, 1, 3), (3, 33, 12), (2, 101, 300)])
+def test_slices_of_batches(L, rows, cols):
+    """Slices of a batch begin at any element; each is stepped as its copy at an address of its own, bit for bit."""
+    say(f"case muon on slices {L} x [{rows}, {cols}]")
+    g = _gen(L * rows)
+    W, G, M, P = (_randn(g, L, rows, cols) * s for s in (0.02, 1e-3, 1e-2, 0.02))
+    W = W.to(BF16)
+    copies = [[t[l].clone() for l in range(L)] for t in (W, G, M, P)]
+    assert any(t[l].data_ptr() % 16 for t in (W, G, M, P) for l in range(L))
+    O = sl.sl_orthogonalize(G)
+    for dtype in (F32, BF16):
+        x = G.to(dtype)
+        out = torch.zeros((L, rows, cols), dtype=BF16, device="cuda")
+        sl.sl_orthogonalize(x[L - 1], out=out[L - 1])
+        assert torch.equal(out[L - 1], sl.sl_orthogonalize(x[L - 1].clone())) and not out[:L - 1].any()
+    sl.sl_muon_step(list(W.unbind(0)), list(G.unbind(0)), list(M.unbind(0)), 0.02, masters=list(P.unbind(0)), weight_decay=0.1)
+    sl.sl_muon_step(*copies[:3], 0.02, masters=copies[3], weight_decay=0.1)
+    for t, c in zip((W, G, M, P), copies):
+        assert all(torch.equal(t[l], c[l]) for l in range(L))
+    assert torch.isfinite(P).all() and O.shape == G.shape
