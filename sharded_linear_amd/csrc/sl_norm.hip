@@ -153,7 +153,7 @@ struct FwdArgs {
   float eps;
 };
 
-// With a residual, rowwise MXFP8: [8192, 2048] 22.1 us, 118 MB, 5.3 TB/s, as a copy; one row of 4096 2.7 us, the launch.
+// With a residual, rowwise MXFP8: [8192, 2048] 21.7 us, 118 MB, 5.4 TB/s, as a copy; one row of 4096 2.8 us, the launch.
 template <int TPR, int NC, bool RES, int OUT>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_fwd(FwdArgs g) {
   constexpr int ROWS = TPR < 256 ? 256 / TPR : 1;
@@ -227,8 +227,8 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_fwd(FwdArgs g) {
 // ---- columnwise MXFP8 copy -----------------------------------------------------------------------
 // One workgroup takes a 128 x 128 tile of h: rows of 16-byte chunks into LDS, from which each thread reads two blocks
 // of 32 rows down a column by transposing reads, scales them (rstd by row, w by column) and encodes them; codes leave
-// as whole 128-byte lines of the transposed copy.  The LDS layout is the quantiser's (sl_quant.hip).  [8192, 2048]: 15.1 us,
-// 51 MB, 3.4 TB/s; rstd needs whole rows before the first column, so h is read again here (from the last-level cache).
+// as whole 128-byte lines of the transposed copy.  The LDS layout is the quantiser's (sl_quant.hip).  [8192, 2048]: 16.5 us,
+// 51 MB, 3.1 TB/s, of which the search for borders takes about 2; rstd needs whole rows before the first column, so h is read again here (from the last-level cache).
 constexpr int kTile = 128, kStride = kTile + 16;
 
 __global__ void __launch_bounds__(256) norm_cols(const uint16_t* __restrict__ h, const uint16_t* __restrict__ w, const float* __restrict__ rstd,
