@@ -22,18 +22,27 @@ from .ops import (sl_embedding_fwd, sl_embedding_wgrad_accum, sl_linear_dgrad, s
 # leave a weight's gradient in main_grad and return none, so a captured backward pass meets the accumulator's stream only at its
 # end, where the engine joins that stream to the capture: if it is not the capture's, that ends the process.  So the functions
 # note the stream on the accumulators that they meet, and refuse what a capture would do beside one noted on another: the
-# linear functions their backward pass, the others the forward pass already, with the other leaves that they meet.  What they
-# cannot know: an accumulator that other operators made, of a graph in which none of these functions has met the leaf, or
+# linear functions a backward pass that comes to their weight's accumulator (torch.autograd.grad does not), the others the
+# forward pass already, with the other leaves that they meet.  What they cannot know: an accumulator that other operators made, of a graph in which none of these functions has met the leaf, or
 # on another stream than that of the first of these calls; and leaves behind an operator that comes before the call.
 
-def _refuse_foreign_accumulators(*leaves):
+def _will_run(node):
+    """Whether the backward pass under way runs an accumulator."""
+    try:
+        return torch._C._will_engine_execute_node(node)
+    except RuntimeError:                  # torch.autograd.grad was asked for the leaf: it takes what flows there itself
+        return False
+
+
+def _refuse_foreign_accumulators(*leaves, in_backward=False):
     """Raises, while a graph is captured, for a leaf whose accumulator was noted on another stream."""
     for t in leaves:
         if t is not None and t.requires_grad and t.is_leaf and t.is_cuda:
             if not torch.cuda.is_current_stream_capturing():
                 return
             stream = _raw_stream(t.device.index)
-            if torch.autograd.graph.get_gradient_edge(t).node.metadata.get("sl_stream", stream) != stream:
+            node = torch.autograd.graph.get_gradient_edge(t).node
+            if node.metadata.get("sl_stream", stream) != stream and (not in_backward or _will_run(node)):
                 raise RuntimeError("a leaf's gradient accumulator belongs to another stream than the capture's and lives, held by a graph "
                                    "that was made there (drop its results before the capture) or by a hook on the accumulator: "
                                    "a backward pass cannot be captured beside it")
@@ -61,7 +70,7 @@ class LinearWithGradAccumulation(torch.autograd.Function):
     @staticmethod
     def backward(ctx, grad_output: torch.Tensor):
         input, weight = ctx.saved_tensors
-        _refuse_foreign_accumulators(weight)
+        _refuse_foreign_accumulators(weight, in_backward=True)
         dy = grad_output.reshape(-1, grad_output.shape[-1]).contiguous()
         x2 = input.reshape(-1, input.shape[-1]).contiguous()
         dx = sl_linear_dgrad(dy, weight.detach())
@@ -128,7 +137,7 @@ class LinearMXFP4WithGradAccumulation(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, grad_output):
         weight, xc, xcs, wc, wcs = ctx.saved_tensors
-        _refuse_foreign_accumulators(weight)
+        _refuse_foreign_accumulators(weight, in_backward=True)
         dy = grad_output.reshape(-1, grad_output.shape[-1]).contiguous()
         need_x, need_w = ctx.needs_input_grad[:2]
         dr, drs, dc, dcs = sl_mxfp4_quantize(dy, rows=need_x, cols=need_w, seed=ctx.seed)

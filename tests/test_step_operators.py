@@ -314,22 +314,23 @@ def _linear_calls(g):
 @pytest.mark.gpu
 @pytest.mark.parametrize("name", ["linear", "mxfp4"])
 def test_captured_linear_gradients(name):
-    """The linear functions leave a weight's gradient in main_grad as the others do: a captured backward pass beside a living eager graph of
-    the same weight is refused, a captured forward pass is not; without such a graph the captured gradients are the eager ones."""
+    """The linear functions leave a weight's gradient in main_grad as the others do: a captured backward pass that comes to the weight's
+    accumulator, beside a living eager graph, is refused.  A captured forward pass is not, and without such a graph the captured
+    gradients are the eager ones."""
     say(f"case captured gradients of {name}")
     buf, w, x, c, calls = _linear_calls(_gen(4))
     call = calls[name]
 
     def both():
         y = call()
-        torch.autograd.grad(y, w, c, allow_unused=True)
+        y.backward(c)
         return y.detach()
 
     eager, graph = call(), torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         y = call()
         with pytest.raises(RuntimeError, match="drop its results"):
-            torch.autograd.grad(y, w, c, allow_unused=True)
+            y.backward(c)
     y = y.detach()
     for k in range(2):
         x.copy_(_bf16(_gen(20 + k), *x.shape))
@@ -358,6 +359,34 @@ def test_captured_linear_gradients(name):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("name", ["linear", "mxfp4"])
+def test_captured_linear_gradients_of_the_input_alone(name):
+    """torch.autograd.grad for the input comes to no accumulator of the weight: it is captured beside a living eager graph of the weight."""
+    say(f"case captured input gradients of {name}")
+    buf, w, x, c, _ = _linear_calls(_gen(5))
+    call = {"linear": sl.linear_with_grad_accumulation, "mxfp4": sl.linear_mxfp4_with_grad_accumulation}[name]
+
+    def both():
+        leaf = x.detach().requires_grad_()
+        y = call(leaf, w)
+        return y.detach(), torch.autograd.grad(y, leaf, c)[0]
+
+    eager, graph = call(x, w), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = both()
+    for k in range(3):
+        x.copy_(_bf16(_gen(30 + k), *x.shape))
+        buf.zero_grad_buffer()
+        graph.replay()
+        got = buf.grad_data.clone()
+        buf.zero_grad_buffer()
+        want = both()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want)) and torch.equal(got, buf.grad_data) and got.any()
+    assert eager.requires_grad
+
+
+@pytest.mark.gpu
 @pytest.mark.filterwarnings("ignore:The CUDA Graph is empty")
 def test_capture_beside_a_graph_of_another_function():
     """The accumulator is the leaf's, whichever function met it first; one that a hook's owner holds is refused by a message that names it."""
@@ -367,7 +396,7 @@ def test_capture_beside_a_graph_of_another_function():
     w = buf.attach("table", torch.nn.Parameter(_bf16(g, 304, 256)))
     ids, x, c = torch.randint(0, 304, (64,), generator=g, device="cuda"), _bf16(g, 32, 256), _bf16(g, 32, 304)
     lookup = lambda: sl.embedding_with_grad_accumulation(ids, w)  # noqa: E731
-    product = lambda: torch.autograd.grad(sl.linear_with_grad_accumulation(x, w), w, c, allow_unused=True)  # noqa: E731
+    product = lambda: sl.linear_with_grad_accumulation(x, w).backward(c)  # noqa: E731
     for first, second in ((lookup, product), (lambda: sl.linear_with_grad_accumulation(x, w), lookup)):          # a tied table
         eager = first()
         with torch.cuda.graph(torch.cuda.CUDAGraph()):
